@@ -10,10 +10,10 @@
 #include <string.h>
 
 #include <algorithm>
-#include <mutex>
 #include <new>
 
 #include "grouped_gemm.h"
+#include "host_common.h"
 #include "moe_ragged_bf16.h"
 
 namespace mdg {
@@ -88,48 +88,6 @@ WgradWorkspace wgrad_workspace(int64_t m_rows, int64_t n, int64_t k, int32_t num
   w.partial_off = kTableBytes;
   w.total = align256(w.partial_off + (size_t)slots * (size_t)n * (size_t)k * sizeof(float));
   return w;
-}
-
-struct DeviceInfo {
-  bool ok = false;
-  bool gfx950 = false;
-  int cus = 0;
-};
-
-DeviceInfo g_dev[64];
-std::once_flag g_dev_once[64];
-
-int query_device(DeviceInfo* out, int* device) {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return MDG_EHIP;
-  *device = dev;
-  std::call_once(g_dev_once[dev], [dev]() {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return;
-    g_dev[dev].gfx950 = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    g_dev[dev].cus = prop.multiProcessorCount;
-    g_dev[dev].ok = true;
-  });
-  if (!g_dev[dev].ok) return MDG_EHIP;
-  *out = g_dev[dev];
-  return MDG_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, int64_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{lo, lo + (uintptr_t)(bytes > 0 ? bytes : 0)};
-}
-
-bool overlaps(Range a, Range b) {
-  if (a.hi == a.lo || b.hi == b.lo) return false;
-  return a.lo < b.hi && b.lo < a.hi;
 }
 
 // Shared size checks.  Sizes are kept small enough for the kernels' 32-bit
@@ -322,8 +280,6 @@ int publish(int st, const mdg_launch& l, mdg_launch** out) {
   *out = h;
   return MDG_OK;
 }
-
-mdg_status status(int st) { return static_cast<mdg_status>(st); }
 
 int kernels_of(const mdg_launch& l) {
   if (l.gemm_grid == 0) return 0;
