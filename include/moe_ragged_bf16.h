@@ -277,6 +277,94 @@ MDG_API mdg_status grouped_det_gemm_launch_info(const mdg_launch* launch, mdg_la
 /* Releases a prepared launch (NULL is ignored).  Work already enqueued is unaffected. */
 MDG_API void grouped_det_gemm_launch_free(mdg_launch* launch);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around the expert products: routing, the plan, rows in and out
+ * ---------------------------------------------------------------------------
+ * These make what the products above read (offs, packed rows) and take their
+ * outputs back to tokens.  The conventions above hold, with these additions:
+ * tokens >= 0, 1 <= experts <= 1024, 1 <= top_k <= 32, tokens * top_k at most
+ * 4,000,000; a "slot" is a (token, choice) pair, number token * top_k + choice;
+ * dtype is MDG_BF16 or MDG_FP32 and names the type of the large tensors.  Sums
+ * are in fp32 (probability sums, dot products, rows) or integers, in one fixed
+ * order, without floating-point atomics.  Outputs must not overlap inputs, the
+ * workspace or each other.
+ *
+ * moe_route_fwd: softmax top-k routing with counts and the balance loss.
+ *   logits [tokens, experts] of dtype (aligned to its element), read.
+ *   token_mask [tokens] bytes or NULL, read: a token whose byte is 0 is not routed.
+ *   An expert is available to a token that is kept and whose logit is not -inf.
+ *   idx [tokens, top_k] int32, written: the available experts with the largest
+ *     logits, largest first, ties to the lower expert (NaN counts as largest);
+ *     -1 in the slots for which no expert is left.
+ *   weight [tokens, top_k] fp32, written: normalize != 0: the softmax over the
+ *     chosen experts; else their entries in the softmax over the available
+ *     ones; 0 in slots without an expert.
+ *   counts [experts] int32, written: slots that chose the expert.
+ *   loss [1] fp32, written: E / (top_k R^2) sum_e counts_e S_e, where R is the
+ *     number of tokens with an available expert and S_e the sum over tokens of
+ *     the expert's softmax probability; 0 when R == 0.
+ *   balance [experts] fp32, written: E counts_e / (top_k R^2), the derivative
+ *     of loss by S_e (counts are constants), for moe_route_bwd.
+ *   workspace: at least moe_route_fwd_workspace_bytes() bytes (may be 0, then
+ *     NULL will do), 256-byte aligned, contents on entry ignored.
+ *   top_k <= experts.  tokens == 0 writes counts, loss and balance (zeros).
+ * A NaN or +inf logit makes its row's weights, and with them loss, NaN.
+ */
+MDG_API size_t moe_route_fwd_workspace_bytes(int64_t tokens, int32_t experts);
+MDG_API mdg_status moe_route_fwd(const void* logits, int dtype, const uint8_t* token_mask, float* weight,
+                                 int32_t* idx, int32_t* counts, float* loss, float* balance, int64_t tokens,
+                                 int32_t experts, int32_t top_k, int normalize, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * moe_route_bwd: the gradient of moe_route_fwd's weight and loss by the logits.
+ *   logits, weight, idx, balance, normalize: as moe_route_fwd took and left them, read.
+ *   dweight [tokens, top_k] fp32 or NULL (zeros); dloss [1] fp32 on the device or NULL (zero), read.
+ *   dlogits [tokens, experts] of dtype, written (zeros for a token whose first slot has no expert).
+ * tokens == 0 enqueues nothing.
+ */
+MDG_API mdg_status moe_route_bwd(const void* logits, int dtype, const float* weight, const int32_t* idx,
+                                 const float* balance, const float* dweight, const float* dloss, void* dlogits,
+                                 int64_t tokens, int32_t experts, int32_t top_k, int normalize, void* stream);
+
+/*
+ * moe_plan: where each slot's row goes, the rows sorted by expert and, within
+ * an expert, by slot.
+ *   idx [tokens, top_k] int32, read (an entry outside [0, experts) has no row).
+ *   offs [experts] int32, written: cumulative end offsets, as the grouped products read them.
+ *   dest [tokens, top_k] int32, written: the slot's row, -1 for a slot without one.
+ *   workspace: at least moe_plan_workspace_bytes() bytes (may be 0), 256-byte aligned.
+ */
+MDG_API size_t moe_plan_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);
+MDG_API mdg_status moe_plan(const int32_t* idx, int32_t* offs, int32_t* dest, int64_t tokens, int32_t top_k,
+                            int32_t experts, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows by a plan.  A row has `hidden` elements of dtype, whole 16-byte pieces
+ * (hidden * element size a multiple of 16, hidden <= 2^20); packed rows are
+ * [tokens * top_k, hidden].  A dest outside [0, tokens * top_k) is a slot
+ * without a row.  tokens == 0 enqueues nothing.
+ *
+ *   moe_dispatch_fwd  rows[dest[t, j]] = x[t]; rows from offs[experts - 1] on: zeros
+ *   moe_dispatch_bwd  dx[t] = sum_j drows[dest[t, j]]
+ *   moe_combine_fwd   out[t] = sum_j weight[t, j] y[dest[t, j]]
+ *   moe_combine_bwd   dy[dest[t, j]] = weight[t, j] dout[t]; rows from offs[experts - 1] on: zeros;
+ *                     dweight[t, j] = <dout[t], y[dest[t, j]]> (0 for a slot without a row)
+ *
+ * Sums over j run in fp32 in the order of j and are rounded to dtype once.
+ */
+MDG_API mdg_status moe_dispatch_fwd(const void* x, const int32_t* dest, const int32_t* offs, void* rows,
+                                    int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden, int dtype,
+                                    void* stream);
+MDG_API mdg_status moe_dispatch_bwd(const void* drows, const int32_t* dest, void* dx, int64_t tokens, int32_t top_k,
+                                    int64_t hidden, int dtype, void* stream);
+MDG_API mdg_status moe_combine_fwd(const void* y, const float* weight, const int32_t* dest, void* out, int64_t tokens,
+                                   int32_t top_k, int64_t hidden, int dtype, void* stream);
+MDG_API mdg_status moe_combine_bwd(const void* dout, const void* y, const float* weight, const int32_t* dest,
+                                   const int32_t* offs, void* dy, float* dweight, int64_t tokens, int32_t top_k,
+                                   int32_t experts, int64_t hidden, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,3 +26,17 @@ from .launch import (  # noqa: F401
     prepare_grouped_det_gemm_dgrad,
     prepare_grouped_det_gemm_wgrad,
 )
+from .moe import (  # noqa: F401
+    MoePlan,
+    MoeRoute,
+    moe_combine,
+    moe_combine_bwd,
+    moe_combine_fwd,
+    moe_dispatch,
+    moe_dispatch_bwd,
+    moe_dispatch_fwd,
+    moe_plan,
+    moe_route,
+    moe_route_bwd,
+    moe_route_fwd,
+)

@@ -33,6 +33,15 @@ EXPORTED = (
     "grouped_det_gemm_launch",
     "grouped_det_gemm_launch_info",
     "grouped_det_gemm_launch_free",
+    "moe_route_fwd",
+    "moe_route_fwd_workspace_bytes",
+    "moe_route_bwd",
+    "moe_plan",
+    "moe_plan_workspace_bytes",
+    "moe_dispatch_fwd",
+    "moe_dispatch_bwd",
+    "moe_combine_fwd",
+    "moe_combine_bwd",
 )
 
 
@@ -107,6 +116,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.grouped_det_gemm_launch_info.argtypes = [vp, ctypes.POINTER(LaunchInfo)]
         lib.grouped_det_gemm_launch_free.restype = None
         lib.grouped_det_gemm_launch_free.argtypes = [vp]
+        st = ctypes.c_int
+        for name, res, args in (
+                ("moe_route_fwd_workspace_bytes", sz, [i64, i32]),
+                ("moe_route_fwd", st, [vp, st, vp, vp, vp, vp, vp, vp, i64, i32, i32, st, vp, sz, vp]),
+                ("moe_route_bwd", st, [vp, st, vp, vp, vp, vp, vp, vp, i64, i32, i32, st, vp]),
+                ("moe_plan_workspace_bytes", sz, [i64, i32, i32]),
+                ("moe_plan", st, [vp, vp, vp, i64, i32, i32, vp, sz, vp]),
+                ("moe_dispatch_fwd", st, [vp, vp, vp, vp, i64, i32, i32, i64, st, vp]),
+                ("moe_dispatch_bwd", st, [vp, vp, vp, i64, i32, i64, st, vp]),
+                ("moe_combine_fwd", st, [vp, vp, vp, vp, i64, i32, i64, st, vp]),
+                ("moe_combine_bwd", st, [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, st, vp])):
+            f = getattr(lib, name)
+            f.restype, f.argtypes = res, args
         _lib = lib
         return lib
 

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoe_ragged_bf16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["grouped_gemm_kernels.hip", "capi.cpp"]
+SOURCES = ["grouped_gemm_kernels.hip", "moe_kernels.hip", "capi.cpp", "capi_moe.cpp"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950",

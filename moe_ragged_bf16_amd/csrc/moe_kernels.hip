@@ -1,0 +1,761 @@
+// gfx950 (CDNA4) kernels around the expert products of a Mixture-of-Experts
+// layer: routing with counts and balance loss, the plan that sorts slots by
+// expert, rows dispatched by the plan and combined back, and the gradients.
+//
+// All sums run in fp32 (integers where they count) in one fixed order and no
+// floating-point atomics are used, so every output is bitwise reproducible.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernel_common.h"
+#include "moe.h"
+
+namespace mdg {
+namespace {
+
+// ---------------------------------------------------------------------------
+// reductions over the L lanes that share a row (L a power of two, 1..64)
+// ---------------------------------------------------------------------------
+// Steps of 1, 2, 4 and 8 lanes are DPP moves within a row of 16 lanes (quad
+// permutes, then the half-row and row mirrors: once groups of 4 (8) agree, the
+// mirror image of a lane holds the other group's value); steps of 16 and 32
+// swap rows with the gfx950 permlane swaps.  No step touches LDS.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+
+template <int STEP>
+__device__ __forceinline__ void partner(uint32_t v, uint32_t* a, uint32_t* b) {
+  if constexpr (STEP == 1) {
+    *a = v, *b = dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  } else if constexpr (STEP == 2) {
+    *a = v, *b = dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  } else if constexpr (STEP == 4) {
+    *a = v, *b = dpp<0x141>(v);  // row_half_mirror
+  } else if constexpr (STEP == 8) {
+    *a = v, *b = dpp<0x140>(v);  // row_mirror
+  } else if constexpr (STEP == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    *a = r[0], *b = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    *a = r[0], *b = r[1];
+  }
+}
+
+template <int L, int STEP = 1>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (STEP < L) {
+    uint32_t a, b;
+    partner<STEP>(v, &a, &b);
+    return group_max<L, STEP * 2>(max(a, b));
+  } else {
+    return v;
+  }
+}
+
+// (The two addends of a step are the same pair on both sides, so every lane of
+// the group ends with the same bits.)
+template <int L, int STEP = 1>
+__device__ __forceinline__ float group_sum(float v) {
+  if constexpr (STEP < L) {
+    uint32_t a, b;
+    partner<STEP>(__float_as_uint(v), &a, &b);
+    return group_sum<L, STEP * 2>(__uint_as_float(a) + __uint_as_float(b));
+  } else {
+    return v;
+  }
+}
+
+template <int L, int STEP = 1>
+__device__ __forceinline__ float group_fmax(float v) {
+  if constexpr (STEP < L) {
+    uint32_t a, b;
+    partner<STEP>(__float_as_uint(v), &a, &b);
+    return group_fmax<L, STEP * 2>(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  } else {
+    return v;
+  }
+}
+
+__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ uint16_t narrow(float f) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
+
+constexpr float kNegInf = -__builtin_inff();
+
+// V consecutive logits of a row from column c0; columns at or past `experts` read -inf.
+template <int V>
+__device__ __forceinline__ void load_logits(float (&l)[V], const void* base, int64_t row, int c0, int experts,
+                                            bool fp32, bool vec) {
+  const int64_t at = row * experts + c0;
+  if (vec) {  // a lane's V columns are all there or all not
+    if (c0 >= experts) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) l[v] = kNegInf;
+    } else if (fp32) {
+      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const f32x4 x = q[i];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) l[4 * i + c] = x[c];
+      }
+    } else {
+      const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at);
+#pragma unroll
+      for (int i = 0; i < V / 8; ++i) {
+        const u32x4 x = q[i];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          l[8 * i + 2 * c] = __uint_as_float(x[c] << 16);
+          l[8 * i + 2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      l[v] = kNegInf;
+      if (c0 + v < experts)
+        l[v] = fp32 ? static_cast<const float*>(base)[at + v] : widen(static_cast<const uint16_t*>(base)[at + v]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// routing
+// ---------------------------------------------------------------------------
+// An order-preserving integer of a logit: -0 and +0 are equal, NaN is above
+// everything.  kKeyNone is -inf's (an expert that cannot be chosen); 0 is below
+// every key (a chosen expert, a column past the last).
+constexpr uint32_t kKeyNone = 0x007fffffu;
+
+__device__ __forceinline__ uint32_t key_of(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  if (f != f) return 0xffffffffu;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+
+// The balance loss from the sums of one expert: a = E c / (k Tr^2) is the
+// derivative of the loss by the expert's probability sum, a * sum its share.
+__device__ __forceinline__ double balance_of(const RouteParams& p, int count, int routed) {
+  return routed > 0 ? (double)p.experts * count / ((double)p.top_k * routed * routed) : 0.0;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// L lanes hold a row, V consecutive logits each.  The top-k is k rounds of the
+// largest key left: the lane's own largest, then over the group, ties to the
+// lowest lane and there to the lowest column (lanes and columns are in expert
+// order).  The first round's value is the softmax maximum.  Each lane adds the
+// probabilities of its columns over all rows of its block in registers.
+template <int L, int V>
+__global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p) {
+  constexpr int kOwn = (kRouteMaxTopK < L * V ? kRouteMaxTopK : L * V) > L
+                           ? (kRouteMaxTopK < L * V ? kRouteMaxTopK : L * V) / L
+                           : 1;  // slots j = i * L + lane-in-group a lane keeps
+  extern __shared__ uint8_t smem[];
+  const int E = p.experts, k = p.top_k;
+  const int waves = blockDim.x >> 6;
+  float* s_sum = reinterpret_cast<float*>(smem);             // [waves][E]
+  int* s_cnt = reinterpret_cast<int*>(s_sum + waves * E);    // [E]
+  int* s_routed = s_cnt + E;                                 // [1]
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int lig = lane & (L - 1), grp = tid / L;
+  for (int e = tid; e < E; e += blockDim.x) s_cnt[e] = 0;
+  if (tid == 0) *s_routed = 0;
+  __syncthreads();
+
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+  int routed = 0;
+  const int64_t row_end = min(p.tokens, (int64_t)(blockIdx.x + 1) * p.rows_per_block);
+  for (int64_t r = (int64_t)blockIdx.x * p.rows_per_block + grp; r < row_end; r += blockDim.x / L) {
+    float l[V];
+    load_logits<V>(l, p.logits, r, lig * V, E, p.fp32 != 0, p.vec != 0);
+    const bool keep = p.mask == nullptr || p.mask[r] != 0;
+    uint32_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!keep) l[v] = kNegInf;
+      key[v] = lig * V + v < E ? key_of(l[v]) : 0u;
+    }
+    uint32_t first = 0;
+    float own_l[kOwn];
+    int own_e[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      own_l[i] = 0.0f;
+      own_e[i] = -1;
+      for (int jl = 0; jl < L && i * L + jl < k; ++jl) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = max(best, key[v]);
+        const uint32_t top = group_max<L>(best);
+        if (i == 0 && jl == 0) first = top;
+        if (top <= kKeyNone) break;  // the group has nothing left to choose
+        uint64_t hit = __ballot(best == top);
+        if constexpr (L < 64) hit = (hit >> (lane & ~(L - 1))) & ((1ull << L) - 1);
+        const int winner = __ffsll((unsigned long long)hit) - 1;
+        int at = 0;  // the winner's lowest column with this key
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+          if (key[v] == top) at = v;
+        if (lig == winner) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (v == at) key[v] = 0u;
+          atomicAdd(&s_cnt[lig * V + at], 1);
+        }
+        const int e = winner * V + __shfl(at, (lane & ~(L - 1)) + winner, 64);
+        if (lig == jl) {
+          own_l[i] = value_of(top);
+          own_e[i] = e;
+        }
+      }
+    }
+    const bool live = first > kKeyNone;
+    const float big = live ? value_of(first) : 0.0f;
+    float ex[V], total = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      ex[v] = live ? expf(l[v] - big) : 0.0f;
+      if (lig * V + v < E) total += ex[v];
+    }
+    total = group_sum<L>(total);
+    float own_x[kOwn], chosen = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      own_x[i] = own_e[i] >= 0 ? expf(own_l[i] - big) : 0.0f;
+      chosen += own_x[i];
+    }
+    chosen = group_sum<L>(chosen);
+    const float by = p.normalize ? chosen : total;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int j = i * L + lig;
+      if (j < k) {
+        p.weight[r * k + j] = live ? own_x[i] / by : 0.0f;
+        p.idx[r * k + j] = own_e[i];
+      }
+    }
+    if (live) {
+      const float inv = 1.0f / total;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += ex[v] * inv;
+      if (lig == 0) ++routed;
+    }
+  }
+
+  // the block's sums: over the wave's groups, then over the waves in order
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float s = acc[v];
+    for (int d = L; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+    if (lane < L && lane * V + v < E) s_sum[w * E + lane * V + v] = s;
+  }
+  if (routed) atomicAdd(s_routed, routed);
+  __syncthreads();
+  if (gridDim.x > 1) {
+    for (int e = tid; e < E; e += blockDim.x) {
+      float s = s_sum[e];
+      for (int i = 1; i < waves; ++i) s += s_sum[i * E + e];
+      p.part_sum[(int64_t)blockIdx.x * E + e] = s;
+      p.part_cnt[(int64_t)blockIdx.x * E + e] = s_cnt[e];
+    }
+    if (tid == 0) p.part_routed[blockIdx.x] = *s_routed;
+    return;
+  }
+  // one block: finish here
+  const int tr = *s_routed;
+  double share = 0.0;
+  for (int e = tid; e < E; e += blockDim.x) {
+    float s = s_sum[e];
+    for (int i = 1; i < waves; ++i) s += s_sum[i * E + e];
+    const double a = balance_of(p, s_cnt[e], tr);
+    p.counts[e] = s_cnt[e];
+    p.balance[e] = (float)a;
+    share += a * s;
+  }
+  share = wave_sum(share);
+  __syncthreads();
+  double* s_share = reinterpret_cast<double*>(smem);
+  if (lane == 0) s_share[w] = share;
+  __syncthreads();
+  if (tid == 0) {
+    double sum = 0.0;
+    for (int i = 0; i < waves; ++i) sum += s_share[i];
+    *p.loss = (float)sum;
+  }
+}
+
+// Adds the blocks' partial sums in block order and writes counts, balance and loss.
+__global__ __launch_bounds__(kRouteThreads) void route_finish_kernel(RouteParams p) {
+  __shared__ double s_share[kRouteThreads / 64];
+  __shared__ int s_tr[kRouteThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int E = p.experts;
+  int tr = tid < p.blocks ? p.part_routed[tid] : 0;
+  tr = wave_incl_sum(tr);
+  if (lane == 63) s_tr[w] = tr;
+  __syncthreads();
+  tr = 0;
+  for (int i = 0; i < kRouteThreads / 64; ++i) tr += s_tr[i];
+  double share = 0.0;
+  for (int e = tid; e < E; e += kRouteThreads) {
+    float s = 0.0f;
+    int c = 0;
+    for (int b = 0; b < p.blocks; ++b) {
+      s += p.part_sum[(int64_t)b * E + e];
+      c += p.part_cnt[(int64_t)b * E + e];
+    }
+    const double a = balance_of(p, c, tr);
+    p.counts[e] = c;
+    p.balance[e] = (float)a;
+    share += a * s;
+  }
+  share = wave_sum(share);
+  if (lane == 0) s_share[w] = share;
+  __syncthreads();
+  if (tid == 0) {
+    double sum = 0.0;
+    for (int i = 0; i < kRouteThreads / 64; ++i) sum += s_share[i];
+    *p.loss = (float)sum;
+  }
+}
+
+// d logits of a row, with p its softmax, w its weights, a = balance, g = dloss:
+//   D = g sum_e p a (+ sum_j w dw without normalisation)
+//   dl_e = p_e (g a_e - D) + [e chosen in slot j] (w_j (dw_j - sum_j w dw) with
+//   normalisation, else w_j dw_j).
+// The softmax is computed anew from the logits (cheaper than reading it back).
+template <int L, int V>
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdParams p) {
+  const int E = p.experts, k = p.top_k;
+  const int lane = threadIdx.x & 63, lig = lane & (L - 1);
+  const int64_t r = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (r >= p.tokens) return;
+  float l[V], dl[V];
+  load_logits<V>(l, p.logits, r, lig * V, E, p.fp32 != 0, p.vec != 0);
+  const int32_t* idx = p.idx + r * k;
+  const bool live = idx[0] >= 0;
+  float big = kNegInf, total = 0.0f, pa = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) big = fmaxf(big, l[v]);
+  big = group_fmax<L>(big);
+  const float g = p.dloss ? *p.dloss : 0.0f;
+  float a[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = lig * V + v;
+    a[v] = e < E ? p.balance[e] * g : 0.0f;
+    l[v] = e < E ? expf(l[v] - big) : 0.0f;
+    total += l[v];
+    pa += l[v] * a[v];
+  }
+  total = group_sum<L>(total);
+  pa = group_sum<L>(pa);
+  const float inv = 1.0f / total;
+  float inner = 0.0f;
+  if (p.dweight)
+    for (int j = 0; j < k; ++j)
+      if (idx[j] >= 0) inner += p.weight[r * k + j] * p.dweight[r * k + j];
+  const float d = pa * inv + (p.normalize ? 0.0f : inner);
+#pragma unroll
+  for (int v = 0; v < V; ++v) dl[v] = l[v] * inv * (a[v] - d);
+  if (p.dweight)
+    for (int j = 0; j < k; ++j) {
+      const float add = p.weight[r * k + j] * (p.dweight[r * k + j] - (p.normalize ? inner : 0.0f));
+      const int at = idx[j] - lig * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (at == v) dl[v] += add;
+    }
+#pragma unroll
+  for (int v = 0; v < V; ++v) dl[v] = live ? dl[v] : 0.0f;
+  const int64_t at = r * E + lig * V;
+  if (p.vec) {
+    if (lig * V >= E) return;
+    if (p.fp32) {
+      f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p.dlogits) + at);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) q[i] = f32x4{dl[4 * i], dl[4 * i + 1], dl[4 * i + 2], dl[4 * i + 3]};
+    } else {
+      u32x4* q = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.dlogits) + at);
+#pragma unroll
+      for (int i = 0; i < V / 8; ++i) {
+        u32x4 x;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = pack_bf16x2(dl[8 * i + 2 * c], dl[8 * i + 2 * c + 1]);
+        q[i] = x;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lig * V + v < E) {
+        if (p.fp32) static_cast<float*>(p.dlogits)[at + v] = dl[v];
+        else static_cast<uint16_t*>(p.dlogits)[at + v] = narrow(dl[v]);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the plan: a stable counting sort of the slots by expert
+// ---------------------------------------------------------------------------
+// Slots (t, j) in order t * top_k + j.  A block sorts p.chunk consecutive
+// slots, each wave a run of consecutive ones: a slot's row is offs of its
+// expert + the expert's slots in earlier blocks + in earlier waves + earlier in
+// its wave's run (lanes that hold the same expert, found with ballots over the
+// bits of the expert number).
+__device__ __forceinline__ int slot_expert(const PlanParams& p, int64_t s, int64_t end) {
+  if (s >= end) return -1;
+  const int e = p.idx[s];
+  return (unsigned)e < (unsigned)p.experts ? e : -1;
+}
+
+// Orders the LDS accesses of one wave's lanes (the hardware runs them in order;
+// this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Adds the experts of slots [begin, end), taken by one wave, to hist.
+__device__ __forceinline__ void plan_count(const PlanParams& p, int* hist, int64_t begin, int64_t end) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t s = begin; s < end; s += 64) {
+    const int e = slot_expert(p, s + lane, end);
+    if (e >= 0) atomicAdd(&hist[e], 1);
+  }
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanParams p) {
+  extern __shared__ int s_plan[];  // [E]
+  const int tid = threadIdx.x;
+  for (int e = tid; e < p.experts; e += kPlanThreads) s_plan[e] = 0;
+  __syncthreads();
+  const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(p.slots, begin + p.chunk);
+  for (int64_t s = begin + tid; s < end; s += kPlanThreads) {
+    const int e = slot_expert(p, s, end);
+    if (e >= 0) atomicAdd(&s_plan[e], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < p.experts; e += kPlanThreads) p.hist[(int64_t)blockIdx.x * p.experts + e] = s_plan[e];
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_rank_kernel(PlanParams p) {
+  extern __shared__ int s_plan[];  // [runs][E] next row of each wave's slots by expert
+  __shared__ int s_scan[kPlanThreads / 64];
+  const int runs = p.runs;  // the first `runs` waves take slots
+  const int E = p.experts, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  for (int i = tid; i < runs * E; i += kPlanThreads) s_plan[i] = 0;
+  __syncthreads();
+  const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(p.slots, begin + p.chunk);
+  const int64_t run = ((end - begin + runs - 1) / runs + 63) / 64 * 64;
+  const int64_t wb = min(end, begin + w * run), we = min(end, wb + run);
+  if (w < runs) plan_count(p, s_plan + w * E, wb, we);
+  __syncthreads();
+  // thread e (E <= kPlanThreads): the expert's slots in all blocks and in the blocks before
+  int all = 0, before = 0;
+  if (tid < E) {
+    if (gridDim.x > 1) {
+      for (int b = 0; b < p.blocks; ++b) {
+        const int c = p.hist[(int64_t)b * E + tid];
+        all += c;
+        if (b < (int)blockIdx.x) before += c;
+      }
+    } else {
+      for (int i = 0; i < runs; ++i) all += s_plan[i * E + tid];
+    }
+  }
+  const int incl = wave_incl_sum(all);
+  if (lane == 63) s_scan[w] = incl;
+  __syncthreads();
+  int start = incl - all;
+  for (int i = 0; i < w; ++i) start += s_scan[i];
+  if (tid < E) {
+    if (blockIdx.x == 0) p.offs[tid] = start + all;
+    int at = start + before;
+    for (int i = 0; i < runs; ++i) {
+      const int c = s_plan[i * E + tid];
+      s_plan[i * E + tid] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  if (w >= runs) return;
+  int* next = s_plan + w * E;
+  for (int64_t s = wb; s < we; s += 64) {
+    const int e = slot_expert(p, s + lane, we);
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; (E - 1) >> b; ++b) {
+      const uint64_t one = __ballot((e >> b) & 1);
+      same &= ((e >> b) & 1) ? one : ~one;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const int base = e >= 0 ? next[e] : 0;
+    if (s + lane < we) p.dest[s + lane] = e >= 0 ? base + rank : -1;
+    wave_lds_order();
+    if (e >= 0 && rank == 0) next[e] = base + __popcll(same);
+    wave_lds_order();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows by the plan
+// ---------------------------------------------------------------------------
+// A team of TEAM threads (64 or 256) takes one token and walks its row in
+// 16-byte pieces.  Bytes bound all of these: each row is read once and written
+// once, wherever the plan puts it.
+
+// Rows from offs[E-1] on belong to no slot: zeros, shared out over the blocks.
+__device__ __forceinline__ void zero_rest(const RowsParams& p) {
+  const int64_t first = min(max((int64_t)p.offs[p.experts - 1], (int64_t)0), p.slots);
+  u32x4* out = static_cast<u32x4*>(p.out);
+  const u32x4 z = {0u, 0u, 0u, 0u};
+  for (int64_t r = first + blockIdx.x; r < p.slots; r += gridDim.x)
+    for (int c = threadIdx.x; c < p.pieces; c += blockDim.x) out[r * p.pieces + c] = z;
+}
+
+template <int TEAM>
+__device__ __forceinline__ int64_t team_token() {
+  const int t = (int)blockIdx.x * (256 / TEAM) + (TEAM == 256 ? 0 : uniform(threadIdx.x >> 6));
+  return t;
+}
+
+// The row slot (t, j) has, or -1 (also for a dest that lies outside the rows).
+__device__ __forceinline__ int slot_row(const RowsParams& p, int64_t t, int j) {
+  const int d = p.dest[t * p.top_k + j];
+  return (unsigned)d < (unsigned)p.slots ? d : -1;
+}
+
+template <int TEAM>
+__global__ __launch_bounds__(256) void dispatch_kernel(RowsParams p) {
+  const int64_t t = team_token<TEAM>();
+  const u32x4* in = static_cast<const u32x4*>(p.in);
+  u32x4* out = static_cast<u32x4*>(p.out);
+  if (t < p.tokens)
+    for (int c = threadIdx.x & (TEAM - 1); c < p.pieces; c += TEAM) {
+      const u32x4 v = in[t * p.pieces + c];
+      for (int j = 0; j < p.top_k; ++j) {
+        const int d = slot_row(p, t, j);
+        if (d >= 0) out[(int64_t)d * p.pieces + c] = v;
+      }
+    }
+  zero_rest(p);
+}
+
+// 16 bytes as fp32 values and back.
+template <bool FP32>
+struct Piece {
+  static constexpr int kN = FP32 ? 4 : 8;
+  static __device__ __forceinline__ void get(float (&f)[kN], const u32x4& x) {
+    if constexpr (FP32) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) f[c] = __uint_as_float(x[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f[2 * c] = __uint_as_float(x[c] << 16);
+        f[2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u);
+      }
+    }
+  }
+  static __device__ __forceinline__ u32x4 put(const float (&f)[kN]) {
+    u32x4 x;
+    if constexpr (FP32) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = __float_as_uint(f[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = pack_bf16x2(f[2 * c], f[2 * c + 1]);
+    }
+    return x;
+  }
+};
+
+// out[t] = sum_j w[t, j] in[dest[t, j]], in fp32 in the order of j, rounded once.
+template <int TEAM, bool FP32>
+__global__ __launch_bounds__(256) void gather_sum_kernel(RowsParams p) {
+  using Pc = Piece<FP32>;
+  const int64_t t = team_token<TEAM>();
+  if (t >= p.tokens) return;
+  const u32x4* in = static_cast<const u32x4*>(p.in);
+  for (int c = threadIdx.x & (TEAM - 1); c < p.pieces; c += TEAM) {
+    float acc[Pc::kN];
+#pragma unroll
+    for (int i = 0; i < Pc::kN; ++i) acc[i] = 0.0f;
+    for (int j = 0; j < p.top_k; ++j) {
+      const int d = slot_row(p, t, j);
+      if (d < 0) continue;
+      const float w = p.weight ? p.weight[t * p.top_k + j] : 1.0f;
+      float f[Pc::kN];
+      Pc::get(f, in[(int64_t)d * p.pieces + c]);
+#pragma unroll
+      for (int i = 0; i < Pc::kN; ++i) acc[i] = __builtin_fmaf(w, f[i], acc[i]);
+    }
+    static_cast<u32x4*>(p.out)[t * p.pieces + c] = Pc::put(acc);
+  }
+}
+
+// dy[dest[t, j]] = w[t, j] dout[t]; dw[t, j] = <dout[t], y[dest[t, j]]>.
+template <int TEAM, bool FP32>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(RowsParams p) {
+  using Pc = Piece<FP32>;
+  constexpr int kSlots = 8;  // slots whose dot products are summed in one walk of the row
+  __shared__ float s_dot[4][kSlots];
+  const int64_t t = team_token<TEAM>();
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const u32x4* y = static_cast<const u32x4*>(p.in);
+  const u32x4* dout = static_cast<const u32x4*>(p.dout);
+  u32x4* dy = static_cast<u32x4*>(p.out);
+  for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {
+    float dot[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) dot[j] = 0.0f;
+    if (t < p.tokens)
+      for (int c = threadIdx.x & (TEAM - 1); c < p.pieces; c += TEAM) {
+        float g[Pc::kN];
+        Pc::get(g, dout[t * p.pieces + c]);
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          if (j0 + j >= p.top_k) break;
+          const int d = slot_row(p, t, j0 + j);
+          if (d < 0) continue;
+          const float wt = p.weight[t * p.top_k + j0 + j];
+          float f[Pc::kN], h[Pc::kN];
+          Pc::get(f, y[(int64_t)d * p.pieces + c]);
+#pragma unroll
+          for (int i = 0; i < Pc::kN; ++i) {
+            dot[j] = __builtin_fmaf(g[i], f[i], dot[j]);
+            h[i] = wt * g[i];
+          }
+          dy[(int64_t)d * p.pieces + c] = Pc::put(h);
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) dot[j] = group_sum<64>(dot[j]);
+    if constexpr (TEAM == 64) {
+      if (lane == 0 && t < p.tokens)
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+          if (j0 + j < p.top_k) p.dweight[t * p.top_k + j0 + j] = dot[j];
+    } else {
+      if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) s_dot[w][j] = dot[j];
+      __syncthreads();
+      if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < p.top_k && t < p.tokens) {
+        const int j = threadIdx.x;
+        p.dweight[t * p.top_k + j0 + j] = ((s_dot[0][j] + s_dot[1][j]) + s_dot[2][j]) + s_dot[3][j];
+      }
+      __syncthreads();
+    }
+  }
+  zero_rest(p);
+}
+
+// A row of at least 4 KiB gives each of 256 threads a piece; a shorter one goes
+// to a wave, four tokens to a block.
+bool wide_team(const RowsParams& p) { return p.pieces >= 256; }
+
+}  // namespace
+
+hipError_t launch_route_fwd(const RouteParams& p, int threads, hipStream_t s) {
+  const size_t waves = threads / 64;
+  const size_t sums = (waves * p.experts + p.experts + 4) * 4, shares = waves * 8;
+  const size_t lds = sums > shares ? sums : shares;
+  const dim3 g(p.blocks), b(threads);
+#define MDG_ROUTE(L, V) hipLaunchKernelGGL((route_fwd_kernel<L, V>), g, b, lds, s, p)
+  if (route_values(p.experts) == 16) {
+    MDG_ROUTE(64, 16);
+  } else {
+    switch (route_lanes(p.experts)) {
+      case 1: MDG_ROUTE(1, 8); break;
+      case 2: MDG_ROUTE(2, 8); break;
+      case 4: MDG_ROUTE(4, 8); break;
+      case 8: MDG_ROUTE(8, 8); break;
+      case 16: MDG_ROUTE(16, 8); break;
+      case 32: MDG_ROUTE(32, 8); break;
+      default: MDG_ROUTE(64, 8); break;
+    }
+  }
+#undef MDG_ROUTE
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.blocks == 1) return err;
+  hipLaunchKernelGGL(route_finish_kernel, dim3(1), dim3(kRouteThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_bwd(const RouteBwdParams& p, hipStream_t s) {
+  const int rows = 256 / route_lanes(p.experts);
+  const dim3 g((unsigned)((p.tokens + rows - 1) / rows)), b(256);
+#define MDG_ROUTE(L, V) hipLaunchKernelGGL((route_bwd_kernel<L, V>), g, b, 0, s, p)
+  if (route_values(p.experts) == 16) {
+    MDG_ROUTE(64, 16);
+  } else {
+    switch (route_lanes(p.experts)) {
+      case 1: MDG_ROUTE(1, 8); break;
+      case 2: MDG_ROUTE(2, 8); break;
+      case 4: MDG_ROUTE(4, 8); break;
+      case 8: MDG_ROUTE(8, 8); break;
+      case 16: MDG_ROUTE(16, 8); break;
+      case 32: MDG_ROUTE(32, 8); break;
+      default: MDG_ROUTE(64, 8); break;
+    }
+  }
+#undef MDG_ROUTE
+  return hipGetLastError();
+}
+
+hipError_t launch_plan(const PlanParams& p, hipStream_t s) {
+  if (p.blocks > 1) {
+    hipLaunchKernelGGL(plan_count_kernel, dim3(p.blocks), dim3(kPlanThreads), (size_t)p.experts * 4, s, p);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL(plan_rank_kernel, dim3(p.blocks), dim3(kPlanThreads),
+                     (size_t)p.experts * 4 * p.runs, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const RowsParams& p, hipStream_t s) {
+  if (wide_team(p)) hipLaunchKernelGGL((dispatch_kernel<256>), dim3((unsigned)p.tokens), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((dispatch_kernel<64>), dim3((unsigned)((p.tokens + 3) / 4)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_gather_sum(const RowsParams& p, hipStream_t s) {
+  const bool wide = wide_team(p);
+  const dim3 g((unsigned)(wide ? p.tokens : (p.tokens + 3) / 4)), b(256);
+  if (wide && p.fp32) hipLaunchKernelGGL((gather_sum_kernel<256, true>), g, b, 0, s, p);
+  else if (wide) hipLaunchKernelGGL((gather_sum_kernel<256, false>), g, b, 0, s, p);
+  else if (p.fp32) hipLaunchKernelGGL((gather_sum_kernel<64, true>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((gather_sum_kernel<64, false>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const RowsParams& p, hipStream_t s) {
+  const bool wide = wide_team(p);
+  const dim3 g((unsigned)(wide ? p.tokens : (p.tokens + 3) / 4)), b(256);
+  if (wide && p.fp32) hipLaunchKernelGGL((combine_bwd_kernel<256, true>), g, b, 0, s, p);
+  else if (wide) hipLaunchKernelGGL((combine_bwd_kernel<256, false>), g, b, 0, s, p);
+  else if (p.fp32) hipLaunchKernelGGL((combine_bwd_kernel<64, true>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((combine_bwd_kernel<64, false>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace mdg
