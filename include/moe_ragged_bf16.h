@@ -84,7 +84,8 @@ typedef enum {
   MDG_ENOMEM = 6         /* host memory for a prepared launch could not be allocated */
 } mdg_status;
 
-typedef enum { MDG_BF16 = 0, MDG_FP32 = 1 } mdg_dtype;
+/* MDG_E4M3: 8-bit floating point (4 exponent and 3 mantissa bits, no infinities), taken where it is named. */
+typedef enum { MDG_BF16 = 0, MDG_FP32 = 1, MDG_E4M3 = 2 } mdg_dtype;
 
 /* Version of this ABI (MDG_ABI_VERSION of the header the library was built with). */
 MDG_API int grouped_det_gemm_abi_version(void);
@@ -364,6 +365,54 @@ MDG_API mdg_status moe_combine_fwd(const void* y, const float* weight, const int
 MDG_API mdg_status moe_combine_bwd(const void* dout, const void* y, const float* weight, const int32_t* dest,
                                    const int32_t* offs, void* dy, float* dweight, int64_t tokens, int32_t top_k,
                                    int32_t experts, int64_t hidden, int dtype, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The grouped product in 8 bits
+ * ---------------------------------------------------------------------------
+ * Values are e4m3 with one scale for each block of 128: of a row of x, 128
+ * consecutive values along k; of a weight, 128 x 128 values.  A scale is a power
+ * of two 2^(code - 127), one byte (e8m0; 255 is NaN): the smallest with which
+ * the block's largest magnitude is at most 448, e4m3's largest value, and not
+ * below 2^-127; a value is rounded once, q = RNE(x / scale).  A block that holds
+ * a NaN or an infinity has scale NaN and q NaN throughout.  Blocks at the end
+ * of a row (k not a multiple of 128) hold what there is.
+ *
+ * Sizes: m_rows as above; n % 8 == 0 (n % 16 == 0 for a transposed weight);
+ * k % 16 == 0; n, k <= 2^20, n * k < 2^31.
+ *
+ * grouped_fp8_quantize_rows: x [m_rows, k] of dtype (MDG_BF16 or MDG_FP32), read.
+ *   q [m_rows, k], written.  scale, written: 32-bit words of four consecutive
+ *   blocks of a row, word [block / 4][row], 4-byte aligned, ceil(ceil(k / 128) / 4)
+ *   * m_rows words (codes past the last block are 0).
+ *   m_rows == 0 enqueues nothing.
+ * grouped_fp8_quantize_weight: w [num_groups, n, k] of dtype, read.
+ *   q [num_groups, n, k] and scale [num_groups, ceil(n / 128), ceil(k / 128)], written.
+ *   q_t [num_groups, k, n] and scale_t [num_groups, ceil(k / 128), ceil(n / 128)],
+ *   written, or both NULL: the same values and scales transposed (a 128 x 128
+ *   block transposes into one), with which the product below computes dgrad.
+ * grouped_fp8_gemm_fwd: Y[s_e:t_e] = X[s_e:t_e] @ W[e]^T with X and W the values
+ *   the 8-bit operands stand for, summed in fp32, bf16 y [m_rows, n], written
+ *   (rows of groups only).
+ *   x_dtype MDG_E4M3: x and x_scale as grouped_fp8_quantize_rows wrote them;
+ *   else x [m_rows, k] of x_dtype and x_scale NULL: quantised by the call into the
+ *   workspace.  w, w_scale: as grouped_fp8_quantize_weight wrote q and scale (or,
+ *   with n and k exchanged, q_t and scale_t: dX = G @ W[e]).
+ *   workspace: at least grouped_fp8_gemm_fwd_workspace_bytes() bytes (0 for
+ *   MDG_E4M3), 256-byte aligned.  m_rows == 0 enqueues nothing.
+ * Every output element is summed in one fixed order: bitwise reproducible.
+ */
+MDG_API mdg_status grouped_fp8_quantize_rows(const void* x, int dtype, void* q, void* scale, int64_t m_rows,
+                                             int64_t k, void* stream);
+MDG_API mdg_status grouped_fp8_quantize_weight(const void* w, int dtype, void* q, void* scale, void* q_t,
+                                               void* scale_t, int32_t num_groups, int64_t n, int64_t k,
+                                               void* stream);
+MDG_API size_t grouped_fp8_gemm_fwd_workspace_bytes(int64_t m_rows, int64_t n, int64_t k, int32_t num_groups,
+                                                    int x_dtype);
+MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* x_scale, const void* w,
+                                        const void* w_scale, const int32_t* offs, void* y, int64_t m_rows,
+                                        int64_t n, int64_t k, int32_t num_groups, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

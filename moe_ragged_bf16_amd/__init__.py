@@ -40,3 +40,13 @@ from .moe import (  # noqa: F401
     moe_route_bwd,
     moe_route_fwd,
 )
+from .fp8 import (  # noqa: F401
+    Fp8Rows,
+    Fp8Weight,
+    fp8_gemm_fwd_workspace_bytes,
+    grouped_fp8_gemm_dgrad,
+    grouped_fp8_gemm_fwd,
+    grouped_fp8_mm,
+    quantize_fp8_rows,
+    quantize_fp8_weight,
+)

@@ -13,7 +13,7 @@ from typing import Optional
 from . import build as _build
 
 MDG_OK, MDG_EINVAL, MDG_EUNSUPPORTED, MDG_EOVERLAP, MDG_EWORKSPACE, MDG_EHIP, MDG_ENOMEM = range(7)
-MDG_BF16, MDG_FP32 = 0, 1
+MDG_BF16, MDG_FP32, MDG_E4M3 = range(3)
 
 EXPORTED = (
     "grouped_det_gemm_abi_version",
@@ -42,6 +42,10 @@ EXPORTED = (
     "moe_dispatch_bwd",
     "moe_combine_fwd",
     "moe_combine_bwd",
+    "grouped_fp8_quantize_rows",
+    "grouped_fp8_quantize_weight",
+    "grouped_fp8_gemm_fwd",
+    "grouped_fp8_gemm_fwd_workspace_bytes",
 )
 
 
@@ -126,7 +130,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                 ("moe_dispatch_fwd", st, [vp, vp, vp, vp, i64, i32, i32, i64, st, vp]),
                 ("moe_dispatch_bwd", st, [vp, vp, vp, i64, i32, i64, st, vp]),
                 ("moe_combine_fwd", st, [vp, vp, vp, vp, i64, i32, i64, st, vp]),
-                ("moe_combine_bwd", st, [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, st, vp])):
+                ("moe_combine_bwd", st, [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, st, vp]),
+                ("grouped_fp8_quantize_rows", st, [vp, st, vp, vp, i64, i64, vp]),
+                ("grouped_fp8_quantize_weight", st, [vp, st, vp, vp, vp, vp, i32, i64, i64, vp]),
+                ("grouped_fp8_gemm_fwd_workspace_bytes", sz, [i64, i64, i64, i32, st]),
+                ("grouped_fp8_gemm_fwd", st, [vp, st, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, sz, vp])):
             f = getattr(lib, name)
             f.restype, f.argtypes = res, args
         _lib = lib

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoe_ragged_bf16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["grouped_gemm_kernels.hip", "moe_kernels.hip", "capi.cpp", "capi_moe.cpp"]
+SOURCES = ["grouped_gemm_kernels.hip", "moe_kernels.hip", "fp8_kernels.hip",
+           "capi.cpp", "capi_moe.cpp", "capi_fp8.cpp"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950",

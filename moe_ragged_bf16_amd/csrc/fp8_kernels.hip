@@ -1,0 +1,471 @@
+// gfx950 (CDNA4) kernels of the ragged grouped product in 8 bits: quantisation
+// to e4m3 with one power-of-two scale (e8m0) for each block of 128, and
+//   Y[s_e:t_e] = (q_x s_x)[s_e:t_e] @ ((q_w s_w)[e])^T
+// with fp32 accumulation and bf16 output.
+//
+// Scales.  Of a block with largest magnitude m the scale is the smallest 2^e with
+// m <= 448 * 2^e (448 is e4m3's largest value), e >= -127; then q = e4m3(x 2^-e),
+// rounded to nearest even.  Being a power of two costs nothing in precision (a
+// floating-point q keeps its relative precision wherever in its range it lies)
+// and makes x 2^-e exact, so q has one rounding; and the matrix instruction
+// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies by such scales itself, so the whole
+// reduction stays in its fp32 accumulators.  A block that holds a NaN or an
+// infinity gets scale NaN (code 255) and q NaN.
+// One instruction covers a reduction of 128: a block.  Its per-lane scale
+// applies to the 32 reductions that lane holds, and all four lanes of a row
+// carry the row's scale of the block.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8.h"
+#include "grouped_gemm.h"
+#include "kernel_common.h"
+#include "tile_epilogue.h"
+
+namespace mdg {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------
+// quantisation
+// ---------------------------------------------------------------------------
+// e8m0 code of a block from the bits of its largest magnitude (as an integer, NaN
+// and infinity above every number): with m = 1.f 2^x, e = x - 8 if 1.f <= 1.75,
+// else x - 7.
+__device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
+  const int x = (int)(amax >> 23);
+  if (x == 255) return 255u;
+  return (uint32_t)max(x - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+}
+
+// The factor 2^-e of a scale code (NaN for code 255).
+__device__ __forceinline__ float inverse_scale(uint32_t code) {
+  return __uint_as_float(code == 255u ? 0x7fc00000u : (254u - code) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+// 16 consecutive values at p (bf16 or fp32, 16-byte aligned).
+template <bool FP32>
+__device__ __forceinline__ void load16(float (&f)[16], const void* base, int64_t at) {
+  if constexpr (FP32) {
+    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 v = q[i];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) f[4 * i + c] = v[c];
+    }
+  } else {
+    const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x4 v = q[i];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f[8 * i + 2 * c] = __uint_as_float(v[c] << 16);
+        f[8 * i + 2 * c + 1] = __uint_as_float(v[c] & 0xffff0000u);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
+
+__device__ __forceinline__ u32x4 quantize16(const float (&f)[16], uint32_t code) {
+  const float inv = inverse_scale(code);
+  u32x4 q;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    q[c] = pack_e4m3(f[4 * c] * inv, f[4 * c + 1] * inv, f[4 * c + 2] * inv, f[4 * c + 3] * inv);
+  return q;
+}
+
+// Rows: 8 lanes take a block, 16 values each; blocks are dealt in memory order.
+template <bool FP32>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(Fp8RowsParams p) {
+  const int l8 = threadIdx.x & 7;
+  const int64_t total = p.m_rows * p.blocks;
+  for (int64_t b = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); b < total; b += (int64_t)gridDim.x * 32) {
+    const int64_t row = b / p.blocks;
+    const int kb = (int)(b - row * p.blocks);
+    const int col = kb * kFp8Block + l8 * 16;
+    float f[16];
+    uint32_t m = 0;
+    if (col < p.k) {
+      load16<FP32>(f, p.x, row * p.k + col);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = max(m, magnitude(f[i]));
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+    const uint32_t code = scale_code(m);
+    if (col < p.k) *reinterpret_cast<u32x4*>(p.q + row * p.k + col) = quantize16(f, code);
+    uint8_t* s = p.scale + ((int64_t)(kb >> 2) * p.m_rows + row) * 4;
+    if (l8 == 0) s[kb & 3] = (uint8_t)code;
+    if (kb == p.blocks - 1 && l8 > (kb & 3) && l8 < 4) s[l8] = 0;  // the last word's unused scales
+  }
+}
+
+// Weights: a workgroup takes a 128 x 128 block; thread t rows t / 8 + 32 i, 16
+// columns at 16 (t % 8).  The transposed copy is the same bytes through LDS.
+template <bool FP32, bool TRANSPOSE>
+__global__ __launch_bounds__(256) void quantize_weight_kernel(Fp8WeightParams p) {
+  __shared__ uint32_t s_max[4];
+  __shared__ __attribute__((aligned(16))) uint8_t s_q[TRANSPOSE ? 128 * 144 : 16];
+  const int t = threadIdx.x;
+  const int nb = (p.n + 127) / 128, kb = (p.k + 127) / 128;
+  const int bk = (int)(blockIdx.x % kb);
+  const int64_t rest = blockIdx.x / kb;
+  const int bn = (int)(rest % nb);
+  const int64_t e = rest / nb;
+  const int col = bk * 128 + (t & 7) * 16;
+  float f[4][16];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = bn * 128 + (t >> 3) + 32 * i;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) f[i][c] = 0.0f;
+    if (row < p.n && col < p.k) load16<FP32>(f[i], p.w, (e * p.n + row) * p.k + col);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) m = max(m, magnitude(f[i][c]));
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+  if ((t & 63) == 0) s_max[t >> 6] = m;
+  __syncthreads();
+  const uint32_t code = scale_code(max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3])));
+  if (t == 0) {
+    p.scale[(e * nb + bn) * kb + bk] = (uint8_t)code;
+    if constexpr (TRANSPOSE) p.scale_t[(e * kb + bk) * nb + bn] = (uint8_t)code;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (t >> 3) + 32 * i, row = bn * 128 + r;
+    const u32x4 q = quantize16(f[i], code);
+    if (row < p.n && col < p.k) *reinterpret_cast<u32x4*>(p.q + (e * p.n + row) * p.k + col) = q;
+    if constexpr (TRANSPOSE) *reinterpret_cast<u32x4*>(s_q + r * 144 + (t & 7) * 16) = q;
+  }
+  if constexpr (TRANSPOSE) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = (t >> 3) + 32 * i, k = bk * 128 + c, n = bn * 128 + (t & 7) * 16;
+      u32x4 q;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) v |= (uint32_t)s_q[((t & 7) * 16 + 4 * d + b) * 144 + c] << (8 * b);
+        q[d] = v;
+      }
+      if (k < p.k && n < p.n) *reinterpret_cast<u32x4*>(p.qt + (e * p.k + k) * p.n + n) = q;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the tile kernel: 256 x 256 output tiles
+// ---------------------------------------------------------------------------
+constexpr int kOperandBytes = kTileI * kFp8Block;  // one operand, one stage: 32 KiB
+constexpr int kLoads = kOperandBytes / 4 / 1024;   // DMA loads of an operand a wave makes per stage
+static_assert(kTileI == kTileJ && kLoads == 8, "a stage of an operand is 32 segments of 1 KiB, 8 for each of 4 waves");
+
+__shared__ __attribute__((aligned(1024))) uint8_t s_a0[kOperandBytes];
+__shared__ __attribute__((aligned(1024))) uint8_t s_a1[kOperandBytes];
+__shared__ __attribute__((aligned(1024))) uint8_t s_b0[kOperandBytes];
+__shared__ __attribute__((aligned(1024))) uint8_t s_b1[kOperandBytes];
+
+template <int B>
+__device__ __forceinline__ uint8_t* buf_a() {
+  if constexpr (B == 0) return s_a0;
+  else return s_a1;
+}
+template <int B>
+__device__ __forceinline__ uint8_t* buf_b() {
+  if constexpr (B == 0) return s_b0;
+  else return s_b1;
+}
+
+// acc += b^T a under the scales in byte S of sb and sa.  (The leading s_nop
+// covers the two wait states between a VALU write of a source and its use, which
+// the compiler does not see inside an asm statement; the matrix pipe is busy with
+// the previous product meanwhile.)
+template <int S>
+__device__ __forceinline__ void mfma_scaled(f32x4& c, const i32x8& b, const i32x8& a, uint32_t sb, uint32_t sa) {
+  if constexpr (S == 0)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else if constexpr (S == 1)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0]"
+                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else if constexpr (S == 2)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0]"
+                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
+                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+}
+
+// One unit: a row tile of one group times a tile of its expert's columns.
+struct Fp8Unit {
+  const uint8_t* a;  // x rows of the tile, column 0
+  const uint8_t* b;  // w[e] rows n of the tile, column 0
+  const uint8_t* sw; // scales of this wave's 128 columns, block 0
+  int row0;          // first row of the tile
+  int i_valid, j_valid, j0;
+  bool valid;
+};
+
+struct Scales {
+  uint32_t x[8];  // per row block of the wave: 4 blocks' scales of this lane's row
+  uint32_t w;     // 4 blocks' scales of the wave's columns
+};
+
+// Stage layout in LDS: 256 rows of 128 bytes, 16-byte chunk c of row r at chunk
+// c ^ (r % 8): the 8 lanes that an LDS read serves together lie in 8 rows, and
+// so in 8 different chunks (all banks once).  A lane of an operand fragment
+// holds chunks l / 16 and l / 16 + 4 of row l % 16 (both operands alike: the order
+// of the reduction inside a block is free).
+struct Fp8Pipe {
+  uint32_t off;       // DMA: byte offset of this lane's chunk in its first row
+  uint32_t chunk;     // ... its byte position within the stage
+  int fa, fb;         // LDS offset of this lane's first chunk of block 0 of its wave's A and B rows
+  int k, w, wi, wj, lane;
+
+  __device__ __forceinline__ void init(int k_) {
+    k = k_;
+    lane = threadIdx.x & 63;
+    w = uniform(threadIdx.x >> 6);
+    wi = w >> 1;
+    wj = w & 1;
+    const int row = w * 8 + (lane >> 3);
+    chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
+    off = (uint32_t)row * (uint32_t)k + chunk;
+    const int r = lane & 15, c = ((lane >> 4) ^ (r & 7)) * 16;
+    fa = (wi * 128 + r) * 128 + c;
+    fb = (wj * 128 + r) * 128 + c;
+  }
+
+  __device__ __forceinline__ static i32x8 frag(const uint8_t* buf, int at, int block) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(buf + at + block * 2048);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(buf + (at ^ 64) + block * 2048);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+
+  // The descriptor of stage kt of an operand with `rows` valid rows: loads past
+  // them (and all loads of a stage past the last) read zeros.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const uint8_t* base, int rows, int kt) const {
+    const int left = k - kt * kFp8Block;
+    const int bytes = uniform(left > 0 ? rows * k - kt * kFp8Block : 0);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base) + (left > 0 ? kt * kFp8Block : 0), 0, bytes,
+                                             0x00020000);
+  }
+  // Load q of a stage; chunks past the row's end (the last stage) read zeros.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint8_t* buf, int kt, int q) const {
+    const uint32_t left = (uint32_t)max(k - kt * kFp8Block, 0);
+    const uint32_t at = chunk < left ? off + (uint32_t)(q * 32) * (uint32_t)k : kOutOfRange;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(buf + (q * 4 + w) * 1024), 16, at, 0, 0, 0);
+  }
+  template <int B>
+  __device__ __forceinline__ void load_stage(const Fp8Unit& u, int kt) const {
+    const __amdgpu_buffer_rsrc_t ra = stage(u.a, u.i_valid, kt), rb = stage(u.b, u.j_valid, kt);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      load(ra, buf_a<B>(), kt, q);
+      load(rb, buf_b<B>(), kt, q);
+    }
+  }
+
+  // The scales of blocks 4 g .. 4 g + 3.  (Lanes of rows past the matrix and
+  // blocks past the last read zeros; their products are zeros or not stored.)
+  __device__ __forceinline__ void load_scales(Scales& s, const Fp8GemmParams& p, const Fp8Unit& u, int g) const {
+    const bool in = 4 * g < p.blocks;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint32_t*>(p.xs) + (in ? (int64_t)g * p.m_rows + u.row0 : 0), 0,
+        uniform(in ? (int)(p.m_rows - u.row0) * 4 : 0), 0x00020000);
+    const uint32_t at = (uint32_t)(wi * 128 + (lane & 15)) * 4;
+#pragma unroll
+    for (int ib = 0; ib < 8; ++ib) s.x[ib] = __builtin_amdgcn_raw_buffer_load_b32(rs, at + ib * 64, 0, 0);
+    const __amdgpu_buffer_rsrc_t rw =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(u.sw), 0, uniform(p.blocks), 0x00020000);
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rw, 4 * g + i, 0, 0) << (8 * i);
+    s.w = v;
+  }
+
+  // Stage kt = S mod 4, held in buffer S % 2, in two halves of 32 products.  On
+  // entry its B fragments are in b (the last of them still on their way from
+  // LDS), its A fragments of row blocks 0..3 in al, and the loads of stage kt + 1
+  // are in flight to the other buffer.  First half: row blocks 0..3, while the A
+  // fragments of row blocks 4..7 are read into ah.  Then wait for those and for
+  // stage kt + 1, and pass the barrier: stage kt + 1 is there for every wave and
+  // buffer S % 2 is free.  Second half: row blocks 4..7, while the loads of stage
+  // kt + 2 go out to buffer S % 2 and stage kt + 1's fragments replace al and
+  // each b that has been used for the last time.
+  template <int S>
+  __device__ __forceinline__ void step(Acc& acc, i32x8 (&al)[4], i32x8 (&ah)[4], i32x8 (&b)[8], const Scales& sc,
+                                       const Fp8Unit& u, int kt) const {
+    constexpr int B = S & 1, N = B ^ 1;
+#pragma unroll
+    for (int jb = 0; jb < 8; ++jb) {
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) mfma_scaled<S>(acc[ib][jb], b[jb], al[ib], sc.w, sc.x[ib]);
+      if (jb < 4) ah[jb] = frag(buf_a<B>(), fa, 4 + jb);
+    }
+    wait_vm_lgkm<0>();
+    lds_barrier();
+    const __amdgpu_buffer_rsrc_t ra = stage(u.a, u.i_valid, kt + 2), rb = stage(u.b, u.j_valid, kt + 2);
+#pragma unroll
+    for (int jb = 0; jb < 8; ++jb) {
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        mfma_scaled<S>(acc[4 + ib][jb], b[jb], ah[ib], sc.w, sc.x[4 + ib]);
+        if (jb < 4) {
+          const int q = 2 * jb + (ib >> 1);
+          if (ib & 1) load(rb, buf_b<B>(), kt + 2, q);
+          else load(ra, buf_a<B>(), kt + 2, q);
+        }
+      }
+      b[jb] = frag(buf_b<N>(), fb, jb);
+      if (jb < 4) al[jb] = frag(buf_a<N>(), fa, jb);
+    }
+  }
+};
+
+// Groups of 4 thread-consecutive experts: clamped ends and the prefix of units.
+__device__ __forceinline__ int fp8_group_table(const Fp8GemmParams& p, int n_j, int* s_end, int* s_uprefix,
+                                               int* scratch) {
+  const int E = p.num_groups, M = (int)p.m_rows, t = threadIdx.x;
+  int endv[4], run = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = 4 * t + q;
+    if (e < E) run = max(run, min(max(p.offs[e], 0), M));
+    endv[q] = run;
+  }
+  const int before = block_excl_max(run, scratch);
+  int units[4], sum = 0, start = before;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int end = max(before, endv[q]);
+    units[q] = 4 * t + q < E ? (end - start + kTileI - 1) / kTileI * n_j : 0;
+    if (4 * t + q < E) s_end[4 * t + q] = end;
+    sum += units[q];
+    start = end;
+  }
+  int total;
+  int at = block_excl_sum(sum, scratch, &total);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (4 * t + q < E) s_uprefix[4 * t + q] = at;
+    at += units[q];
+  }
+  if (t == 0) s_uprefix[E] = total;
+  __syncthreads();
+  return total;
+}
+
+__global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) {
+  __shared__ int s_end[kMaxGroups];
+  __shared__ int s_uprefix[kMaxGroups + 1];
+  __shared__ int s_scratch[4];
+  const int n_j = (p.n + kTileJ - 1) / kTileJ;
+  const int total = uniform(fp8_group_table(p, n_j, s_end, s_uprefix, s_scratch));
+  const int P = gridDim.x, bid = blockIdx.x;
+  const int vb = (P % 8 == 0) ? (bid % 8) * (P / 8) + bid / 8 : bid;
+  Fp8Pipe pipe;
+  pipe.init(p.k);
+  const int nk = p.blocks;
+  for (int v = vb; v < total; v += P) {
+    Fp8Unit u;
+    const int e = uniform(find_group(s_uprefix, p.num_groups, v));
+    const int gs = uniform(e == 0 ? 0 : s_end[e - 1]);
+    const int gm = uniform(s_end[e]) - gs;
+    int rt, ct;
+    panel_order(v - uniform(s_uprefix[e]), (gm + kTileI - 1) / kTileI, n_j, 4, &rt, &ct);
+    u.row0 = gs + rt * kTileI;
+    u.i_valid = min(kTileI, gm - rt * kTileI);
+    u.j0 = ct * kTileJ;
+    u.j_valid = min(kTileJ, p.n - u.j0);
+    u.a = p.x + (int64_t)u.row0 * p.k;
+    u.b = p.w + ((int64_t)e * p.n + u.j0) * p.k;
+    const int nb = (p.n + kFp8Block - 1) / kFp8Block;
+    u.sw = p.ws + ((int64_t)e * nb + min(u.j0 / kFp8Block + pipe.wj, nb - 1)) * p.blocks;
+
+    Acc acc;
+    zero(acc);
+    Scales sc, sn;
+    pipe.load_scales(sc, p, u, 0);
+    pipe.load_stage<0>(u, 0);
+    pipe.load_stage<1>(u, 1);
+    wait_vm_lgkm<2 * kLoads>();  // stage 0 has landed (stage 1's loads follow it)
+    lds_barrier();
+    i32x8 al[4], ah[4], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      b[i] = Fp8Pipe::frag(s_b0, pipe.fb, i);
+      if (i < 4) al[i] = Fp8Pipe::frag(s_a0, pipe.fa, i);
+    }
+    int kt = 0;
+    for (; kt + 4 <= nk; kt += 4) {
+      pipe.step<0>(acc, al, ah, b, sc, u, kt);
+      pipe.step<1>(acc, al, ah, b, sc, u, kt + 1);
+      pipe.load_scales(sn, p, u, (kt >> 2) + 1);
+      pipe.step<2>(acc, al, ah, b, sc, u, kt + 2);
+      pipe.step<3>(acc, al, ah, b, sc, u, kt + 3);
+      sc = sn;
+    }
+    if (kt < nk) {
+      pipe.step<0>(acc, al, ah, b, sc, u, kt);
+      if (kt + 1 < nk) pipe.step<1>(acc, al, ah, b, sc, u, kt + 1);
+      if (kt + 2 < nk) pipe.step<2>(acc, al, ah, b, sc, u, kt + 2);
+    }
+    wait_vm_lgkm<0>();
+    __syncthreads();  // every wave is done with LDS before results pass through it
+    const int ln = lane_here();
+    const OutTile ot = out_tile(p.y + (int64_t)u.row0 * p.n + u.j0, p.n, u.i_valid, u.j_valid, pipe.wi, pipe.wj, ln, 2);
+    epilogue_store<kStoreBf16>(acc, ot, s_a1 + pipe.w * 8192, ln);
+    wait_vm_lgkm<63>();
+    __syncthreads();  // ... and before the next unit's loads
+  }
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize_rows(const Fp8RowsParams& p, hipStream_t s) {
+  const int64_t blocks = (p.m_rows * p.blocks + 31) / 32;
+  const dim3 g((unsigned)(blocks < 8192 ? blocks : 8192)), b(256);
+  if (p.fp32) hipLaunchKernelGGL((quantize_rows_kernel<true>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((quantize_rows_kernel<false>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_quantize_weight(const Fp8WeightParams& p, hipStream_t s) {
+  const int64_t blocks = (int64_t)p.experts * ((p.n + 127) / 128) * ((p.k + 127) / 128);
+  const dim3 g((unsigned)blocks), b(256);
+  if (p.qt) {
+    if (p.fp32) hipLaunchKernelGGL((quantize_weight_kernel<true, true>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((quantize_weight_kernel<false, true>), g, b, 0, s, p);
+  } else {
+    if (p.fp32) hipLaunchKernelGGL((quantize_weight_kernel<true, false>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((quantize_weight_kernel<false, false>), g, b, 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_gemm(const Fp8GemmParams& p, int grid, hipStream_t s) {
+  hipLaunchKernelGGL(fp8_gemm_kernel, dim3(grid), dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace mdg

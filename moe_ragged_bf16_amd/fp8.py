@@ -1,0 +1,179 @@
+"""The grouped product in 8 bits: e4m3 operands with a power-of-two scale for
+each block of 128 (rows of x: 128 values along K; weights: 128 x 128).
+
+    w8 = quantize_fp8_weight(w)                              # once, for serving
+    y = grouped_fp8_gemm_fwd(x, w8.q, w8.scale, offs)        # bf16 rows in, bf16 rows out
+
+    y = grouped_fp8_mm(x, w, offs)                           # training: fwd and dgrad in 8 bits, wgrad in bf16
+
+The scale of a block is the smallest 2^e (e >= -127) with which its largest
+magnitude is at most 448; values are rounded once, to nearest even.  Sums run in
+fp32 in one fixed order.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional, Union
+
+import torch
+
+from . import _capi, ops
+from .moe import _CODES, _call, _need_float
+from .ops import _need, _offs_ptr, _same_device, _workspace, _written
+
+__all__ = ["Fp8Rows", "Fp8Weight", "quantize_fp8_rows", "quantize_fp8_weight", "fp8_gemm_fwd_workspace_bytes",
+           "grouped_fp8_gemm_fwd", "grouped_fp8_gemm_dgrad", "grouped_fp8_mm"]
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+class Fp8Rows(NamedTuple):
+    q: torch.Tensor                          # [M, K] float8_e4m3fn
+    scale: torch.Tensor                      # [ceil(B / 4), M, 4] float8_e8m0fnu, B = ceil(K / 128): scale of block b of
+                                             # row r at [b // 4, r, b % 4]
+
+
+class Fp8Weight(NamedTuple):
+    q: torch.Tensor                          # [E, N, K] float8_e4m3fn
+    scale: torch.Tensor                      # [E, ceil(N / 128), ceil(K / 128)] float8_e8m0fnu
+    qt: Optional[torch.Tensor] = None        # [E, K, N]: q transposed (dgrad)
+    scale_t: Optional[torch.Tensor] = None   # [E, ceil(K / 128), ceil(N / 128)]
+
+
+def quantize_fp8_rows(x: torch.Tensor) -> Fp8Rows:
+    """x [M, K] (bf16 or fp32; K a multiple of 16) in 8 bits."""
+    code = _need_float(x, "x")
+    M, K = x.shape
+    q = torch.empty((M, K), dtype=_E4M3, device=x.device)
+    scale = torch.empty((-(-_blocks(K) // 4), M, 4), dtype=_E8M0, device=x.device)
+    _call("grouped_fp8_quantize_rows", x.device, x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), M, K)
+    return Fp8Rows(q, scale)
+
+
+def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weight:
+    """w [E, N, K] (bf16 or fp32; N a multiple of 8, K of 16) in 8 bits.
+    ``transpose``: also the transposed copy that ``grouped_fp8_gemm_dgrad``
+    reads (N a multiple of 16)."""
+    if not isinstance(w, torch.Tensor) or w.dtype not in _CODES:
+        raise TypeError("w must be a bfloat16 or float32 tensor")
+    if not isinstance(transpose, bool):
+        raise TypeError("transpose must be a bool")
+    _need(w, "w", w.dtype, 3)
+    E, N, K = w.shape
+    q = torch.empty((E, N, K), dtype=_E4M3, device=w.device)
+    scale = torch.empty((E, _blocks(N), _blocks(K)), dtype=_E8M0, device=w.device)
+    qt = scale_t = None
+    if transpose:
+        qt = torch.empty((E, K, N), dtype=_E4M3, device=w.device)
+        scale_t = torch.empty((E, _blocks(K), _blocks(N)), dtype=_E8M0, device=w.device)
+    _call("grouped_fp8_quantize_weight", w.device, w.data_ptr(), _CODES[w.dtype], q.data_ptr(), scale.data_ptr(),
+          qt.data_ptr() if transpose else 0, scale_t.data_ptr() if transpose else 0, E, N, K)
+    return Fp8Weight(q, scale, qt, scale_t)
+
+
+def fp8_gemm_fwd_workspace_bytes(m_rows: int, n: int, k: int, num_groups: int, x_dtype=torch.bfloat16) -> int:
+    code = _capi.MDG_E4M3 if x_dtype == _E4M3 else _CODES[x_dtype]
+    return int(_capi.load_library().grouped_fp8_gemm_fwd_workspace_bytes(m_rows, n, k, num_groups, code))
+
+
+def grouped_fp8_gemm_fwd(x: Union[torch.Tensor, Fp8Rows], wq: torch.Tensor, w_scale: torch.Tensor,
+                         offs: torch.Tensor, out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[s_e:t_e] = X[s_e:t_e] @ W[e]^T, bf16 [M, N], with X in 8 bits (x [M, K]
+    in bf16 or fp32 is quantised by the call; ``Fp8Rows`` already is) and W what
+    wq [E, N, K] and w_scale (``quantize_fp8_weight``'s q and scale) stand for.
+    offs as in ``grouped_det_gemm_fwd``; rows past offs[E-1] of a freshly
+    allocated Y are left uninitialised.  ``workspace`` (uint8, at least
+    ``fp8_gemm_fwd_workspace_bytes()``) is allocated per call when not given."""
+    xs_ptr = 0
+    if isinstance(x, Fp8Rows):
+        _need(x.q, "x.q", _E4M3, 2)
+        q, code = x.q, _capi.MDG_E4M3
+        _need(x.scale, "x.scale", _E8M0, 3)
+        if tuple(x.scale.shape) != (-(-_blocks(q.shape[1]) // 4), q.shape[0], 4):
+            raise ValueError("x.scale does not belong to x.q")
+        _same_device(q, x.scale)
+        xs_ptr = x.scale.data_ptr()
+    else:
+        code = _need_float(x, "x")
+        q = x
+    M, K = q.shape
+    _need(wq, "wq", _E4M3, 3)
+    E, N, K2 = wq.shape
+    if K2 != K:
+        raise ValueError(f"x has K={K} but wq has K={K2}")
+    _need(w_scale, "w_scale", _E8M0, 3)
+    if tuple(w_scale.shape) != (E, _blocks(N), _blocks(K)):
+        raise ValueError(f"w_scale must have shape {(E, _blocks(N), _blocks(K))}")
+    given = out is not None
+    if given:
+        _need(out, "out", torch.bfloat16, 2)
+        if tuple(out.shape) != (M, N):
+            raise ValueError(f"out must have shape {(M, N)}")
+    else:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=q.device)
+    _same_device(q, wq, w_scale, offs, out)
+    op = _offs_ptr(offs, E)
+    need = _capi.load_library().grouped_fp8_gemm_fwd_workspace_bytes(M, N, K, E, code)
+    ws = _workspace(workspace, need, q.device)
+    _same_device(q, ws)
+    _call("grouped_fp8_gemm_fwd", q.device, q.data_ptr(), code, xs_ptr, wq.data_ptr(), w_scale.data_ptr(), op,
+          out.data_ptr(), M, N, K, E, ws.data_ptr(), ws.numel())
+    if given:
+        _written(out)
+    return out
+
+
+def grouped_fp8_gemm_dgrad(g: Union[torch.Tensor, Fp8Rows], wqt: torch.Tensor, w_scale_t: torch.Tensor,
+                           offs: torch.Tensor, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX[s_e:t_e] = G[s_e:t_e] @ W[e], bf16 [M, K], with G in 8 bits (as x in
+    ``grouped_fp8_gemm_fwd``) and W what wqt [E, K, N] and w_scale_t
+    (``quantize_fp8_weight(w, transpose=True)``'s qt and scale_t) stand for."""
+    return grouped_fp8_gemm_fwd(g, wqt, w_scale_t, offs, out, workspace)
+
+
+class _Fp8Mm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offs, w8):
+        y = grouped_fp8_gemm_fwd(x, w8.q, w8.scale, offs)
+        ops.zero_pad_rows(y, offs, w.shape[0])
+        ctx.save_for_backward(x, offs, w8.qt, w8.scale_t)
+        ctx.num_groups, ctx.w_dtype = w.shape[0], w.dtype
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, offs, qt, scale_t = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = grouped_fp8_gemm_dgrad(dy, qt, scale_t, offs)
+            ops.zero_pad_rows(dx, offs, ctx.num_groups)
+        if ctx.needs_input_grad[1]:
+            dw = ops.grouped_det_gemm_wgrad(dy, x, offs, out_dtype=ctx.w_dtype, num_groups=ctx.num_groups)
+        return dx, dw, None, None
+
+
+def grouped_fp8_mm(x: torch.Tensor, w: torch.Tensor, offs: torch.Tensor, *,
+                   w8: Optional[Fp8Weight] = None) -> torch.Tensor:
+    """Differentiable ragged grouped product in 8 bits: Y[s_e:t_e] = X[s_e:t_e] @
+    W[e]^T with X and W quantised, bf16 x [M, K] and w [E, N, K].  The gradient
+    by x is G (quantised) times the quantised W; the gradient by w is the bf16
+    wgrad of this package (from x and G unquantised), in w's type.  Rows past
+    offs[E-1] are zero.  ``w8``: ``quantize_fp8_weight(w, transpose=True)`` where
+    the caller keeps it between steps; quantised by the call otherwise.  N and K
+    are multiples of 16."""
+    _need(x, "x", torch.bfloat16, 2)
+    _need(w, "w", torch.bfloat16, 3)
+    if w8 is None:
+        w8 = quantize_fp8_weight(w.detach(), transpose=True)
+    if w8.qt is None or w8.scale_t is None:
+        raise ValueError("w8 needs its transposed copy (quantize_fp8_weight(w, transpose=True))")
+    if tuple(w8.q.shape) != tuple(w.shape):
+        raise ValueError(f"w8 has shape {tuple(w8.q.shape)}, w has {tuple(w.shape)}")
+    return _Fp8Mm.apply(x, w, offs, w8)
