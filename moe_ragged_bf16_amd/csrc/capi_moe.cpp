@@ -73,9 +73,13 @@ RouteCut route_cut(int64_t tokens, int32_t experts) {
   return c;
 }
 
+// Workspace of a cut call: shares and counter of the finishing kernel, then the
+// blocks' probability sums, counts and routed tokens.
+constexpr size_t kRouteHead = 1024 * 8 + 256;  // a share for every expert at most
+
 size_t route_workspace(int64_t tokens, int32_t experts) {
   const RouteCut c = route_cut(tokens, experts);
-  return c.blocks == 1 ? 0 : align256((size_t)c.blocks * ((size_t)experts * 8 + 4));
+  return c.blocks == 1 ? 0 : align256(kRouteHead + (size_t)c.blocks * ((size_t)experts * 8 + 4));
 }
 
 int check_rows_sizes(int64_t tokens, int32_t top_k, int32_t experts) {
@@ -176,7 +180,10 @@ MDG_API mdg_status moe_route_fwd(const void* logits, int dtype, const uint8_t* t
   p.vec = aligned16(logits) && experts % route_values(experts) == 0;
   p.blocks = cut.blocks;
   if (cut.blocks > 1) {
-    p.part_sum = static_cast<float*>(workspace);
+    char* ws = static_cast<char*>(workspace);
+    p.part_share = reinterpret_cast<double*>(ws);
+    p.part_done = reinterpret_cast<int32_t*>(ws + kRouteHead - 256);
+    p.part_sum = reinterpret_cast<float*>(ws + kRouteHead);
     p.part_cnt = reinterpret_cast<int32_t*>(p.part_sum + (size_t)cut.blocks * experts);
     p.part_routed = p.part_cnt + (size_t)cut.blocks * experts;
   }

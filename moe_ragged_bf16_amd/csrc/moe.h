@@ -26,6 +26,8 @@ struct RouteParams {
   float* part_sum;      // [blocks, experts] workspace: probability sums of a block's tokens
   int32_t* part_cnt;    // [blocks, experts]
   int32_t* part_routed; // [blocks]
+  double* part_share;   // finishing workgroups' shares of the loss
+  int32_t* part_done;   // finishing workgroups that are through
   int64_t tokens;
   int64_t rows_per_block;
   int32_t experts, top_k, normalize, fp32;

@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional, Union
 import torch
 
 from . import _capi, ops
-from .moe import _CODES, _call, _need_float
+from .moe import _CODES, _call, _check, _entry, _need_float, _scratch
 from .ops import _need, _offs_ptr, _same_device, _workspace, _written
 
 __all__ = ["Fp8Rows", "Fp8Weight", "quantize_fp8_rows", "quantize_fp8_weight", "fp8_gemm_fwd_workspace_bytes",
@@ -49,7 +49,7 @@ def quantize_fp8_rows(x: torch.Tensor) -> Fp8Rows:
     M, K = x.shape
     q = torch.empty((M, K), dtype=_E4M3, device=x.device)
     scale = torch.empty((-(-_blocks(K) // 4), M, 4), dtype=_E8M0, device=x.device)
-    _call("grouped_fp8_quantize_rows", x.device, x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), M, K)
+    _call("grouped_fp8_quantize_rows", x, x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), M, K)
     return Fp8Rows(q, scale)
 
 
@@ -69,7 +69,7 @@ def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weigh
     if transpose:
         qt = torch.empty((E, K, N), dtype=_E4M3, device=w.device)
         scale_t = torch.empty((E, _blocks(K), _blocks(N)), dtype=_E8M0, device=w.device)
-    _call("grouped_fp8_quantize_weight", w.device, w.data_ptr(), _CODES[w.dtype], q.data_ptr(), scale.data_ptr(),
+    _call("grouped_fp8_quantize_weight", w, w.data_ptr(), _CODES[w.dtype], q.data_ptr(), scale.data_ptr(),
           qt.data_ptr() if transpose else 0, scale_t.data_ptr() if transpose else 0, E, N, K)
     return Fp8Weight(q, scale, qt, scale_t)
 
@@ -90,38 +90,42 @@ def grouped_fp8_gemm_fwd(x: Union[torch.Tensor, Fp8Rows], wq: torch.Tensor, w_sc
     ``fp8_gemm_fwd_workspace_bytes()``) is allocated per call when not given."""
     xs_ptr = 0
     if isinstance(x, Fp8Rows):
-        _need(x.q, "x.q", _E4M3, 2)
+        _check(x.q, "x.q", _E4M3, 2)
         q, code = x.q, _capi.MDG_E4M3
-        _need(x.scale, "x.scale", _E8M0, 3)
+        _check(x.scale, "x.scale", _E8M0, 3, q)
         if tuple(x.scale.shape) != (-(-_blocks(q.shape[1]) // 4), q.shape[0], 4):
             raise ValueError("x.scale does not belong to x.q")
-        _same_device(q, x.scale)
         xs_ptr = x.scale.data_ptr()
     else:
         code = _need_float(x, "x")
         q = x
     M, K = q.shape
-    _need(wq, "wq", _E4M3, 3)
+    _check(wq, "wq", _E4M3, 3, q)
     E, N, K2 = wq.shape
     if K2 != K:
         raise ValueError(f"x has K={K} but wq has K={K2}")
-    _need(w_scale, "w_scale", _E8M0, 3)
+    _check(w_scale, "w_scale", _E8M0, 3, q)
     if tuple(w_scale.shape) != (E, _blocks(N), _blocks(K)):
         raise ValueError(f"w_scale must have shape {(E, _blocks(N), _blocks(K))}")
     given = out is not None
     if given:
-        _need(out, "out", torch.bfloat16, 2)
+        _check(out, "out", torch.bfloat16, 2, q)
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must have shape {(M, N)}")
     else:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=q.device)
-    _same_device(q, wq, w_scale, offs, out)
     op = _offs_ptr(offs, E)
-    need = _capi.load_library().grouped_fp8_gemm_fwd_workspace_bytes(M, N, K, E, code)
-    ws = _workspace(workspace, need, q.device)
-    _same_device(q, ws)
-    _call("grouped_fp8_gemm_fwd", q.device, q.data_ptr(), code, xs_ptr, wq.data_ptr(), w_scale.data_ptr(), op,
-          out.data_ptr(), M, N, K, E, ws.data_ptr(), ws.numel())
+    if offs.get_device() != q.get_device():
+        _same_device(q, offs)
+    need = _entry("grouped_fp8_gemm_fwd_workspace_bytes")(M, N, K, E, code)
+    if workspace is None:
+        ws, wp = _scratch(need, q.device)
+    else:
+        ws = _workspace(workspace, need, q.device)
+        _same_device(q, ws)
+        wp, need = ws.data_ptr(), ws.numel()
+    _call("grouped_fp8_gemm_fwd", q, q.data_ptr(), code, xs_ptr, wq.data_ptr(), w_scale.data_ptr(), op,
+          out.data_ptr(), M, N, K, E, wp, need)
     if given:
         _written(out)
     return out

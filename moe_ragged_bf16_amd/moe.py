@@ -40,33 +40,53 @@ class MoePlan(NamedTuple):
     dest: torch.Tensor     # [tokens, top_k] int32: the slot's row, -1: none
 
 
+def _check(t: torch.Tensor, name: str, dtype, ndim: int, like: Optional[torch.Tensor] = None) -> None:
+    """_need and _same_device at the cost of one test where all is well."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous() and \
+            (like is None or t.get_device() == like.get_device()):
+        return
+    _need(t, name, dtype, ndim)
+    _same_device(like, t)
+
+
 def _need_float(t: torch.Tensor, name: str) -> int:
-    code = _CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _CODES.get(t.dtype)
     if code is None:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    _need(t, name, t.dtype, 2)
+    _check(t, name, t.dtype, 2)
     return code
 
 
-def _call(name: str, device: torch.device, *args) -> None:
-    """Calls a library entry with the current stream of `device` as the last argument."""
-    entry = getattr(_capi.load_library(), name)
-    if device.index == torch.cuda.current_device():
-        st = entry(*args, torch.cuda.current_stream(device).cuda_stream)
+_entries = {}
+
+
+def _entry(name: str):
+    f = _entries.get(name)
+    if f is None:
+        f = _entries[name] = getattr(_capi.load_library(), name)
+    return f
+
+
+def _call(name: str, t: torch.Tensor, *args) -> None:
+    """Calls a library entry on t's device, with its current stream as the last argument."""
+    index = t.get_device()
+    if index == torch.cuda.current_device():
+        st = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = entry(*args, torch.cuda.current_stream(device).cuda_stream)
-    _capi.check(name, st)
+        with torch.cuda.device(index):
+            st = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _capi.check(name, st)
 
 
-def _scratch(need: int, device) -> Tuple[Optional[torch.Tensor], int, int]:
-    """A workspace of `need` bytes (kept alive by the caller until the launch), its address and size."""
+def _scratch(need: int, device) -> Tuple[Optional[torch.Tensor], int]:
+    """A workspace of `need` bytes (kept alive by the caller until the launch) and its address."""
     if need == 0:
-        return None, 0, 0
+        return None, 0
     t = torch.empty(need, dtype=torch.uint8, device=device)
-    return t, t.data_ptr(), need
+    return t, t.data_ptr()
 
 
 def _plain_int(v, name: str) -> int:
@@ -98,10 +118,9 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, *, normalize: bool = True,
         raise ValueError(f"top_k must be between 1 and the number of experts {E}, got {top_k}")
     mask = 0
     if token_mask is not None:
-        _need(token_mask, "token_mask", torch.bool, 1)
+        _check(token_mask, "token_mask", torch.bool, 1, logits)
         if token_mask.shape[0] != T:
             raise ValueError(f"token_mask must have {T} entries")
-        _same_device(logits, token_mask)
         mask = token_mask.data_ptr()
     dev = logits.device
     weight = torch.empty((T, top_k), dtype=torch.float32, device=dev)
@@ -109,9 +128,10 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, *, normalize: bool = True,
     counts = torch.empty(E, dtype=torch.int32, device=dev)
     loss = torch.empty((), dtype=torch.float32, device=dev)
     balance = torch.empty(E, dtype=torch.float32, device=dev)
-    ws, wp, wn = _scratch(_capi.load_library().moe_route_fwd_workspace_bytes(T, E), dev)
-    _call("moe_route_fwd", dev, logits.data_ptr(), code, mask, weight.data_ptr(), idx.data_ptr(), counts.data_ptr(),
-          loss.data_ptr(), balance.data_ptr(), T, E, top_k, int(normalize), wp, wn)
+    need = _entry("moe_route_fwd_workspace_bytes")(T, E)
+    ws, wp = _scratch(need, dev)
+    _call("moe_route_fwd", logits, logits.data_ptr(), code, mask, weight.data_ptr(), idx.data_ptr(), counts.data_ptr(),
+          loss.data_ptr(), balance.data_ptr(), T, E, top_k, normalize, wp, need)
     return MoeRoute(weight, idx, counts, loss, balance)
 
 
@@ -123,26 +143,23 @@ def moe_route_bwd(dweight: Optional[torch.Tensor], dloss: Optional[torch.Tensor]
     ``moe_route_fwd(logits, ..., normalize=normalize)`` returned."""
     code = _need_float(logits, "logits")
     T, E = logits.shape
-    _need(route.weight, "route.weight", torch.float32, 2)
-    _need(route.idx, "route.idx", torch.int32, 2)
-    _need(route.balance, "route.balance", torch.float32, 1)
+    _check(route.weight, "route.weight", torch.float32, 2, logits)
+    _check(route.idx, "route.idx", torch.int32, 2, logits)
+    _check(route.balance, "route.balance", torch.float32, 1, logits)
     k = route.idx.shape[1]
     if tuple(route.idx.shape) != (T, k) or tuple(route.weight.shape) != (T, k) or route.balance.shape[0] != E:
         raise ValueError("route does not belong to logits of this shape")
-    _same_device(logits, route.weight, route.idx, route.balance)
     dw = dl = 0
     if dweight is not None:
-        _need(dweight, "dweight", torch.float32, 2)
+        _check(dweight, "dweight", torch.float32, 2, logits)
         if tuple(dweight.shape) != (T, k):
             raise ValueError(f"dweight must have shape {(T, k)}")
-        _same_device(logits, dweight)
         dw = dweight.data_ptr()
     if dloss is not None:
-        _need(dloss, "dloss", torch.float32, 0)
-        _same_device(logits, dloss)
+        _check(dloss, "dloss", torch.float32, 0, logits)
         dl = dloss.data_ptr()
     out = torch.empty_like(logits)
-    _call("moe_route_bwd", logits.device, logits.data_ptr(), code, route.weight.data_ptr(), route.idx.data_ptr(),
+    _call("moe_route_bwd", logits, logits.data_ptr(), code, route.weight.data_ptr(), route.idx.data_ptr(),
           route.balance.data_ptr(), dw, dl, out.data_ptr(), T, E, k, int(normalize))
     return out
 
@@ -180,7 +197,7 @@ def moe_plan(idx: torch.Tensor, num_experts: int) -> MoePlan:
     keeping their order within an expert: ``offs`` [num_experts] as the grouped
     products take it and ``dest`` [tokens, top_k], each slot's row.  Entries
     outside [0, num_experts) have no row (dest -1)."""
-    _need(idx, "idx", torch.int32, 2)
+    _check(idx, "idx", torch.int32, 2)
     _plain_int(num_experts, "num_experts")
     T, k = idx.shape
     if k < 1 or num_experts < 1:
@@ -188,16 +205,18 @@ def moe_plan(idx: torch.Tensor, num_experts: int) -> MoePlan:
     dev = idx.device
     offs = torch.empty(num_experts, dtype=torch.int32, device=dev)
     dest = torch.empty((T, k), dtype=torch.int32, device=dev)
-    ws, wp, wn = _scratch(_capi.load_library().moe_plan_workspace_bytes(T, k, num_experts), dev)
-    _call("moe_plan", dev, idx.data_ptr(), offs.data_ptr(), dest.data_ptr(), T, k, num_experts, wp, wn)
+    need = _entry("moe_plan_workspace_bytes")(T, k, num_experts)
+    ws, wp = _scratch(need, dev)
+    _call("moe_plan", idx, idx.data_ptr(), offs.data_ptr(), dest.data_ptr(), T, k, num_experts, wp, need)
     return MoePlan(offs, dest)
 
 
 def _need_plan(plan: MoePlan, t: torch.Tensor) -> Tuple[int, int, int]:
-    _need(plan.offs, "plan.offs", torch.int32, 1)
-    _need(plan.dest, "plan.dest", torch.int32, 2)
-    _same_device(t, plan.offs, plan.dest)
-    return plan.dest.shape[0], plan.dest.shape[1], plan.offs.shape[0]
+    offs, dest = plan
+    _check(offs, "plan.offs", torch.int32, 1, t)
+    _check(dest, "plan.dest", torch.int32, 2, t)
+    T, k = dest.shape
+    return T, k, offs.shape[0]
 
 
 def _need_rows(t: torch.Tensor, name: str, rows: int) -> None:
@@ -213,7 +232,7 @@ def moe_dispatch_fwd(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     _need_rows(x, "x", T)
     H = x.shape[1]
     rows = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
-    _call("moe_dispatch_fwd", x.device, x.data_ptr(), plan.dest.data_ptr(), plan.offs.data_ptr(), rows.data_ptr(),
+    _call("moe_dispatch_fwd", x, x.data_ptr(), plan.dest.data_ptr(), plan.offs.data_ptr(), rows.data_ptr(),
           T, k, E, H, code)
     return rows
 
@@ -225,7 +244,7 @@ def moe_dispatch_bwd(drows: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     _need_rows(drows, "drows", T * k)
     H = drows.shape[1]
     dx = torch.empty((T, H), dtype=drows.dtype, device=drows.device)
-    _call("moe_dispatch_bwd", drows.device, drows.data_ptr(), plan.dest.data_ptr(), dx.data_ptr(), T, k, H, code)
+    _call("moe_dispatch_bwd", drows, drows.data_ptr(), plan.dest.data_ptr(), dx.data_ptr(), T, k, H, code)
     return dx
 
 
@@ -238,16 +257,15 @@ def moe_combine_fwd(y: torch.Tensor, weight: torch.Tensor, plan: MoePlan) -> tor
     _need_weight(weight, y, T, k)
     H = y.shape[1]
     out = torch.empty((T, H), dtype=y.dtype, device=y.device)
-    _call("moe_combine_fwd", y.device, y.data_ptr(), weight.data_ptr(), plan.dest.data_ptr(), out.data_ptr(), T, k, H,
+    _call("moe_combine_fwd", y, y.data_ptr(), weight.data_ptr(), plan.dest.data_ptr(), out.data_ptr(), T, k, H,
           code)
     return out
 
 
 def _need_weight(weight: torch.Tensor, like: torch.Tensor, T: int, k: int) -> None:
-    _need(weight, "weight", torch.float32, 2)
+    _check(weight, "weight", torch.float32, 2, like)
     if tuple(weight.shape) != (T, k):
         raise ValueError(f"weight must have shape {(T, k)}")
-    _same_device(like, weight)
 
 
 def moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor,
@@ -259,13 +277,12 @@ def moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor,
     _need_rows(y, "y", T * k)
     _need_weight(weight, y, T, k)
     H = y.shape[1]
-    _need(dout, "dout", y.dtype, 2)
+    _check(dout, "dout", y.dtype, 2, y)
     if tuple(dout.shape) != (T, H):
         raise ValueError(f"dout must have shape {(T, H)}")
-    _same_device(y, dout)
     dy = torch.empty_like(y)
     dweight = torch.empty((T, k), dtype=torch.float32, device=y.device)
-    _call("moe_combine_bwd", y.device, dout.data_ptr(), y.data_ptr(), weight.data_ptr(), plan.dest.data_ptr(),
+    _call("moe_combine_bwd", y, dout.data_ptr(), y.data_ptr(), weight.data_ptr(), plan.dest.data_ptr(),
           plan.offs.data_ptr(), dy.data_ptr(), dweight.data_ptr(), T, k, E, H, code)
     return dy, dweight
 
