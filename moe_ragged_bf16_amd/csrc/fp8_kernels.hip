@@ -182,6 +182,7 @@ __shared__ __attribute__((aligned(1024))) uint8_t s_a0[kOperandBytes];
 __shared__ __attribute__((aligned(1024))) uint8_t s_a1[kOperandBytes];
 __shared__ __attribute__((aligned(1024))) uint8_t s_b0[kOperandBytes];
 __shared__ __attribute__((aligned(1024))) uint8_t s_b1[kOperandBytes];
+__shared__ __attribute__((aligned(1024))) uint8_t s_out[4][4096];  // each wave's results on their way out
 
 template <int B>
 __device__ __forceinline__ uint8_t* buf_a() {
@@ -213,6 +214,9 @@ __device__ __forceinline__ void mfma_scaled(f32x4& c, const i32x8& b, const i32x
     asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
                  : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
 }
+
+// Waits until all of this wave's LDS reads have returned.
+__device__ __forceinline__ void wait_lgkm() { __builtin_amdgcn_s_waitcnt(0xC07F); }  // lgkmcnt(0), the others at their most
 
 // One unit: a row tile of one group times a tile of its expert's columns.
 struct Fp8Unit {
@@ -260,27 +264,32 @@ struct Fp8Pipe {
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 
-  // The descriptor of stage kt of an operand with `rows` valid rows: loads past
-  // them (and all loads of a stage past the last) read zeros.
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const uint8_t* base, int rows, int kt) const {
+  // One stage of an operand: from `base`, `bytes` to the end of the tile's valid
+  // rows (loads past it read zeros), `left` of them in the current row (chunks
+  // past it, in the last stage, read zeros).
+  struct Stage {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t left;
+  };
+  __device__ __forceinline__ Stage stage(const uint8_t* base, int rows, int kt) const {
     const int left = k - kt * kFp8Block;
-    const int bytes = uniform(left > 0 ? rows * k - kt * kFp8Block : 0);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base) + (left > 0 ? kt * kFp8Block : 0), 0, bytes,
-                                             0x00020000);
+    const int bytes = uniform(left > 0 && rows > 0 ? rows * k - kt * kFp8Block : 0);
+    return Stage{__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base) + (left > 0 ? kt * kFp8Block : 0), 0,
+                                                   bytes, 0x00020000),
+                 (uint32_t)max(left, 0)};
   }
-  // Load q of a stage; chunks past the row's end (the last stage) read zeros.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint8_t* buf, int kt, int q) const {
-    const uint32_t left = (uint32_t)max(k - kt * kFp8Block, 0);
-    const uint32_t at = chunk < left ? off + (uint32_t)(q * 32) * (uint32_t)k : kOutOfRange;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(buf + (q * 4 + w) * 1024), 16, at, 0, 0, 0);
+  // Load q of a stage.
+  __device__ __forceinline__ void load(const Stage& st, uint8_t* buf, int q) const {
+    const uint32_t at = chunk < st.left ? off + (uint32_t)(q * 32) * (uint32_t)k : kOutOfRange;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rs, (lds_void*)(buf + (q * 4 + w) * 1024), 16, at, 0, 0, 0);
   }
   template <int B>
   __device__ __forceinline__ void load_stage(const Fp8Unit& u, int kt) const {
-    const __amdgpu_buffer_rsrc_t ra = stage(u.a, u.i_valid, kt), rb = stage(u.b, u.j_valid, kt);
+    const Stage a = stage(u.a, u.i_valid, kt), b = stage(u.b, u.j_valid, kt);
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
-      load(ra, buf_a<B>(), kt, q);
-      load(rb, buf_b<B>(), kt, q);
+      load(a, buf_a<B>(), q);
+      load(b, buf_b<B>(), q);
     }
   }
 
@@ -303,44 +312,98 @@ struct Fp8Pipe {
     s.w = v;
   }
 
-  // Stage kt = S mod 4, held in buffer S % 2, in two halves of 32 products.  On
-  // entry its B fragments are in b (the last of them still on their way from
-  // LDS), its A fragments of row blocks 0..3 in al, and the loads of stage kt + 1
-  // are in flight to the other buffer.  First half: row blocks 0..3, while the A
-  // fragments of row blocks 4..7 are read into ah.  Then wait for those and for
-  // stage kt + 1, and pass the barrier: stage kt + 1 is there for every wave and
-  // buffer S % 2 is free.  Second half: row blocks 4..7, while the loads of stage
-  // kt + 2 go out to buffer S % 2 and stage kt + 1's fragments replace al and
-  // each b that has been used for the last time.
+  // Fragments of a unit's stage 0 (landed in buffer 0).
+  __device__ __forceinline__ void first_frags(i32x8 (&al)[4], i32x8 (&ah)[4], i32x8 (&b)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      b[i] = frag(s_b0, fb, i);
+      if (i < 4) al[i] = frag(s_a0, fa, i);
+      else ah[i - 4] = frag(s_a0, fa, i);
+    }
+  }
+
+  // Stage kt (S = kt % 4, buffer S % 2) in two halves of 32 products, row blocks
+  // 0..3 (al) and 4..7 (ah).  On entry its fragments are in registers (the last of
+  // them still on their way from LDS) and the loads of stage kt + 1 are in flight.
+  //  * After the first products: this wave's LDS reads have returned; behind the
+  //    barrier every wave's have, so buffer S % 2 is free, and the loads of stage
+  //    kt + 2 go out to it during the first half.  For a unit's last two stages
+  //    these are the next unit's stages 0 and 1 (stage S % 2), so the loads never
+  //    pause between units.
+  //  * Half way: stage kt + 1 has landed, behind the barrier in
+  //    every wave; the second half reads its fragments, each b into the registers
+  //    of the one that has been used.
+  // A stage's loads thus have 1 1/4 to 1 1/2 steps to land.
   template <int S>
-  __device__ __forceinline__ void step(Acc& acc, i32x8 (&al)[4], i32x8 (&ah)[4], i32x8 (&b)[8], const Scales& sc,
-                                       const Fp8Unit& u, int kt) const {
+  __device__ __forceinline__ void step(Acc& acc, i32x8 (&al)[4], const i32x8 (&ah)[4], i32x8 (&ahn)[4], i32x8 (&b)[8],
+                                       const Scales& sc, Scales& sn, const Fp8GemmParams& p, const Fp8Unit& u,
+                                       const Fp8Unit& nx, int kt) const {
     constexpr int B = S & 1, N = B ^ 1;
 #pragma unroll
-    for (int jb = 0; jb < 8; ++jb) {
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib) mfma_scaled<S>(acc[ib][jb], b[jb], al[ib], sc.w, sc.x[ib]);
-      if (jb < 4) ah[jb] = frag(buf_a<B>(), fa, 4 + jb);
-    }
-    wait_vm_lgkm<0>();
+    for (int ib = 0; ib < 4; ++ib) mfma_scaled<S>(acc[ib][0], b[0], al[ib], sc.w, sc.x[ib]);
+    wait_lgkm();
     lds_barrier();
-    const __amdgpu_buffer_rsrc_t ra = stage(u.a, u.i_valid, kt + 2), rb = stage(u.b, u.j_valid, kt + 2);
+    if constexpr (S == 3) load_scales(sn, p, u, (kt >> 2) + 1);
+    const bool in = kt + 2 < p.blocks;
+    const Stage sa = stage(in ? u.a : nx.a, in ? u.i_valid : nx.i_valid, in ? kt + 2 : B);
+    const Stage sb = stage(in ? u.b : nx.b, in ? u.j_valid : nx.j_valid, in ? kt + 2 : B);
+#pragma unroll
+    for (int jb = 1; jb < 8; ++jb)
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        mfma_scaled<S>(acc[ib][jb], b[jb], al[ib], sc.w, sc.x[ib]);
+        const int i = (jb - 1) * 4 + ib;
+        if (i < 16) {
+          if (i & 1) load(sb, buf_b<B>(), i >> 1);
+          else load(sa, buf_a<B>(), i >> 1);
+        }
+      }
+    // Stage kt + 1 has landed.  After it were issued this step's 16 loads and, in a
+    // unit's first step, the previous unit's 32 stores.
+    if (S == 0 && kt == 0) wait_vm_lgkm<2 * kLoads + epilogue_ops<kStoreBf16>()>();
+    else wait_vm_lgkm<2 * kLoads>();
+    lds_barrier();
 #pragma unroll
     for (int jb = 0; jb < 8; ++jb) {
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
         mfma_scaled<S>(acc[4 + ib][jb], b[jb], ah[ib], sc.w, sc.x[4 + ib]);
-        if (jb < 4) {
-          const int q = 2 * jb + (ib >> 1);
-          if (ib & 1) load(rb, buf_b<B>(), kt + 2, q);
-          else load(ra, buf_a<B>(), kt + 2, q);
-        }
+        if (ib == 1 && jb < 4) al[jb] = frag(buf_a<N>(), fa, jb);
+        if (ib == 1 && jb >= 4) ahn[jb - 4] = frag(buf_a<N>(), fa, jb);
       }
       b[jb] = frag(buf_b<N>(), fb, jb);
-      if (jb < 4) al[jb] = frag(buf_a<N>(), fa, jb);
     }
   }
 };
+
+// Writes the wave's 128 x 128 sub-tile as bf16, 16 rows at a time through 4 KiB of
+// LDS of its own (layout as in stage_slab: 256-byte rows, chunk c of row r at
+// c ^ (r % 16)), so that a store covers whole 256-byte row segments.
+__device__ __forceinline__ void store_tile(const Acc& acc, const OutTile& t, uint8_t* xb, int lane) {
+  const Staging x = staging(xb, lane, true);
+#pragma unroll
+  for (int ib = 0; ib < 8; ++ib) {
+    __builtin_amdgcn_sched_barrier(0);  // one slab at a time (bounds the registers in use)
+#pragma unroll
+    for (int jb = 0; jb < 8; ++jb) {
+      const f32x4& a = acc[ib][jb];
+      u32x2 pk;
+      pk[0] = pack_bf16x2(acc_read(a[0]), acc_read(a[1]));
+      pk[1] = pack_bf16x2(acc_read(a[2]), acc_read(a[3]));
+      *reinterpret_cast<u32x2*>(x.w + (((2 * jb) ^ x.kw) << 4)) = pk;
+    }
+    u32x4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      v[q] = *reinterpret_cast<const u32x4*>(x.r + q * 1024 + ((x.sw ^ ((4 * q + x.rl) & 15)) << 4));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = ib * 16 + q * 4;
+      __builtin_amdgcn_raw_buffer_store_b128(v[q], t.rs, r < t.rows_left ? t.base0 + (uint32_t)(r * t.ldc_b) : kOutOfRange,
+                                             0, 0);
+    }
+  }
+}
 
 // Groups of 4 thread-consecutive experts: clamped ends and the prefix of units.
 __device__ __forceinline__ int fp8_group_table(const Fp8GemmParams& p, int n_j, int* s_end, int* s_uprefix,
@@ -375,6 +438,31 @@ __device__ __forceinline__ int fp8_group_table(const Fp8GemmParams& p, int n_j, 
   return total;
 }
 
+// Unit v of the launch; one past the last has no rows and loads nothing.
+__device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& p, const int* s_end, const int* s_uprefix, int n_j,
+                                            int total, int v, int wj) {
+  Fp8Unit u{p.x, p.w, p.ws, 0, 0, 0, 0, v < total};
+  if (!u.valid) return u;
+  const int e = uniform(find_group(s_uprefix, p.num_groups, v));
+  const int gs = uniform(e == 0 ? 0 : s_end[e - 1]);
+  const int gm = uniform(s_end[e]) - gs;
+  int rt, ct;
+  panel_order(v - uniform(s_uprefix[e]), (gm + kTileI - 1) / kTileI, n_j, 4, &rt, &ct);
+  u.row0 = gs + rt * kTileI;
+  u.i_valid = min(kTileI, gm - rt * kTileI);
+  u.j0 = ct * kTileJ;
+  u.j_valid = min(kTileJ, p.n - u.j0);
+  u.a = p.x + (int64_t)u.row0 * p.k;
+  u.b = p.w + ((int64_t)e * p.n + u.j0) * p.k;
+  const int nb = (p.n + kFp8Block - 1) / kFp8Block;
+  u.sw = p.ws + ((int64_t)e * nb + min(u.j0 / kFp8Block + wj, nb - 1)) * p.blocks;
+  return u;
+}
+
+// A persistent grid of workgroups that walk the units.  A unit's stages 0 and 1
+// and the first fragments are loaded during the previous unit's last steps (see
+// Fp8Pipe::step) and its results leave by stores nothing waits for until two
+// steps into the next unit.
 __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) {
   __shared__ int s_end[kMaxGroups];
   __shared__ int s_uprefix[kMaxGroups + 1];
@@ -386,58 +474,52 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
   Fp8Pipe pipe;
   pipe.init(p.k);
   const int nk = p.blocks;
-  for (int v = vb; v < total; v += P) {
-    Fp8Unit u;
-    const int e = uniform(find_group(s_uprefix, p.num_groups, v));
-    const int gs = uniform(e == 0 ? 0 : s_end[e - 1]);
-    const int gm = uniform(s_end[e]) - gs;
-    int rt, ct;
-    panel_order(v - uniform(s_uprefix[e]), (gm + kTileI - 1) / kTileI, n_j, 4, &rt, &ct);
-    u.row0 = gs + rt * kTileI;
-    u.i_valid = min(kTileI, gm - rt * kTileI);
-    u.j0 = ct * kTileJ;
-    u.j_valid = min(kTileJ, p.n - u.j0);
-    u.a = p.x + (int64_t)u.row0 * p.k;
-    u.b = p.w + ((int64_t)e * p.n + u.j0) * p.k;
-    const int nb = (p.n + kFp8Block - 1) / kFp8Block;
-    u.sw = p.ws + ((int64_t)e * nb + min(u.j0 / kFp8Block + pipe.wj, nb - 1)) * p.blocks;
-
+  Fp8Unit u = fp8_unit(p, s_end, s_uprefix, n_j, total, vb, pipe.wj);
+  if (!u.valid) return;
+  i32x8 al[4], ah[4], ahn[4], b[8];
+  Scales sc, sn;
+  pipe.load_scales(sc, p, u, 0);
+  pipe.load_stage<0>(u, 0);
+  pipe.load_stage<1>(u, 1);
+  wait_vm_lgkm<0>();
+  lds_barrier();
+  pipe.first_frags(al, ah, b);
+  for (int v = vb; u.valid; v += P) {
+    const Fp8Unit nx = fp8_unit(p, s_end, s_uprefix, n_j, total, v + P, pipe.wj);
     Acc acc;
     zero(acc);
-    Scales sc, sn;
-    pipe.load_scales(sc, p, u, 0);
-    pipe.load_stage<0>(u, 0);
-    pipe.load_stage<1>(u, 1);
-    wait_vm_lgkm<2 * kLoads>();  // stage 0 has landed (stage 1's loads follow it)
-    lds_barrier();
-    i32x8 al[4], ah[4], b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      b[i] = Fp8Pipe::frag(s_b0, pipe.fb, i);
-      if (i < 4) al[i] = Fp8Pipe::frag(s_a0, pipe.fa, i);
-    }
     int kt = 0;
     for (; kt + 4 <= nk; kt += 4) {
-      pipe.step<0>(acc, al, ah, b, sc, u, kt);
-      pipe.step<1>(acc, al, ah, b, sc, u, kt + 1);
-      pipe.load_scales(sn, p, u, (kt >> 2) + 1);
-      pipe.step<2>(acc, al, ah, b, sc, u, kt + 2);
-      pipe.step<3>(acc, al, ah, b, sc, u, kt + 3);
+      pipe.step<0>(acc, al, ah, ahn, b, sc, sn, p, u, nx, kt);
+      pipe.step<1>(acc, al, ahn, ah, b, sc, sn, p, u, nx, kt + 1);
+      pipe.step<2>(acc, al, ah, ahn, b, sc, sn, p, u, nx, kt + 2);
+      pipe.step<3>(acc, al, ahn, ah, b, sc, sn, p, u, nx, kt + 3);
       sc = sn;
     }
     if (kt < nk) {
-      pipe.step<0>(acc, al, ah, b, sc, u, kt);
-      if (kt + 1 < nk) pipe.step<1>(acc, al, ah, b, sc, u, kt + 1);
-      if (kt + 2 < nk) pipe.step<2>(acc, al, ah, b, sc, u, kt + 2);
+      pipe.step<0>(acc, al, ah, ahn, b, sc, sn, p, u, nx, kt);
+      if (kt + 1 < nk) pipe.step<1>(acc, al, ahn, ah, b, sc, sn, p, u, nx, kt + 1);
+      if (kt + 2 < nk) pipe.step<2>(acc, al, ah, ahn, b, sc, sn, p, u, nx, kt + 2);
     }
-    wait_vm_lgkm<0>();
-    __syncthreads();  // every wave is done with LDS before results pass through it
+    if (nk == 1) {  // no second step has loaded the next unit's stage 1
+      wait_vm_lgkm<0>();
+      lds_barrier();
+      pipe.load_stage<1>(nx, 1);
+    }
+    pipe.load_scales(sc, p, nx, 0);
     const int ln = lane_here();
     const OutTile ot = out_tile(p.y + (int64_t)u.row0 * p.n + u.j0, p.n, u.i_valid, u.j_valid, pipe.wi, pipe.wj, ln, 2);
-    epilogue_store<kStoreBf16>(acc, ot, s_a1 + pipe.w * 8192, ln);
-    wait_vm_lgkm<63>();
-    __syncthreads();  // ... and before the next unit's loads
+    store_tile(acc, ot, s_out[pipe.w], ln);
+    if (nk & 1) {
+      // the last step's fragments came from buffer 1; the next unit's stage 0 is in
+      // buffer 0, loaded before the 32 stores
+      wait_vm_lgkm<epilogue_ops<kStoreBf16>()>();
+      lds_barrier();
+      pipe.first_frags(al, ah, b);
+    }
+    u = nx;
   }
+  wait_vm_lgkm<0>();
 }
 
 }  // namespace
