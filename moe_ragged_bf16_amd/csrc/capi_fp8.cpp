@@ -163,13 +163,6 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
   Fp8GemmParams p{};
   p.x = static_cast<const uint8_t*>(x);
   p.xs = static_cast<const uint32_t*>(x_scale);
-  if (!quantized) {
-    uint8_t* q = static_cast<uint8_t*>(workspace);
-    if (launch_fp8_quantize_rows(rows_params(x, x_dtype, q, q + xs.scale_off, m_rows, k), s) != hipSuccess)
-      return status(MDG_EHIP);
-    p.x = q;
-    p.xs = reinterpret_cast<const uint32_t*>(q + xs.scale_off);
-  }
   p.w = static_cast<const uint8_t*>(w);
   p.ws = static_cast<const uint8_t*>(w_scale);
   p.offs = offs;
@@ -179,12 +172,31 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
   p.k = (int32_t)k;
   p.num_groups = num_groups;
   p.blocks = (int32_t)blocks_of(k);
-  // at most this many tiles: the whole row tiles and one partial one of every group
-  const int64_t tiles = ((m_rows + kTileI - 1) / kTileI + std::min<int64_t>(num_groups, m_rows)) *
-                        ((n + kTileJ - 1) / kTileJ);
-  if (tiles > INT32_MAX) return status(MDG_EUNSUPPORTED);
+  const int64_t active = std::min<int64_t>(num_groups, m_rows);  // groups with rows, at most
+  const bool few = m_rows <= kFp8FewRows * active;
+  if (!quantized) {
+    uint8_t* q = static_cast<uint8_t*>(workspace);
+    if (launch_fp8_quantize_rows(rows_params(x, x_dtype, q, q + xs.scale_off, m_rows, k), s) != hipSuccess)
+      return status(MDG_EHIP);
+    p.x = q;
+    p.xs = reinterpret_cast<const uint32_t*>(q + xs.scale_off);
+  }
+  // Groups of kFp8FewRows rows on average: the small kernel alone, a group of more
+  // rows than its units hold as several units.  Up to twice its units' rows on
+  // average: it takes the groups of at most one unit, the tile kernels the others.
+  // Above, groups that small are few and stay with the tile kernels.
+  if (few) return launched(launch_fp8_small(p, (int)(active + m_rows / kFp8SmallRows), INT32_MAX, s));
+  if (m_rows <= 2 * kFp8SmallRows * active) {
+    p.small_rows = kFp8SmallRows;
+    if (launch_fp8_small(p, (int)active, kFp8SmallRows, s) != hipSuccess) return status(MDG_EHIP);
+    if (m_rows <= kFp8SmallRows) return status(MDG_OK);  // no group has more rows
+  }
+  // Tiles of a size, at most: the whole row tiles and a partial one of every group.
+  const auto tiles = [&](int64_t tile) { return ((m_rows + tile - 1) / tile + active) * ((n + tile - 1) / tile); };
+  if (tiles(kFp8MidTile) > INT32_MAX) return status(MDG_EUNSUPPORTED);
   const int64_t cus = dev.cus > 0 ? dev.cus : 256;
-  return launched(launch_fp8_gemm(p, (int)std::min(tiles, cus), s));
+  if (tiles(kTileI) < 2 * cus) return launched(launch_fp8_mid(p, (int)(tiles(kFp8MidTile) + 7) / 8 * 8, s));
+  return launched(launch_fp8_gemm(p, (int)std::min(tiles(kTileI), cus), s));
 }
 
 }  // extern "C"

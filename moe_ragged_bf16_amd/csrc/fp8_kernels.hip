@@ -23,6 +23,8 @@
 #include "kernel_common.h"
 #include "tile_epilogue.h"
 
+#include <type_traits>
+
 namespace mdg {
 namespace {
 
@@ -199,21 +201,25 @@ __device__ __forceinline__ uint8_t* buf_b() {
 // covers the two wait states between a VALU write of a source and its use, which
 // the compiler does not see inside an asm statement; the matrix pipe is busy with
 // the previous product meanwhile.)
+#define MDG_MFMA(REGS, SEL)                                                                                  \
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL : REGS(c) : "v"(b), "v"(a), \
+               "v"(sb), "v"(sa))
+#define MDG_MFMA_BYTE(REGS)                                              \
+  if constexpr (S == 0) MDG_MFMA(REGS, "op_sel_hi:[0,0,0]");             \
+  else if constexpr (S == 1) MDG_MFMA(REGS, "op_sel:[1,1,0] op_sel_hi:[0,0,0]"); \
+  else if constexpr (S == 2) MDG_MFMA(REGS, "op_sel_hi:[1,1,0]");        \
+  else MDG_MFMA(REGS, "op_sel:[1,1,0] op_sel_hi:[1,1,0]")
+// The accumulator in AGPRs (the tile kernel, whose 256 would not fit else) or VGPRs.
 template <int S>
 __device__ __forceinline__ void mfma_scaled(f32x4& c, const i32x8& b, const i32x8& a, uint32_t sb, uint32_t sa) {
-  if constexpr (S == 0)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
-  else if constexpr (S == 1)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0]"
-                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
-  else if constexpr (S == 2)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0]"
-                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
-  else
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
-                 : "+a"(c) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  MDG_MFMA_BYTE("+a");
 }
+template <int S>
+__device__ __forceinline__ void mfma_scaled_v(f32x4& c, const i32x8& b, const i32x8& a, uint32_t sb, uint32_t sa) {
+  MDG_MFMA_BYTE("+v");
+}
+#undef MDG_MFMA_BYTE
+#undef MDG_MFMA
 
 // Waits until all of this wave's LDS reads have returned.
 __device__ __forceinline__ void wait_lgkm() { __builtin_amdgcn_s_waitcnt(0xC07F); }  // lgkmcnt(0), the others at their most
@@ -405,7 +411,9 @@ __device__ __forceinline__ void store_tile(const Acc& acc, const OutTile& t, uin
   }
 }
 
-// Groups of 4 thread-consecutive experts: clamped ends and the prefix of units.
+// Thread t handles groups 4 t .. 4 t + 3: clamped ends and the prefix of units.
+// Groups the small kernel takes have none.
+template <int TILE>
 __device__ __forceinline__ int fp8_group_table(const Fp8GemmParams& p, int n_j, int* s_end, int* s_uprefix,
                                                int* scratch) {
   const int E = p.num_groups, M = (int)p.m_rows, t = threadIdx.x;
@@ -421,7 +429,8 @@ __device__ __forceinline__ int fp8_group_table(const Fp8GemmParams& p, int n_j, 
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int end = max(before, endv[q]);
-    units[q] = 4 * t + q < E ? (end - start + kTileI - 1) / kTileI * n_j : 0;
+    const int rows = end - start;
+    units[q] = 4 * t + q < E && rows > p.small_rows ? (rows + TILE - 1) / TILE * n_j : 0;
     if (4 * t + q < E) s_end[4 * t + q] = end;
     sum += units[q];
     start = end;
@@ -468,7 +477,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
   __shared__ int s_uprefix[kMaxGroups + 1];
   __shared__ int s_scratch[4];
   const int n_j = (p.n + kTileJ - 1) / kTileJ;
-  const int total = uniform(fp8_group_table(p, n_j, s_end, s_uprefix, s_scratch));
+  const int total = uniform(fp8_group_table<kTileI>(p, n_j, s_end, s_uprefix, s_scratch));
   const int P = gridDim.x, bid = blockIdx.x;
   const int vb = (P % 8 == 0) ? (bid % 8) * (P / 8) + bid / 8 : bid;
   Fp8Pipe pipe;
@@ -522,6 +531,333 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
   wait_vm_lgkm<0>();
 }
 
+// ---------------------------------------------------------------------------
+// the small kernel: few rows to a group
+// ---------------------------------------------------------------------------
+// With few rows a product is the reading of its weights.  A workgroup takes 32
+// columns (rows of w[e]) and up to kFp8SmallRows rows of one group; its waves
+// share the reduction out in pieces of 4 blocks (512 bytes of each weight row),
+// each wave loading weights straight from memory to registers, 16 KiB in flight at
+// once, without LDS or barriers; rows of x come from the caches.  The waves' sums
+// are added in wave order through LDS.  (Quantising bf16 rows in each wave instead
+// of a launch before took as long: 29.8 against 28.8 us for one token.)  Measured: 2 experts' 14336 x 4096 weights at 4.8 TB/s, 64 experts'
+// 1536 x 2048 at 4.9 TB/s (a large copy: 4.9).  (The non-temporal hint lost 7 %: a
+// lane group's two halves of a cache line are two loads.)
+constexpr int kSmallCols = 32;
+
+// Row pieces of TILE rows, group by group (groups of more than `most` rows, and of
+// at most `least`, have none).  A wave finds the piece that holds unit `slot` of
+// `per` units to a piece: expert, first row, rows, and the unit's number within
+// its group; returns the number of units, which slot reaches where there is none.
+// (64 groups at a time with shuffles: no LDS, no barrier.)
+struct Piece {
+  int e, start, rows, unit;
+};
+template <int TILE>
+__device__ __forceinline__ int find_piece(const Fp8GemmParams& p, int slot, int per, int least, int most, Piece* out) {
+  const int lane = threadIdx.x & 63, E = p.num_groups, M = (int)p.m_rows;
+  int carry = 0, before = 0;
+  for (int base = 0; base < E; base += 64) {
+    const int v = base + lane < E ? min(max(p.offs[base + lane], 0), M) : 0;
+    const int incl = max(wave_incl_max(v), carry);
+    int prev = __shfl_up(incl, 1, 64);
+    if (lane == 0) prev = carry;
+    const int m = incl - prev;
+    const int units = m > least && m <= most ? (m + TILE - 1) / TILE * per : 0;
+    const int upto = before + wave_incl_sum(units);
+    const uint64_t over = __ballot(slot < upto);
+    if (over != 0 && slot >= before) {
+      const int src = __ffsll((unsigned long long)over) - 1;
+      out->e = uniform(base + src);
+      out->start = uniform(__shfl(prev, src, 64));
+      out->rows = uniform(__shfl(m, src, 64));
+      out->unit = uniform(slot - (__shfl(upto, src, 64) - __shfl(units, src, 64)));
+    }
+    before = uniform(__shfl(upto, 63, 64));
+    carry = __shfl(incl, 63, 64);
+  }
+  return before;
+}
+
+template <int S>
+__device__ __forceinline__ f32x4 mfma_small(const i32x8& w, const i32x8& x, f32x4 c, uint32_t sw, uint32_t sx) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, S, sw, S, sx);
+}
+
+// MB row blocks of 16; acc[i][j]: row block i, column block j.
+template <int MB>
+__device__ __forceinline__ void small_product(const Fp8GemmParams& p, int e, int row0, int rows, int n0,
+                                              f32x4 (&acc)[MB][2]) {
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int k = p.k, r = lane & 15, c = (lane >> 4) * 16;
+  const int cols = min(kSmallCols, p.n - n0);
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.w) + ((int64_t)e * p.n + n0) * k, 0, uniform(cols * k), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.x) + (int64_t)row0 * k, 0, uniform(rows * k), 0x00020000);
+  const int nb = (p.n + kFp8Block - 1) / kFp8Block;
+  const uint8_t* ws = p.ws + ((int64_t)e * nb + n0 / kFp8Block) * p.blocks;
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ws), 0, uniform(p.blocks), 0x00020000);
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g = w; 4 * g < p.blocks; g += 4) {
+    // 16 bytes at chunk h of block b of row `row` (chunks past the row's end read zeros)
+    auto chunk = [&](__amdgpu_buffer_rsrc_t rsrc, int row, int b, int h) {
+      const int at = (4 * g + b) * kFp8Block + h * 64 + c;
+      return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           rsrc, at < k ? (uint32_t)(row * k + at) : kOutOfRange, 0, 0));
+    };
+    auto join = [](const i32x4& lo, const i32x4& hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); };
+    i32x4 wf[4][2][2], xf[MB == 1 ? 4 : 1][2];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) wf[b][j][h] = chunk(rw, j * 16 + r, b, h);
+    uint32_t sx[MB], sw = 0;
+    const __amdgpu_buffer_rsrc_t rxs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint32_t*>(p.xs) + (int64_t)g * p.m_rows + row0, 0, uniform(rows * 4), 0x00020000);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) sx[i] = __builtin_amdgcn_raw_buffer_load_b32(rxs, (uint32_t)(i * 16 + r) * 4, 0, 0);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      sw |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 4 * g + b, 0, 0) << (8 * b);
+    if constexpr (MB == 1) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) xf[b][h] = chunk(rx, r, b, h);
+    }
+    // All of these loads go out before anything waits (left to itself the
+    // compiler moves each next to its use: 33 us instead of 25 for two experts'
+    // 14336 x 4096).
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        if constexpr (MB > 1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) xf[0][h] = chunk(rx, i * 16 + r, b, h);
+        }
+        const i32x8 x = MB == 1 ? join(xf[MB == 1 ? b : 0][0], xf[MB == 1 ? b : 0][1]) : join(xf[0][0], xf[0][1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const i32x8 wv = join(wf[b][j][0], wf[b][j][1]);
+          if (b == 0) acc[i][j] = mfma_small<0>(wv, x, acc[i][j], sw, sx[i]);
+          else if (b == 1) acc[i][j] = mfma_small<1>(wv, x, acc[i][j], sw, sx[i]);
+          else if (b == 2) acc[i][j] = mfma_small<2>(wv, x, acc[i][j], sw, sx[i]);
+          else acc[i][j] = mfma_small<3>(wv, x, acc[i][j], sw, sx[i]);
+        }
+      }
+  }
+}
+
+// Adds the waves' sums in wave order and stores rows < rows, columns < n as bf16:
+// lane l of a block holds row l % 16 and columns 4 (l / 16) .. + 3.
+template <int MB>
+__device__ __forceinline__ void small_store(const Fp8GemmParams& p, int row0, int rows, int n0,
+                                            const f32x4 (&acc)[MB][2], f32x4* s_acc) {
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) s_acc[((i * 2 + j) * 4 + w) * 64 + lane] = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int t0 = 0; t0 < MB * 2; t0 += 4) {
+    const int t = t0 + w;
+    if (t >= MB * 2) break;
+    f32x4 s = s_acc[t * 4 * 64 + lane];
+#pragma unroll
+    for (int q = 1; q < 4; ++q) s += s_acc[(t * 4 + q) * 64 + lane];
+    const int row = (t >> 1) * 16 + (lane & 15), col = n0 + (t & 1) * 16 + (lane >> 4) * 4;
+    if (row < rows && col < p.n) {
+      u32x2 pk;
+      pk[0] = pack_bf16x2(s[0], s[1]);
+      pk[1] = pack_bf16x2(s[2], s[3]);
+      *reinterpret_cast<u32x2*>(p.y + (int64_t)(row0 + row) * p.n + col) = pk;
+    }
+  }
+}
+
+template <int MB>
+__device__ __forceinline__ void small_unit(const Fp8GemmParams& p, int e, int row0, int rows, int n0, f32x4* s_acc) {
+  f32x4 acc[MB][2];
+  small_product<MB>(p, e, row0, rows, n0, acc);
+  small_store<MB>(p, row0, rows, n0, acc, s_acc);
+}
+
+__global__ __launch_bounds__(256, 3) void fp8_small_kernel(Fp8GemmParams p, int most) {
+  __shared__ f32x4 s_acc[kFp8SmallRows / 16 * 2 * 4 * 64];
+  Piece u;
+  if ((int)blockIdx.y >= find_piece<kFp8SmallRows>(p, blockIdx.y, 1, 0, most, &u)) return;
+  const int row0 = u.start + u.unit * kFp8SmallRows, rows = min(kFp8SmallRows, u.rows - u.unit * kFp8SmallRows);
+  const int n0 = blockIdx.x * kSmallCols;
+  if (rows <= 16) small_unit<1>(p, u.e, row0, rows, n0, s_acc);
+  else if (rows <= 32) small_unit<2>(p, u.e, row0, rows, n0, s_acc);
+  else small_unit<4>(p, u.e, row0, rows, n0, s_acc);
+}
+
+// ---------------------------------------------------------------------------
+// the middle kernel: 128 x 128 tiles
+// ---------------------------------------------------------------------------
+// For launches whose 256 x 256 tiles would leave most CUs idle.  Four waves of
+// 64 x 64, the same stages and LDS layout as the tile kernel's at half the rows
+// (16 KiB an operand), two buffers, two workgroups to a CU, one of which computes
+// while the other waits.  A CU's stages then move 64 bytes per clock of matrix work,
+// about what it can load, which bounds it: 2048 x 2048 x 2048 takes 15 us and 16 groups
+// of 188 rows on average x 1000 x 2000 16 us, where the tile kernel takes 23 and 36.
+// (Four buffers and one workgroup to a CU: 15.5 and 16.5 us, and 27 % longer where
+// there are more units than CUs.)
+constexpr int kMidTile = kFp8MidTile;
+constexpr int kMidBytes = kMidTile * kFp8Block;
+
+// Buffer B of operand A (0) or B (1); each a static array of its own, so that the
+// compiler can tell reads of one from loads still landing in another.
+template <int OPERAND, int B>
+__device__ __forceinline__ uint8_t* mid_buffer() {
+  __shared__ __attribute__((aligned(1024))) uint8_t s_buf[kMidBytes];
+  return s_buf;
+}
+
+__global__ __launch_bounds__(256, 2) void fp8_mid_kernel(Fp8GemmParams p) {
+  const int n_j = (p.n + kMidTile - 1) / kMidTile;
+  // Workgroups go round the XCDs; each XCD takes consecutive units (which share
+  // weights and rows), an eighth of them all.  The grid is an upper bound, so this
+  // goes by the units there are: by the grid's size the first XCDs would get more.
+  Piece u;
+  const int total = find_piece<kMidTile>(p, -1, n_j, p.small_rows, INT32_MAX, &u), share = (total + 7) / 8;
+  const int v = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= share || v >= total) return;
+  find_piece<kMidTile>(p, v, n_j, p.small_rows, INT32_MAX, &u);
+  const int e = u.e, gs = u.start, gm = u.rows;
+  int rt, ct;
+  panel_order(u.unit, (gm + kMidTile - 1) / kMidTile, n_j, 4, &rt, &ct);
+  const int row0 = gs + rt * kMidTile, j0 = ct * kMidTile;
+  const int i_valid = min(kMidTile, gm - rt * kMidTile), j_valid = min(kMidTile, p.n - j0);
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), wi = w >> 1, wj = w & 1;
+  const int k = p.k, nk = p.blocks;
+  const uint8_t* xa = p.x + (int64_t)row0 * k;
+  const uint8_t* xb = p.w + ((int64_t)e * p.n + j0) * k;
+  const int nb = (p.n + kFp8Block - 1) / kFp8Block;
+  const uint8_t* ws = p.ws + ((int64_t)e * nb + ct) * nk;  // (a tile's 128 columns are one block's)
+  const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
+  const uint32_t off = (uint32_t)(w * 8 + (lane >> 3)) * (uint32_t)k + chunk;
+
+  auto load_stage = [&](auto buffer, int kt) {
+    constexpr int B = decltype(buffer)::value;
+    const int left = k - kt * kFp8Block;
+    const bool in = left > 0;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(xa) + (in ? kt * kFp8Block : 0), 0, uniform(in ? i_valid * k - kt * kFp8Block : 0), 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(xb) + (in ? kt * kFp8Block : 0), 0, uniform(in ? j_valid * k - kt * kFp8Block : 0), 0x00020000);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t at = (int)chunk < left ? off + (uint32_t)(q * 32) * (uint32_t)k : kOutOfRange;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(mid_buffer<0, B>() + (q * 4 + w) * 1024), 16, at, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(mid_buffer<1, B>() + (q * 4 + w) * 1024), 16, at, 0, 0, 0);
+    }
+  };
+  const int r = lane & 15, c = ((lane >> 4) ^ (r & 7)) * 16;
+  const int fa = (wi * 64 + r) * 128 + c, fb = (wj * 64 + r) * 128 + c;
+  uint32_t sx[4], sw, nx[4], nw;  // scales of 4 blocks, and of the next 4
+  auto load_scales = [&](uint32_t (&x)[4], uint32_t* ww, int g) {
+    const bool in = 4 * g < nk;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint32_t*>(p.xs) + (in ? (int64_t)g * p.m_rows + row0 : 0), 0,
+        uniform(in ? (int)(p.m_rows - row0) * 4 : 0), 0x00020000);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(wi * 64 + i * 16 + r) * 4, 0, 0);
+    const __amdgpu_buffer_rsrc_t rws = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ws), 0, uniform(nk), 0x00020000);
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rws, 4 * g + i, 0, 0) << (8 * i);
+    *ww = v;
+  };
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // Stage kt (S = kt % 4, buffer S % BUFS): wait for its loads (those of the next
+  // BUFS - 1, or 2 of 4 buffers', 8 each, follow them) and read its fragments.
+  // BUFS == 4: behind the barrier every wave is done with stage kt - 1, whose
+  // buffer takes stage kt + 3.  BUFS == 2: a second barrier after the reads frees
+  // stage kt's own buffer for stage kt + 2.
+  auto step = [&](auto number, int kt) {
+    constexpr int S = decltype(number)::value, B = S & 1;
+    wait_vm_lgkm<8>();
+    lds_barrier();
+    i32x8 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = Fp8Pipe::frag(mid_buffer<0, B>(), fa, i);
+      b[i] = Fp8Pipe::frag(mid_buffer<1, B>(), fb, i);
+    }
+    wait_lgkm();
+    lds_barrier();  // every wave has its fragments
+    if constexpr (S == 3) load_scales(nx, &nw, (kt >> 2) + 1);
+    load_stage(std::integral_constant<int, B>{}, kt + 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mfma_scaled_v<S>(acc[i][j], b[j], a[i], sw, sx[i]);
+    if constexpr (S == 3) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sx[i] = nx[i];
+      sw = nw;
+    }
+  };
+  load_scales(sx, &sw, 0);
+  load_stage(std::integral_constant<int, 0>{}, 0);
+  load_stage(std::integral_constant<int, 1>{}, 1);
+  int kt = 0;
+  for (; kt + 4 <= nk; kt += 4) {
+    step(std::integral_constant<int, 0>{}, kt);
+    step(std::integral_constant<int, 1>{}, kt + 1);
+    step(std::integral_constant<int, 2>{}, kt + 2);
+    step(std::integral_constant<int, 3>{}, kt + 3);
+  }
+  if (kt < nk) {
+    step(std::integral_constant<int, 0>{}, kt);
+    if (kt + 1 < nk) step(std::integral_constant<int, 1>{}, kt + 1);
+    if (kt + 2 < nk) step(std::integral_constant<int, 2>{}, kt + 2);
+  }
+  wait_vm_lgkm<0>();
+  __syncthreads();
+  // 16 rows x 64 columns of a wave at a time through LDS to 128-byte row segments
+  uint8_t* xo = mid_buffer<0, 0>() + w * 2048;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x2 pk;
+      pk[0] = pack_bf16x2(acc[i][j][0], acc[i][j][1]);
+      pk[1] = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
+      *reinterpret_cast<u32x2*>(xo + r * 128 + (((2 * j + (lane >> 5)) ^ (r & 7)) << 4) + ((lane >> 4) & 1) * 8) = pk;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int rr = q * 8 + (lane >> 3), cc = lane & 7;
+      const u32x4 v4 = *reinterpret_cast<const u32x4*>(xo + rr * 128 + ((cc ^ (rr & 7)) << 4));
+      const int row = wi * 64 + i * 16 + rr, col = wj * 64 + cc * 8;
+      if (row < i_valid && col < j_valid)
+        *reinterpret_cast<u32x4*>(p.y + (int64_t)(row0 + row) * p.n + j0 + col) = v4;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 }  // namespace
 
 hipError_t launch_fp8_quantize_rows(const Fp8RowsParams& p, hipStream_t s) {
@@ -542,6 +878,17 @@ hipError_t launch_fp8_quantize_weight(const Fp8WeightParams& p, hipStream_t s) {
     if (p.fp32) hipLaunchKernelGGL((quantize_weight_kernel<true, false>), g, b, 0, s, p);
     else hipLaunchKernelGGL((quantize_weight_kernel<false, false>), g, b, 0, s, p);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_small(const Fp8GemmParams& p, int units, int most, hipStream_t s) {
+  const dim3 g((p.n + kSmallCols - 1) / kSmallCols, units), b(256);
+  hipLaunchKernelGGL(fp8_small_kernel, g, b, 0, s, p, most);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_mid(const Fp8GemmParams& p, int grid, hipStream_t s) {
+  hipLaunchKernelGGL(fp8_mid_kernel, dim3(grid), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

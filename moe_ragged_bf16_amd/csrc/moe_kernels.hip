@@ -14,72 +14,6 @@
 namespace mdg {
 namespace {
 
-// ---------------------------------------------------------------------------
-// reductions over the L lanes that share a row (L a power of two, 1..64)
-// ---------------------------------------------------------------------------
-// Steps of 1, 2, 4 and 8 lanes are DPP moves within a row of 16 lanes (quad
-// permutes, then the half-row and row mirrors: once groups of 4 (8) agree, the
-// mirror image of a lane holds the other group's value); steps of 16 and 32
-// swap rows with the gfx950 permlane swaps.  No step touches LDS.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
-}
-
-template <int STEP>
-__device__ __forceinline__ void partner(uint32_t v, uint32_t* a, uint32_t* b) {
-  if constexpr (STEP == 1) {
-    *a = v, *b = dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
-  } else if constexpr (STEP == 2) {
-    *a = v, *b = dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
-  } else if constexpr (STEP == 4) {
-    *a = v, *b = dpp<0x141>(v);  // row_half_mirror
-  } else if constexpr (STEP == 8) {
-    *a = v, *b = dpp<0x140>(v);  // row_mirror
-  } else if constexpr (STEP == 16) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    *a = r[0], *b = r[1];
-  } else {
-    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    *a = r[0], *b = r[1];
-  }
-}
-
-template <int L, int STEP = 1>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  if constexpr (STEP < L) {
-    uint32_t a, b;
-    partner<STEP>(v, &a, &b);
-    return group_max<L, STEP * 2>(max(a, b));
-  } else {
-    return v;
-  }
-}
-
-// (The two addends of a step are the same pair on both sides, so every lane of
-// the group ends with the same bits.)
-template <int L, int STEP = 1>
-__device__ __forceinline__ float group_sum(float v) {
-  if constexpr (STEP < L) {
-    uint32_t a, b;
-    partner<STEP>(__float_as_uint(v), &a, &b);
-    return group_sum<L, STEP * 2>(__uint_as_float(a) + __uint_as_float(b));
-  } else {
-    return v;
-  }
-}
-
-template <int L, int STEP = 1>
-__device__ __forceinline__ float group_fmax(float v) {
-  if constexpr (STEP < L) {
-    uint32_t a, b;
-    partner<STEP>(__float_as_uint(v), &a, &b);
-    return group_fmax<L, STEP * 2>(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  } else {
-    return v;
-  }
-}
-
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t narrow(float f) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));

@@ -174,6 +174,19 @@ def test_product(sizes, N, K):
     assert torch.equal(mdg.grouped_fp8_gemm_fwd(rows, w8.q, w8.scale, indptr)[:t], y[:t])
 
 
+@pytest.mark.parametrize("E,rows,N,K", [
+    (220, 29000, 768, 128), (220, 29000, 520, 256), (180, 24000, 776, 384), (150, 30000, 1000, 400), (90, 30000, 1536, 640),
+    (1, 2050, 14600, 512), (3, 5000, 6144, 896), (64, 20000, 1288, 1168), (200, 28000, 640, 16)])
+def test_product_of_many_tiles(E, rows, N, K):
+    """Launches whose 256 x 256 tiles fill the GPU more than twice, with 1 to 10
+    stages (odd and even numbers) and rows in groups of every size."""
+    rng = np.random.default_rng(E + K)
+    sizes = rng.multinomial(rows, rng.dirichlet(np.full(E, 1.0)))
+    if E > 4:
+        sizes[1] = 0
+    check_product(draw((int(sizes.sum()) + 5, K), 1, spread=False), draw((E, N, K), 2, spread=False), sizes, 5)
+
+
 @pytest.mark.parametrize("sizes,N,K", [([40, 0, 300], 264, 400), ([7, 9], 128, 2048), ([20, 520], 384, 128)])
 def test_product_of_blocks_of_different_size(sizes, N, K):
     """Each block of 128 under a scale of its own, rows and weights alike."""
