@@ -333,13 +333,13 @@ struct Fp8Pipe {
   // them still on their way from LDS) and the loads of stage kt + 1 are in flight.
   //  * After the first products: this wave's LDS reads have returned; behind the
   //    barrier every wave's have, so buffer S % 2 is free, and the loads of stage
-  //    kt + 2 go out to it during the first half.  For a unit's last two stages
+  //    kt + 2 go out to it over the next 44 products.  For a unit's last two stages
   //    these are the next unit's stages 0 and 1 (stage S % 2), so the loads never
   //    pause between units.
   //  * Half way: stage kt + 1 has landed, behind the barrier in
   //    every wave; the second half reads its fragments, each b into the registers
   //    of the one that has been used.
-  // A stage's loads thus have 1 1/4 to 1 1/2 steps to land.
+  // A stage's loads thus have 3/4 to 1 1/2 steps to land.
   template <int S>
   __device__ __forceinline__ void step(Acc& acc, i32x8 (&al)[4], const i32x8 (&ah)[4], i32x8 (&ahn)[4], i32x8 (&b)[8],
                                        const Scales& sc, Scales& sn, const Fp8GemmParams& p, const Fp8Unit& u,
@@ -353,33 +353,39 @@ struct Fp8Pipe {
     const bool in = kt + 2 < p.blocks;
     const Stage sa = stage(in ? u.a : nx.a, in ? u.i_valid : nx.i_valid, in ? kt + 2 : B);
     const Stage sb = stage(in ? u.b : nx.b, in ? u.j_valid : nx.j_valid, in ? kt + 2 : B);
+    auto issue = [&](int i) {
+      if (i & 1) load(sb, buf_b<B>(), i >> 1);
+      else load(sa, buf_a<B>(), i >> 1);
+    };
 #pragma unroll
     for (int jb = 1; jb < 8; ++jb)
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
         mfma_scaled<S>(acc[ib][jb], b[jb], al[ib], sc.w, sc.x[ib]);
-        const int i = (jb - 1) * 4 + ib;
-        if (i < 16) {
-          if (i & 1) load(sb, buf_b<B>(), i >> 1);
-          else load(sa, buf_a<B>(), i >> 1);
-        }
+        const int m = (jb - 1) * 4 + ib;
+        if (m * kFirstLoads / 28 < (m + 1) * kFirstLoads / 28) issue(m * kFirstLoads / 28);
       }
-    // Stage kt + 1 has landed.  After it were issued this step's 16 loads and, in a
-    // unit's first step, the previous unit's 32 stores.
-    if (S == 0 && kt == 0) wait_vm_lgkm<2 * kLoads + epilogue_ops<kStoreBf16>()>();
-    else wait_vm_lgkm<2 * kLoads>();
+    // Stage kt + 1 has landed.  After it were issued this step's loads so far and,
+    // in a unit's first step, the previous unit's 32 stores.
+    if (S == 0 && kt == 0) wait_vm_lgkm<kFirstLoads + epilogue_ops<kStoreBf16>()>();
+    else wait_vm_lgkm<kFirstLoads>();
     lds_barrier();
 #pragma unroll
     for (int jb = 0; jb < 8; ++jb) {
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
         mfma_scaled<S>(acc[4 + ib][jb], b[jb], ah[ib], sc.w, sc.x[4 + ib]);
+        if (jb < 4 && ib == 3) issue(kFirstLoads + jb);
         if (ib == 1 && jb < 4) al[jb] = frag(buf_a<N>(), fa, jb);
         if (ib == 1 && jb >= 4) ahn[jb - 4] = frag(buf_a<N>(), fa, jb);
       }
       b[jb] = frag(buf_b<N>(), fb, jb);
     }
   }
+  // Loads of a step that go out in its first half; the other 4 follow in the second.
+  // All 16 within 16 products stalled the products behind them (16384 rows, 8
+  // experts of 14336 x 4096: 810 us; over the first half 776, so 758, 8 + 8 763).
+  static constexpr int kFirstLoads = 2 * kLoads - 4;
 };
 
 // Writes the wave's 128 x 128 sub-tile as bf16, 16 rows at a time through 4 KiB of
