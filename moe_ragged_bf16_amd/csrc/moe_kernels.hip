@@ -14,58 +14,77 @@
 namespace mdg {
 namespace {
 
-__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t narrow(float f) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
 }
 
 constexpr float kNegInf = -__builtin_inff();
 
-// V consecutive logits of a row from column c0; columns at or past `experts` read -inf.
-template <int V>
-__device__ __forceinline__ void load_logits(float (&l)[V], const void* base, int64_t row, int c0, int experts,
-                                            bool fp32, bool vec) {
-  const int64_t at = row * experts + c0;
-  if (vec) {  // a lane's V columns are all there or all not
-    if (c0 >= experts) {
+// Sum over a wave's groups of L lanes, lane by lane of a group: rotations within
+// rows of 16 lanes, then the permlane swaps.
+template <int L, int STEP = 8>
+__device__ __forceinline__ float sum_over_groups(float v) {
+  if constexpr (STEP >= L && STEP > 0) {
+    return sum_over_groups<L, STEP / 2>(v + __uint_as_float(dpp<0x120 + STEP>(__float_as_uint(v))));  // row_ror
+  } else {
+    uint32_t a, b;
+    if constexpr (L <= 16) {
+      partner<16>(__float_as_uint(v), &a, &b);
+      v = __uint_as_float(a) + __uint_as_float(b);
+    }
+    if constexpr (L <= 32) {
+      partner<32>(__float_as_uint(v), &a, &b);
+      v = __uint_as_float(a) + __uint_as_float(b);
+    }
+    return v;
+  }
+}
+
+// V consecutive logits of a row from column c0, in their bits (bf16: two to a word).
+template <int V, bool FP32>
+struct LogitBits {
+  static constexpr int kWords = FP32 ? V : V / 2;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const void* base, int64_t row, int c0, int experts, bool vec) {
+    const int64_t at = row * experts + c0;
+    if (vec) {  // a lane's V columns are all there or all not
+      if (c0 < experts) {
+        const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + at * (FP32 ? 4 : 2));
 #pragma unroll
-      for (int v = 0; v < V; ++v) l[v] = kNegInf;
-    } else if (fp32) {
-      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at);
+        for (int i = 0; i < kWords / 4; ++i) {
+          const u32x4 x = q[i];
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const f32x4 x = q[i];
+          for (int c = 0; c < 4; ++c) w[4 * i + c] = x[c];
+        }
+      } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) l[4 * i + c] = x[c];
+        for (int i = 0; i < kWords; ++i) w[i] = FP32 ? 0xff800000u : 0xff80ff80u;
       }
-    } else {
-      const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at);
+    } else {  // columns at or past `experts` read -inf
 #pragma unroll
-      for (int i = 0; i < V / 8; ++i) {
-        const u32x4 x = q[i];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          l[8 * i + 2 * c] = __uint_as_float(x[c] << 16);
-          l[8 * i + 2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u);
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (FP32) {
+          w[i] = c0 + i < experts ? static_cast<const uint32_t*>(base)[at + i] : 0xff800000u;
+        } else {
+          const uint16_t* q = static_cast<const uint16_t*>(base) + at + 2 * i;
+          const uint32_t lo = c0 + 2 * i < experts ? q[0] : 0xff80u, hi = c0 + 2 * i + 1 < experts ? q[1] : 0xff80u;
+          w[i] = lo | (hi << 16);
         }
       }
     }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      l[v] = kNegInf;
-      if (c0 + v < experts)
-        l[v] = fp32 ? static_cast<const float*>(base)[at + v] : widen(static_cast<const uint16_t*>(base)[at + v]);
-    }
   }
-}
+  __device__ __forceinline__ float value(int v) const {
+    if constexpr (FP32) return __uint_as_float(w[v]);
+    else return __uint_as_float((v & 1) ? w[v / 2] & 0xffff0000u : w[v / 2] << 16);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // routing
 // ---------------------------------------------------------------------------
 // An order-preserving integer of a logit: -0 and +0 are equal, NaN is above
-// everything.  kKeyNone is -inf's (an expert that cannot be chosen); 0 is below
-// every key (a chosen expert, a column past the last).
+// everything.  -inf, an expert that cannot be chosen, is kKeyNone or (bf16) below.
 constexpr uint32_t kKeyNone = 0x007fffffu;
 
 __device__ __forceinline__ uint32_t key_of(float f) {
@@ -75,6 +94,51 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+
+// One round of the top-k: the largest key left in the group's V keys a lane, the
+// lowest expert among equal ones.  A bf16 key leaves the lower 16 bits free for the
+// expert's complement, so its maximum is the choice; fp32 takes the maximum of the
+// keys, then the lowest column that has it.  The chosen key is cleared.  Returns
+// the key (<= kKeyNone: nothing is left) and the expert.
+template <int L, int V, bool FP32>
+__device__ __forceinline__ uint32_t choose(uint32_t (&key)[V], int c0, int* expert) {
+  uint32_t best = key[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) best = max(best, key[v]);
+  const uint32_t top = group_max<L>(best);
+  if constexpr (FP32) {
+    uint32_t col = 0xffffu;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v)
+      if (key[v] == top) col = c0 + v;
+    col = 0xffffu - group_max<L>(0xffffu - col);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (c0 + v == (int)col) key[v] = 0u;
+    *expert = (int)col;
+    return top;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key[v] == top) key[v] = 0u;
+    *expert = (int)(0xffffu - (top & 0xffffu));
+    return top;
+  }
+}
+
+// The key of column c0 + v of a row.
+template <bool FP32>
+__device__ __forceinline__ uint32_t choice_key(float f, int column) {
+  const uint32_t k = key_of(f);
+  return FP32 ? k : (k & 0xffff0000u) | (0xffffu - (uint32_t)column);
+}
+// A key's logit.
+template <bool FP32>
+__device__ __forceinline__ float choice_value(uint32_t key) {
+  if constexpr (FP32) return value_of(key);
+  else return (key & 0xffff0000u) == 0xffff0000u ? __uint_as_float(0x7fc00000u)
+                                                 : value_of((key & 0x80000000u) ? key & 0xffff0000u : key | 0xffffu);
 }
 
 // The balance loss from the sums of one expert: a = E c / (k Tr^2) is the
@@ -89,16 +153,20 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// L lanes hold a row, V consecutive logits each.  The top-k is k rounds of the
-// largest key left: the lane's own largest, then over the group, ties to the
-// lowest lane and there to the lowest column (lanes and columns are in expert
-// order).  The first round's value is the softmax maximum.  Each lane adds the
-// probabilities of its columns over all rows of its block in registers.
+// Slots j = i * L + (lane in group) that a lane keeps of its row's top-k.
 template <int L, int V>
+constexpr int own_slots() {
+  constexpr int most = kRouteMaxTopK < L * V ? kRouteMaxTopK : L * V;
+  return most > L ? most / L : 1;
+}
+
+// L lanes hold a row, V consecutive logits each.  The top-k is k rounds of choose(),
+// in registers and DPP moves; the first round's value is the softmax maximum.
+// Each lane adds the probabilities of its columns over all rows of its block in
+// registers; the next row's logits load while a row is worked on.
+template <int L, int V, bool FP32>
 __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p) {
-  constexpr int kOwn = (kRouteMaxTopK < L * V ? kRouteMaxTopK : L * V) > L
-                           ? (kRouteMaxTopK < L * V ? kRouteMaxTopK : L * V) / L
-                           : 1;  // slots j = i * L + lane-in-group a lane keeps
+  constexpr int kOwn = own_slots<L, V>();
   extern __shared__ uint8_t smem[];
   const int E = p.experts, k = p.top_k;
   const int waves = blockDim.x >> 6;
@@ -106,73 +174,66 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p)
   int* s_cnt = reinterpret_cast<int*>(s_sum + waves * E);    // [E]
   int* s_routed = s_cnt + E;                                 // [1]
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int lig = lane & (L - 1), grp = tid / L;
+  const int lig = lane & (L - 1), grp = tid / L, c0 = lig * V;
   for (int e = tid; e < E; e += blockDim.x) s_cnt[e] = 0;
   if (tid == 0) *s_routed = 0;
-  __syncthreads();
 
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
   int routed = 0;
   const int64_t row_end = min(p.tokens, (int64_t)(blockIdx.x + 1) * p.rows_per_block);
-  for (int64_t r = (int64_t)blockIdx.x * p.rows_per_block + grp; r < row_end; r += blockDim.x / L) {
+  int64_t r = (int64_t)blockIdx.x * p.rows_per_block + grp;
+  LogitBits<V, FP32> bits;
+  bool keep = true;
+  if (r < row_end) {
+    bits.load(p.logits, r, c0, E, p.vec != 0);
+    keep = p.mask == nullptr || p.mask[r] != 0;
+  }
+  __syncthreads();
+  while (r < row_end) {
     float l[V];
-    load_logits<V>(l, p.logits, r, lig * V, E, p.fp32 != 0, p.vec != 0);
-    const bool keep = p.mask == nullptr || p.mask[r] != 0;
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (!keep) l[v] = kNegInf;
-      key[v] = lig * V + v < E ? key_of(l[v]) : 0u;
+      l[v] = keep ? bits.value(v) : kNegInf;
+      key[v] = c0 + v < E ? choice_key<FP32>(l[v], c0 + v) : 0u;
     }
-    uint32_t first = 0;
-    float own_l[kOwn];
+    const int64_t row = r;
+    r += blockDim.x / L;
+    if (r < row_end) {
+      bits.load(p.logits, r, c0, E, p.vec != 0);
+      keep = p.mask == nullptr || p.mask[r] != 0;
+    }
+    uint32_t first = 0, own_key[kOwn];
     int own_e[kOwn];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      own_l[i] = 0.0f;
+      own_key[i] = 0u;
       own_e[i] = -1;
       for (int jl = 0; jl < L && i * L + jl < k; ++jl) {
-        uint32_t best = key[0];
-#pragma unroll
-        for (int v = 1; v < V; ++v) best = max(best, key[v]);
-        const uint32_t top = group_max<L>(best);
+        int e;
+        const uint32_t top = choose<L, V, FP32>(key, c0, &e);
         if (i == 0 && jl == 0) first = top;
-        if (top <= kKeyNone) break;  // the group has nothing left to choose
-        uint64_t hit = __ballot(best == top);
-        if constexpr (L < 64) hit = (hit >> (lane & ~(L - 1))) & ((1ull << L) - 1);
-        const int winner = __ffsll((unsigned long long)hit) - 1;
-        int at = 0;  // the winner's lowest column with this key
-#pragma unroll
-        for (int v = V - 1; v >= 0; --v)
-          if (key[v] == top) at = v;
-        if (lig == winner) {
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (v == at) key[v] = 0u;
-          atomicAdd(&s_cnt[lig * V + at], 1);
-        }
-        const int e = winner * V + __shfl(at, (lane & ~(L - 1)) + winner, 64);
-        if (lig == jl) {
-          own_l[i] = value_of(top);
+        if (lig == jl && top > kKeyNone) {
+          own_key[i] = top;
           own_e[i] = e;
         }
       }
     }
     const bool live = first > kKeyNone;
-    const float big = live ? value_of(first) : 0.0f;
+    const float big = live ? choice_value<FP32>(first) : 0.0f;
     float ex[V], total = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       ex[v] = live ? expf(l[v] - big) : 0.0f;
-      if (lig * V + v < E) total += ex[v];
+      if (c0 + v < E) total += ex[v];
     }
     total = group_sum<L>(total);
     float own_x[kOwn], chosen = 0.0f;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      own_x[i] = own_e[i] >= 0 ? expf(own_l[i] - big) : 0.0f;
+      own_x[i] = own_e[i] >= 0 ? expf(choice_value<FP32>(own_key[i]) - big) : 0.0f;
       chosen += own_x[i];
     }
     chosen = group_sum<L>(chosen);
@@ -181,8 +242,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p)
     for (int i = 0; i < kOwn; ++i) {
       const int j = i * L + lig;
       if (j < k) {
-        p.weight[r * k + j] = live ? own_x[i] / by : 0.0f;
-        p.idx[r * k + j] = own_e[i];
+        p.weight[row * k + j] = live ? own_x[i] / by : 0.0f;
+        p.idx[row * k + j] = own_e[i];
+        if (own_e[i] >= 0) atomicAdd(&s_cnt[own_e[i]], 1);
       }
     }
     if (live) {
@@ -196,8 +258,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p)
   // the block's sums: over the wave's groups, then over the waves in order
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float s = acc[v];
-    for (int d = L; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+    const float s = sum_over_groups<L>(acc[v]);
     if (lane < L && lane * V + v < E) s_sum[w * E + lane * V + v] = s;
   }
   if (routed) atomicAdd(s_routed, routed);
@@ -303,54 +364,82 @@ __global__ __launch_bounds__(kRouteThreads) void route_finish_kernel(RouteParams
 //   dl_e = p_e (g a_e - D) + [e chosen in slot j] (w_j (dw_j - sum_j w dw) with
 //   normalisation, else w_j dw_j).
 // The softmax is computed anew from the logits (cheaper than reading it back).
-template <int L, int V>
+template <int L, int V, bool FP32>
 __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdParams p) {
+  constexpr int kOwn = own_slots<L, V>();
   const int E = p.experts, k = p.top_k;
-  const int lane = threadIdx.x & 63, lig = lane & (L - 1);
+  const int lane = threadIdx.x & 63, lig = lane & (L - 1), c0 = lig * V;
   const int64_t r = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   if (r >= p.tokens) return;
-  float l[V], dl[V];
-  load_logits<V>(l, p.logits, r, lig * V, E, p.fp32 != 0, p.vec != 0);
-  const int32_t* idx = p.idx + r * k;
-  const bool live = idx[0] >= 0;
-  float big = kNegInf, total = 0.0f, pa = 0.0f;
+  LogitBits<V, FP32> bits;
+  bits.load(p.logits, r, c0, E, p.vec != 0);
+  // this lane's slots of the row
+  int own_e[kOwn];
+  float own_w[kOwn], own_d[kOwn];
 #pragma unroll
-  for (int v = 0; v < V; ++v) big = fmaxf(big, l[v]);
-  big = group_fmax<L>(big);
+  for (int i = 0; i < kOwn; ++i) {
+    const int j = i * L + lig;
+    own_e[i] = j < k ? p.idx[r * k + j] : -1;
+    own_w[i] = j < k ? p.weight[r * k + j] : 0.0f;
+    own_d[i] = j < k && p.dweight ? p.dweight[r * k + j] : 0.0f;
+  }
   const float g = p.dloss ? *p.dloss : 0.0f;
   float a[V];
+  if (p.vec && c0 < E) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = p.balance[c0 + v];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = c0 + v < E ? p.balance[c0 + v] : 0.0f;
+  }
+  float inner = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    own_d[i] = own_e[i] >= 0 ? own_d[i] : 0.0f;
+    inner += own_w[i] * own_d[i];
+  }
+  inner = group_sum<L>(inner);
+  const bool live = __shfl(own_e[0], lane & ~(L - 1), 64) >= 0;
+  float l[V], dl[V], big = kNegInf, total = 0.0f, pa = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = lig * V + v;
-    a[v] = e < E ? p.balance[e] * g : 0.0f;
-    l[v] = e < E ? expf(l[v] - big) : 0.0f;
+    l[v] = bits.value(v);
+    big = fmaxf(big, l[v]);
+  }
+  big = group_fmax<L>(big);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    a[v] *= g;
+    l[v] = c0 + v < E ? expf(l[v] - big) : 0.0f;
     total += l[v];
     pa += l[v] * a[v];
   }
   total = group_sum<L>(total);
   pa = group_sum<L>(pa);
   const float inv = 1.0f / total;
-  float inner = 0.0f;
-  if (p.dweight)
-    for (int j = 0; j < k; ++j)
-      if (idx[j] >= 0) inner += p.weight[r * k + j] * p.dweight[r * k + j];
   const float d = pa * inv + (p.normalize ? 0.0f : inner);
 #pragma unroll
   for (int v = 0; v < V; ++v) dl[v] = l[v] * inv * (a[v] - d);
-  if (p.dweight)
-    for (int j = 0; j < k; ++j) {
-      const float add = p.weight[r * k + j] * (p.dweight[r * k + j] - (p.normalize ? inner : 0.0f));
-      const int at = idx[j] - lig * V;
+  if (p.dweight) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (at == v) dl[v] += add;
+    for (int i = 0; i < kOwn; ++i) {
+      const float own_add = own_w[i] * (own_d[i] - (p.normalize ? inner : 0.0f));
+      for (int jl = 0; jl < L && i * L + jl < k; ++jl) {  // slot by slot to the lane that holds its expert
+        const int from = (lane & ~(L - 1)) + jl;
+        const float add = L == 1 ? own_add : __shfl(own_add, from, 64);
+        const int at = (L == 1 ? own_e[i] : __shfl(own_e[i], from, 64)) - c0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (at == v) dl[v] += add;
+      }
     }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) dl[v] = live ? dl[v] : 0.0f;
-  const int64_t at = r * E + lig * V;
+  const int64_t at = r * E + c0;
   if (p.vec) {
-    if (lig * V >= E) return;
-    if (p.fp32) {
+    if (c0 >= E) return;
+    if constexpr (FP32) {
       f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p.dlogits) + at);
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) q[i] = f32x4{dl[4 * i], dl[4 * i + 1], dl[4 * i + 2], dl[4 * i + 3]};
@@ -367,8 +456,8 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdParams p) {
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (lig * V + v < E) {
-        if (p.fp32) static_cast<float*>(p.dlogits)[at + v] = dl[v];
+      if (c0 + v < E) {
+        if constexpr (FP32) static_cast<float*>(p.dlogits)[at + v] = dl[v];
         else static_cast<uint16_t*>(p.dlogits)[at + v] = narrow(dl[v]);
       }
   }
@@ -641,7 +730,9 @@ hipError_t launch_route_fwd(const RouteParams& p, int threads, hipStream_t s) {
   const size_t sums = (waves * p.experts + p.experts + 4) * 4, shares = waves * 8;
   const size_t lds = sums > shares ? sums : shares;
   const dim3 g(p.blocks), b(threads);
-#define MDG_ROUTE(L, V) hipLaunchKernelGGL((route_fwd_kernel<L, V>), g, b, lds, s, p)
+#define MDG_ROUTE(L, V)                                                             \
+  if (p.fp32) hipLaunchKernelGGL((route_fwd_kernel<L, V, true>), g, b, lds, s, p); \
+  else hipLaunchKernelGGL((route_fwd_kernel<L, V, false>), g, b, lds, s, p)
   if (route_values(p.experts) == 16) {
     MDG_ROUTE(64, 16);
   } else {
@@ -666,7 +757,9 @@ hipError_t launch_route_fwd(const RouteParams& p, int threads, hipStream_t s) {
 hipError_t launch_route_bwd(const RouteBwdParams& p, hipStream_t s) {
   const int rows = 256 / route_lanes(p.experts);
   const dim3 g((unsigned)((p.tokens + rows - 1) / rows)), b(256);
-#define MDG_ROUTE(L, V) hipLaunchKernelGGL((route_bwd_kernel<L, V>), g, b, 0, s, p)
+#define MDG_ROUTE(L, V)                                                           \
+  if (p.fp32) hipLaunchKernelGGL((route_bwd_kernel<L, V, true>), g, b, 0, s, p); \
+  else hipLaunchKernelGGL((route_bwd_kernel<L, V, false>), g, b, 0, s, p)
   if (route_values(p.experts) == 16) {
     MDG_ROUTE(64, 16);
   } else {

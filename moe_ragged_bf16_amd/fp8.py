@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional, Union
 import torch
 
 from . import _capi, ops
-from .moe import _CODES, _call, _check, _entry, _need_float, _scratch
+from .moe import _CODES, _allocator, _call, _check, _entry, _need_float, _scratch
 from .ops import _need, _offs_ptr, _same_device, _workspace, _written
 
 __all__ = ["Fp8Rows", "Fp8Weight", "quantize_fp8_rows", "quantize_fp8_weight", "fp8_gemm_fwd_workspace_bytes",
@@ -47,8 +47,9 @@ def quantize_fp8_rows(x: torch.Tensor) -> Fp8Rows:
     """x [M, K] (bf16 or fp32; K a multiple of 16) in 8 bits."""
     code = _need_float(x, "x")
     M, K = x.shape
-    q = torch.empty((M, K), dtype=_E4M3, device=x.device)
-    scale = torch.empty((-(-_blocks(K) // 4), M, 4), dtype=_E8M0, device=x.device)
+    new = _allocator(x)
+    q = new((M, K), (K, 1), _E4M3)
+    scale = new((-(-_blocks(K) // 4), M, 4), (4 * M, 4, 1), _E8M0)
     _call("grouped_fp8_quantize_rows", x, x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), M, K)
     return Fp8Rows(q, scale)
 
@@ -63,12 +64,13 @@ def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weigh
         raise TypeError("transpose must be a bool")
     _need(w, "w", w.dtype, 3)
     E, N, K = w.shape
-    q = torch.empty((E, N, K), dtype=_E4M3, device=w.device)
-    scale = torch.empty((E, _blocks(N), _blocks(K)), dtype=_E8M0, device=w.device)
+    new, nb, kb = _allocator(w), _blocks(N), _blocks(K)
+    q = new((E, N, K), (N * K, K, 1), _E4M3)
+    scale = new((E, nb, kb), (nb * kb, kb, 1), _E8M0)
     qt = scale_t = None
     if transpose:
-        qt = torch.empty((E, K, N), dtype=_E4M3, device=w.device)
-        scale_t = torch.empty((E, _blocks(K), _blocks(N)), dtype=_E8M0, device=w.device)
+        qt = new((E, K, N), (N * K, N, 1), _E4M3)
+        scale_t = new((E, kb, nb), (nb * kb, nb, 1), _E8M0)
     _call("grouped_fp8_quantize_weight", w, w.data_ptr(), _CODES[w.dtype], q.data_ptr(), scale.data_ptr(),
           qt.data_ptr() if transpose else 0, scale_t.data_ptr() if transpose else 0, E, N, K)
     return Fp8Weight(q, scale, qt, scale_t)
@@ -107,19 +109,19 @@ def grouped_fp8_gemm_fwd(x: Union[torch.Tensor, Fp8Rows], wq: torch.Tensor, w_sc
     _check(w_scale, "w_scale", _E8M0, 3, q)
     if tuple(w_scale.shape) != (E, _blocks(N), _blocks(K)):
         raise ValueError(f"w_scale must have shape {(E, _blocks(N), _blocks(K))}")
-    given = out is not None
+    given, new = out is not None, _allocator(q)
     if given:
         _check(out, "out", torch.bfloat16, 2, q)
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must have shape {(M, N)}")
     else:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=q.device)
+        out = new((M, N), (N, 1), torch.bfloat16)
     op = _offs_ptr(offs, E)
     if offs.get_device() != q.get_device():
         _same_device(q, offs)
     need = _entry("grouped_fp8_gemm_fwd_workspace_bytes")(M, N, K, E, code)
     if workspace is None:
-        ws, wp = _scratch(need, q.device)
+        ws, wp = _scratch(new, need)
     else:
         ws = _workspace(workspace, need, q.device)
         _same_device(q, ws)

@@ -24,6 +24,11 @@ from .ops import _need, _same_device
 __all__ = ["MoeRoute", "MoePlan", "moe_route", "moe_route_fwd", "moe_route_bwd", "moe_plan", "moe_dispatch",
            "moe_dispatch_fwd", "moe_dispatch_bwd", "moe_combine", "moe_combine_fwd", "moe_combine_bwd"]
 
+try:  # the allocation torch's own compiled programs make: half the host time of torch.empty
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:  # pragma: no cover
+    _empty_strided_cuda = None
+
 _CODES = {torch.bfloat16: _capi.MDG_BF16, torch.float32: _capi.MDG_FP32}
 
 
@@ -59,6 +64,13 @@ def _need_float(t: torch.Tensor, name: str) -> int:
     return code
 
 
+def _allocator(like: torch.Tensor):
+    """f(size, stride, dtype): an uninitialised tensor on like's device."""
+    if _empty_strided_cuda is not None and like.get_device() == torch.cuda.current_device():
+        return _empty_strided_cuda
+    return lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device=like.device)
+
+
 _entries = {}
 
 
@@ -81,11 +93,11 @@ def _call(name: str, t: torch.Tensor, *args) -> None:
         _capi.check(name, st)
 
 
-def _scratch(need: int, device) -> Tuple[Optional[torch.Tensor], int]:
+def _scratch(new, need: int) -> Tuple[Optional[torch.Tensor], int]:
     """A workspace of `need` bytes (kept alive by the caller until the launch) and its address."""
     if need == 0:
         return None, 0
-    t = torch.empty(need, dtype=torch.uint8, device=device)
+    t = new((need,), (1,), torch.uint8)
     return t, t.data_ptr()
 
 
@@ -122,14 +134,14 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, *, normalize: bool = True,
         if token_mask.shape[0] != T:
             raise ValueError(f"token_mask must have {T} entries")
         mask = token_mask.data_ptr()
-    dev = logits.device
-    weight = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    balance = torch.empty(E, dtype=torch.float32, device=dev)
+    new = _allocator(logits)
+    weight = new((T, top_k), (top_k, 1), torch.float32)
+    idx = new((T, top_k), (top_k, 1), torch.int32)
+    counts = new((E,), (1,), torch.int32)
+    loss = new((), (), torch.float32)
+    balance = new((E,), (1,), torch.float32)
     need = _entry("moe_route_fwd_workspace_bytes")(T, E)
-    ws, wp = _scratch(need, dev)
+    ws, wp = _scratch(new, need)
     _call("moe_route_fwd", logits, logits.data_ptr(), code, mask, weight.data_ptr(), idx.data_ptr(), counts.data_ptr(),
           loss.data_ptr(), balance.data_ptr(), T, E, top_k, normalize, wp, need)
     return MoeRoute(weight, idx, counts, loss, balance)
@@ -158,7 +170,7 @@ def moe_route_bwd(dweight: Optional[torch.Tensor], dloss: Optional[torch.Tensor]
     if dloss is not None:
         _check(dloss, "dloss", torch.float32, 0, logits)
         dl = dloss.data_ptr()
-    out = torch.empty_like(logits)
+    out = _allocator(logits)((T, E), (E, 1), logits.dtype)
     _call("moe_route_bwd", logits, logits.data_ptr(), code, route.weight.data_ptr(), route.idx.data_ptr(),
           route.balance.data_ptr(), dw, dl, out.data_ptr(), T, E, k, int(normalize))
     return out
@@ -202,11 +214,11 @@ def moe_plan(idx: torch.Tensor, num_experts: int) -> MoePlan:
     T, k = idx.shape
     if k < 1 or num_experts < 1:
         raise ValueError("idx needs at least one column and num_experts at least one expert")
-    dev = idx.device
-    offs = torch.empty(num_experts, dtype=torch.int32, device=dev)
-    dest = torch.empty((T, k), dtype=torch.int32, device=dev)
+    new = _allocator(idx)
+    offs = new((num_experts,), (1,), torch.int32)
+    dest = new((T, k), (k, 1), torch.int32)
     need = _entry("moe_plan_workspace_bytes")(T, k, num_experts)
-    ws, wp = _scratch(need, dev)
+    ws, wp = _scratch(new, need)
     _call("moe_plan", idx, idx.data_ptr(), offs.data_ptr(), dest.data_ptr(), T, k, num_experts, wp, need)
     return MoePlan(offs, dest)
 
@@ -231,7 +243,7 @@ def moe_dispatch_fwd(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     T, k, E = _need_plan(plan, x)
     _need_rows(x, "x", T)
     H = x.shape[1]
-    rows = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    rows = _allocator(x)((T * k, H), (H, 1), x.dtype)
     _call("moe_dispatch_fwd", x, x.data_ptr(), plan.dest.data_ptr(), plan.offs.data_ptr(), rows.data_ptr(),
           T, k, E, H, code)
     return rows
@@ -243,7 +255,7 @@ def moe_dispatch_bwd(drows: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     T, k, _ = _need_plan(plan, drows)
     _need_rows(drows, "drows", T * k)
     H = drows.shape[1]
-    dx = torch.empty((T, H), dtype=drows.dtype, device=drows.device)
+    dx = _allocator(drows)((T, H), (H, 1), drows.dtype)
     _call("moe_dispatch_bwd", drows, drows.data_ptr(), plan.dest.data_ptr(), dx.data_ptr(), T, k, H, code)
     return dx
 
@@ -256,7 +268,7 @@ def moe_combine_fwd(y: torch.Tensor, weight: torch.Tensor, plan: MoePlan) -> tor
     _need_rows(y, "y", T * k)
     _need_weight(weight, y, T, k)
     H = y.shape[1]
-    out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+    out = _allocator(y)((T, H), (H, 1), y.dtype)
     _call("moe_combine_fwd", y, y.data_ptr(), weight.data_ptr(), plan.dest.data_ptr(), out.data_ptr(), T, k, H,
           code)
     return out
@@ -280,8 +292,9 @@ def moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor,
     _check(dout, "dout", y.dtype, 2, y)
     if tuple(dout.shape) != (T, H):
         raise ValueError(f"dout must have shape {(T, H)}")
-    dy = torch.empty_like(y)
-    dweight = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    new = _allocator(y)
+    dy = new((T * k, H), (H, 1), y.dtype)
+    dweight = new((T, k), (k, 1), torch.float32)
     _call("moe_combine_bwd", y, dout.data_ptr(), y.data_ptr(), weight.data_ptr(), plan.dest.data_ptr(),
           plan.offs.data_ptr(), dy.data_ptr(), dweight.data_ptr(), T, k, E, H, code)
     return dy, dweight
