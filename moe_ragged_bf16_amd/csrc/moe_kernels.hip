@@ -84,50 +84,22 @@ struct LogitBits {
 // routing
 // ---------------------------------------------------------------------------
 // An order-preserving integer of a logit: -0 and +0 are equal, NaN is above
-// everything.  -inf, an expert that cannot be chosen, is kKeyNone or (bf16) below.
+// everything.  -inf, an expert that cannot be chosen, is kKeyNone or (bf16) a little
+// below; a chosen expert's key becomes its slot's number + 1, far below.
 constexpr uint32_t kKeyNone = 0x007fffffu;
 
 __device__ __forceinline__ uint32_t key_of(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);
   if (f != f) return 0xffffffffu;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
-// One round of the top-k: the largest key left in the group's V keys a lane, the
-// lowest expert among equal ones.  A bf16 key leaves the lower 16 bits free for the
-// expert's complement, so its maximum is the choice; fp32 takes the maximum of the
-// keys, then the lowest column that has it.  The chosen key is cleared.  Returns
-// the key (<= kKeyNone: nothing is left) and the expert.
-template <int L, int V, bool FP32>
-__device__ __forceinline__ uint32_t choose(uint32_t (&key)[V], int c0, int* expert) {
-  uint32_t best = key[0];
-#pragma unroll
-  for (int v = 1; v < V; ++v) best = max(best, key[v]);
-  const uint32_t top = group_max<L>(best);
-  if constexpr (FP32) {
-    uint32_t col = 0xffffu;
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == top) col = c0 + v;
-    col = 0xffffu - group_max<L>(0xffffu - col);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (c0 + v == (int)col) key[v] = 0u;
-    *expert = (int)col;
-    return top;
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (key[v] == top) key[v] = 0u;
-    *expert = (int)(0xffffu - (top & 0xffffu));
-    return top;
-  }
-}
-
-// The key of column c0 + v of a row.
+// The key of a column of a row.  A bf16 key leaves the lower 16 bits free for the
+// expert's complement, so keys differ and the largest is the choice, the lowest
+// expert among equal logits.
 template <bool FP32>
 __device__ __forceinline__ uint32_t choice_key(float f, int column) {
   const uint32_t k = key_of(f);
@@ -139,6 +111,53 @@ __device__ __forceinline__ float choice_value(uint32_t key) {
   if constexpr (FP32) return value_of(key);
   else return (key & 0xffff0000u) == 0xffff0000u ? __uint_as_float(0x7fc00000u)
                                                  : value_of((key & 0x80000000u) ? key & 0xffff0000u : key | 0xffffu);
+}
+
+// One round of the top-k over the V keys a lane of the group: the largest key becomes
+// slot + 1.  fp32 keys may be equal: where a wave has more hits than groups, the
+// lowest column of each group's is taken.  Returns the key (<= kKeyNone: the group has
+// nothing left, and no key was changed).
+template <int L, int V, bool FP32>
+__device__ __forceinline__ uint32_t choose(uint32_t (&key)[V], int c0, uint32_t slot) {
+  uint32_t best = key[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) best = max(best, key[v]);
+  const uint32_t top = group_max<L>(best);
+  const bool some = top > kKeyNone;
+  const uint32_t want = some ? top : 0xffffffffu;  // (no key of a group without a choice equals it)
+  if constexpr (FP32) {
+    int hits = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) hits += __popcll(__ballot(key[v] == want));
+    if (hits * L != __popcll(__ballot(some))) {
+      uint32_t col = 0xffffu;
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v)
+        if (key[v] == want) col = c0 + v;
+      col = 0xffffu - group_max<L>(0xffffu - col);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (key[v] == want && c0 + v == (int)col) key[v] = slot + 1;
+      return top;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) key[v] = key[v] == want ? slot + 1 : key[v];
+  return top;
+}
+
+// e^x for x <= 0, to about 1.5 units in the last place: 2^t with t = x log2(e) in two
+// parts (t rounded, and what rounding left, which enters by its first-order term).
+// Below -200 the result is 0; the clamp also keeps -inf - (-inf) out (and loses NaN).
+__device__ __forceinline__ float exp_nonpositive(float x) {
+  constexpr float kLog2e = 1.44269502162933349609375f;    // log2(e) rounded to fp32
+  constexpr float kLog2eLow = 1.925963033500011079e-08f;  // log2(e) - kLog2e
+  constexpr float kLn2 = 0.693147180559945309f;
+  x = fmaxf(x, -200.0f);
+  const float t = x * kLog2e;
+  const float rest = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
+  const float r = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(r, rest * kLn2, r);
 }
 
 // The balance loss from the sums of one expert: a = E c / (k Tr^2) is the
@@ -161,12 +180,14 @@ constexpr int own_slots() {
 }
 
 // L lanes hold a row, V consecutive logits each.  The top-k is k rounds of choose(),
-// in registers and DPP moves; the first round's value is the softmax maximum.
-// Each lane adds the probabilities of its columns over all rows of its block in
-// registers; the next row's logits load while a row is worked on.
+// in registers and DPP moves; the first round's value is the softmax maximum; lanes
+// that hold a chosen expert write its slot.  Each lane adds the probabilities of its
+// columns over all rows of its block in registers; the next row's logits load while
+// a row is worked on.  Memory and the launch bound it: 65536 rows of 128 fp32 logits,
+// top-4, take 17.2 us (12.3 us with one round in place of four); the library
+// exponential and passing each round's choice to the slot's lane made it 18.6 us.
 template <int L, int V, bool FP32>
 __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p) {
-  constexpr int kOwn = own_slots<L, V>();
   extern __shared__ uint8_t smem[];
   const int E = p.experts, k = p.top_k;
   const int waves = blockDim.x >> 6;
@@ -195,9 +216,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p)
     float l[V];
     uint32_t key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < V; ++v) {  // (columns past the last are -inf)
       l[v] = keep ? bits.value(v) : kNegInf;
-      key[v] = c0 + v < E ? choice_key<FP32>(l[v], c0 + v) : 0u;
+      key[v] = choice_key<FP32>(l[v], c0 + v);
     }
     const int64_t row = r;
     r += blockDim.x / L;
@@ -205,52 +226,44 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p)
       bits.load(p.logits, r, c0, E, p.vec != 0);
       keep = p.mask == nullptr || p.mask[r] != 0;
     }
-    uint32_t first = 0, own_key[kOwn];
-    int own_e[kOwn];
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      own_key[i] = 0u;
-      own_e[i] = -1;
-      for (int jl = 0; jl < L && i * L + jl < k; ++jl) {
-        int e;
-        const uint32_t top = choose<L, V, FP32>(key, c0, &e);
-        if (i == 0 && jl == 0) first = top;
-        if (lig == jl && top > kKeyNone) {
-          own_key[i] = top;
-          own_e[i] = e;
-        }
-      }
+    uint32_t first = 0;
+    int found = 0;
+    for (int j = 0; j < k; ++j) {
+      const uint32_t top = choose<L, V, FP32>(key, c0, (uint32_t)j);
+      if (j == 0) first = top;
+      found += top > kKeyNone;
     }
     const bool live = first > kKeyNone;
     const float big = live ? choice_value<FP32>(first) : 0.0f;
-    float ex[V], total = 0.0f;
+    const float poison = big < __builtin_inff() ? 0.0f : __uint_as_float(0x7fc00000u);  // NaN for a row with NaN or +inf
+    float ex[V], total = poison, chosen = poison;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      ex[v] = live ? expf(l[v] - big) : 0.0f;
-      if (c0 + v < E) total += ex[v];
+      ex[v] = exp_nonpositive(l[v] - big);
+      total += ex[v];
+      chosen += key[v] - 1u < (uint32_t)kRouteMaxTopK ? ex[v] : 0.0f;
     }
     total = group_sum<L>(total);
-    float own_x[kOwn], chosen = 0.0f;
+    if (p.normalize) chosen = group_sum<L>(chosen);
+    const float scale = 1.0f / (p.normalize ? chosen : total);
+    const int64_t slots = row * k;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      own_x[i] = own_e[i] >= 0 ? expf(choice_value<FP32>(own_key[i]) - big) : 0.0f;
-      chosen += own_x[i];
-    }
-    chosen = group_sum<L>(chosen);
-    const float by = p.normalize ? chosen : total;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const int j = i * L + lig;
-      if (j < k) {
-        p.weight[row * k + j] = live ? own_x[i] / by : 0.0f;
-        p.idx[row * k + j] = own_e[i];
-        if (own_e[i] >= 0) atomicAdd(&s_cnt[own_e[i]], 1);
+    for (int v = 0; v < V; ++v) {
+      const uint32_t j = key[v] - 1u;
+      if (j < (uint32_t)kRouteMaxTopK) {
+        p.weight[slots + j] = ex[v] * scale;
+        p.idx[slots + j] = c0 + v;
+        atomicAdd(&s_cnt[c0 + v], 1);
       }
+    }
+    for (int j = found + lig; j < k; j += L) {  // slots no expert is left for
+      p.weight[slots + j] = 0.0f;
+      p.idx[slots + j] = -1;
     }
     if (live) {
       const float inv = 1.0f / total;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += ex[v] * inv;
+      for (int v = 0; v < V; ++v) acc[v] = __builtin_fmaf(ex[v], inv, acc[v]);
       if (lig == 0) ++routed;
     }
   }
