@@ -64,6 +64,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed building %s" % LIB_NAME)
     try:
         check_no_packed_fp32(tmp)
+        check_mfma_sources(tmp)
     except Exception:
         os.unlink(tmp)
         raise
@@ -72,21 +73,32 @@ def build(verbose: bool = False) -> str:
 
 
 def device_assembly(lib_path: str = LIB_PATH) -> str:
-    """AMD assembly of the gfx950 code object built into `lib_path` (its
-    .hip_fatbin section, unbundled and disassembled with ROCm's LLVM tools)."""
+    """AMD assembly of the gfx950 code objects built into `lib_path` (its
+    .hip_fatbin section holds one bundle for each source file; each is unbundled
+    and disassembled with ROCm's LLVM tools)."""
+    magic = b"__CLANG_OFFLOAD_BUNDLE__"
+
+    def run(what, *cmd):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("%s failed: %s" % (what, res.stderr))
+        return res.stdout
+
     with tempfile.TemporaryDirectory() as d:
         fat = os.path.join(d, "fatbin.bin")
-        co = os.path.join(d, "gfx950.co")
-        for cmd in ([os.path.join(LLVM_BIN, "llvm-objcopy"), "--dump-section", ".hip_fatbin=" + fat, lib_path],
-                    [os.path.join(LLVM_BIN, "clang-offload-bundler"), "--unbundle", "--type=o", "--input=" + fat,
-                     "--targets=" + DEVICE_TARGET, "--output=" + co]):
-            res = subprocess.run(cmd, capture_output=True, text=True)
-            if res.returncode != 0:
-                raise RuntimeError("extracting the gfx950 code object failed: " + res.stderr)
-        res = subprocess.run([os.path.join(LLVM_BIN, "llvm-objdump"), "-d", co], capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError("llvm-objdump failed: " + res.stderr)
-        return res.stdout
+        run("extracting the device code", os.path.join(LLVM_BIN, "llvm-objcopy"), "--dump-section",
+            ".hip_fatbin=" + fat, lib_path)
+        with open(fat, "rb") as f:
+            bundles = f.read().split(magic)[1:]
+        out = []
+        for i, bundle in enumerate(bundles):
+            one, co = os.path.join(d, "%d.bundle" % i), os.path.join(d, "%d.co" % i)
+            with open(one, "wb") as f:
+                f.write(magic + bundle)
+            run("extracting the gfx950 code object", os.path.join(LLVM_BIN, "clang-offload-bundler"), "--unbundle",
+                "--type=o", "--input=" + one, "--targets=" + DEVICE_TARGET, "--output=" + co)
+            out.append(run("llvm-objdump", os.path.join(LLVM_BIN, "llvm-objdump"), "-d", co))
+        return "".join(out)
 
 
 def check_no_packed_fp32(lib_path: str = LIB_PATH) -> int:
@@ -97,6 +109,51 @@ def check_no_packed_fp32(lib_path: str = LIB_PATH) -> int:
     if bad:
         raise RuntimeError("packed fp32 arithmetic in the gfx950 code: %d instructions, e.g. %s" % (len(bad), bad[0]))
     return sum(1 for ln in asm.splitlines() if "v_mfma" in ln)
+
+
+_REGS = re.compile(r"\b([va])(?:(\d+)\b|\[(\d+):(\d+)\])")
+
+
+def _registers(operand: str) -> set:
+    """The vector registers an operand names ({"v12", ...})."""
+    out = set()
+    for kind, one, first, last in _REGS.findall(operand):
+        out |= {kind + str(i) for i in range(int(one or first), int(one or last) + 1)}
+    return out
+
+
+def mfma_source_hazards(asm: str) -> list:
+    """Scaled matrix instructions of a disassembly with a source register that one
+    of the two instructions before wrote as a vector instruction (the hardware
+    needs two wait states there; the compiler adds them for its own instructions,
+    not around the asm statements of the 8-bit kernels)."""
+    bad, before = [], []           # before: (wait states, registers written, text) of the latest instructions
+    for line in asm.splitlines():
+        text = line.split("//")[0].strip()
+        m = re.match(r"([a-z]\w+)\s*(.*)", text)
+        if not m or text.endswith(":"):
+            before = []            # a label: another path may lead here, whose last instructions are its own
+            continue
+        name, args = m.group(1), m.group(2)
+        operands = re.split(r",\s*(?![^\[]*\])", args)
+        if name.startswith("v_mfma_scale"):
+            sources, states = set().union(*(_registers(o) for o in operands[1:])), 0
+            for waits, written, what in reversed(before):
+                if states >= 2:
+                    break
+                if written & sources:
+                    bad.append("%s; %s" % (what, text))
+                states += waits
+        valu = name.startswith("v_") and not name.startswith("v_mfma") and not name.startswith("v_cmp")
+        waits = 1 + (int(args, 0) if name == "s_nop" else 0)
+        before = before[-3:] + [(waits, _registers(operands[0]) if valu else set(), text)]
+    return bad
+
+
+def check_mfma_sources(lib_path: str = LIB_PATH) -> None:
+    bad = mfma_source_hazards(device_assembly(lib_path))
+    if bad:
+        raise RuntimeError("a matrix instruction too close behind a write of its source: %d, e.g. %s" % (len(bad), bad[0]))
 
 
 C_SMOKE_SRC = os.path.join(ROOT, "tests", "c_abi_smoke.cpp")

@@ -197,12 +197,14 @@ __device__ __forceinline__ uint8_t* buf_b() {
   else return s_b1;
 }
 
-// acc += b^T a under the scales in byte S of sb and sa.  (The leading s_nop
-// covers the two wait states between a VALU write of a source and its use, which
-// the compiler does not see inside an asm statement; the matrix pipe is busy with
-// the previous product meanwhile.)
-#define MDG_MFMA(REGS, SEL)                                                                                  \
-  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL : REGS(c) : "v"(b), "v"(a), \
+// c += b^T a under the scales in byte S of sb and sa.  Written as asm so that the
+// tile kernel's 256 accumulators stay in AGPRs, in place.  The compiler does not see
+// that a source written by a vector instruction needs two wait states before its
+// use here: operands come from LDS (which it waits for), and scales through
+// settle().  The build checks the generated code for it.  (An s_nop in front of each
+// product cost 2 %.)
+#define MDG_MFMA(REGS, SEL)                                                                            \
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL : REGS(c) : "v"(b), "v"(a), \
                "v"(sb), "v"(sa))
 #define MDG_MFMA_BYTE(REGS)                                              \
   if constexpr (S == 0) MDG_MFMA(REGS, "op_sel_hi:[0,0,0]");             \
@@ -220,6 +222,14 @@ __device__ __forceinline__ void mfma_scaled_v(f32x4& c, const i32x8& b, const i3
 }
 #undef MDG_MFMA_BYTE
 #undef MDG_MFMA
+
+// The wait states between the moves of scales and the products that take them.
+template <int N>
+__device__ __forceinline__ void settle(uint32_t (&x)[N], uint32_t& w) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i]));
+  asm volatile("s_nop 1" : "+v"(w));
+}
 
 // Waits until all of this wave's LDS reads have returned.
 __device__ __forceinline__ void wait_lgkm() { __builtin_amdgcn_s_waitcnt(0xC07F); }  // lgkmcnt(0), the others at their most
@@ -503,6 +513,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
     const Fp8Unit nx = fp8_unit(p, s_end, s_uprefix, n_j, total, v + P, pipe.wj);
     Acc acc;
     zero(acc);
+    settle(sc.x, sc.w);
     int kt = 0;
     for (; kt + 4 <= nk; kt += 4) {
       pipe.step<0>(acc, al, ah, ahn, b, sc, sn, p, u, nx, kt);
@@ -510,6 +521,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
       pipe.step<2>(acc, al, ah, ahn, b, sc, sn, p, u, nx, kt + 2);
       pipe.step<3>(acc, al, ahn, ah, b, sc, sn, p, u, nx, kt + 3);
       sc = sn;
+      settle(sc.x, sc.w);
     }
     if (kt < nk) {
       pipe.step<0>(acc, al, ah, ahn, b, sc, sn, p, u, nx, kt);
@@ -819,11 +831,13 @@ __global__ __launch_bounds__(256, 2) void fp8_mid_kernel(Fp8GemmParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) sx[i] = nx[i];
       sw = nw;
+      settle(sx, sw);
     }
   };
   load_scales(sx, &sw, 0);
   load_stage(std::integral_constant<int, 0>{}, 0);
   load_stage(std::integral_constant<int, 1>{}, 1);
+  settle(sx, sw);
   int kt = 0;
   for (; kt + 4 <= nk; kt += 4) {
     step(std::integral_constant<int, 0>{}, kt);

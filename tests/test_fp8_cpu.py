@@ -131,3 +131,15 @@ def test_oracle_group_sums_by_hand():
     a[0, 1], a[1, 1], a[2, 8] = 2.0 ** -5, 2.0 ** -6, 2.0 ** -6
     a[3, 0], a[3, 1] = 0, 2.0 ** -6
     assert ref.group_sums(a, b).sum(axis=1).tolist() == [256 + 2.0 ** -5, 256, 256 + 2.0 ** -6, 2.0 ** -6]
+
+
+def test_matrix_instructions_keep_their_distance_from_writes_of_their_sources():
+    from moe_ragged_bf16_amd import build
+    mfma = "\tv_mfma_scale_f32_16x16x128_f8f6f4 a[0:3], v[8:15], v[16:23], a[0:3], v30, v31 op_sel_hi:[0,0,0]\n"
+    bad = lambda pre: build.mfma_source_hazards(pre + mfma)
+    assert bad("\tv_mov_b32_e32 v10, v1\n") and bad("\tv_lshrrev_b32_e32 v31, 8, v31\n\ts_nop 0\n")
+    assert bad("\tv_accvgpr_write_b32 a2, v1\n\tv_add_u32_e32 v40, v1, v2\n")
+    assert not bad("\tv_mov_b32_e32 v10, v1\n\ts_nop 1\n") and not bad("\tv_mov_b32_e32 v24, v10\n")
+    assert not bad("\tv_mov_b32_e32 v10, v1\n\tv_mov_b32_e32 v1, v2\n\ts_mov_b32 s0, s1\n")
+    assert not bad("\tds_read_b128 v[8:11], v1\n\ts_waitcnt lgkmcnt(0)\n")
+    build.check_mfma_sources(build.LIB_PATH)
