@@ -378,8 +378,11 @@ MDG_API mdg_status moe_combine_bwd(const void* dout, const void* y, const float*
  * a NaN or an infinity has scale NaN and q NaN throughout.  Blocks at the end
  * of a row (k not a multiple of 128) hold what there is.
  *
- * Sizes: m_rows as above; n % 8 == 0 (n % 16 == 0 for a transposed weight);
- * k % 16 == 0; n, k <= 2^20, n * k < 2^31.
+ * Rows of 8-bit values (of q, and of q_t) lie at a pitch of their length rounded
+ * up to 16 bytes, with zeros behind the values.
+ *
+ * Sizes: m_rows as above; n % 8 == 0; k % 8 == 0; n, k <= 2^20, n * k (each rounded
+ * up to 16) < 2^31.
  *
  * grouped_fp8_quantize_rows: x [m_rows, k] of dtype (MDG_BF16 or MDG_FP32), read.
  *   q [m_rows, k], written.  scale, written: 32-bit words of four consecutive

@@ -30,14 +30,14 @@ int check_device(DeviceInfo* dev) {
 
 int check_rows(int64_t m_rows, int64_t k) {
   if (m_rows < 0 || k <= 0) return MDG_EINVAL;
-  if (k % kFp8KAlign != 0 || k > (1 << 20) || m_rows > kMaxRows) return MDG_EUNSUPPORTED;
+  if (k % kKAlign != 0 || k > (1 << 20) || m_rows > kMaxRows) return MDG_EUNSUPPORTED;
   return MDG_OK;
 }
 
 int check_weight(int32_t experts, int64_t n, int64_t k) {
   if (experts <= 0 || n <= 0 || k <= 0) return MDG_EINVAL;
-  if (experts > kMaxGroups || n % kNAlign != 0 || k % kFp8KAlign != 0) return MDG_EUNSUPPORTED;
-  if (n > (1 << 20) || k > (1 << 20) || n * k > INT32_MAX) return MDG_EUNSUPPORTED;
+  if (experts > kMaxGroups || n % kNAlign != 0 || k % kKAlign != 0) return MDG_EUNSUPPORTED;
+  if (n > (1 << 20) || k > (1 << 20) || fp8_pitch(n) * fp8_pitch(k) > INT32_MAX) return MDG_EUNSUPPORTED;
   return MDG_OK;
 }
 
@@ -48,7 +48,7 @@ struct XSpace {
 XSpace x_space(int64_t m_rows, int64_t k, int x_dtype) {
   XSpace w{0, 0};
   if (x_dtype == MDG_E4M3) return w;
-  w.scale_off = align256((size_t)(m_rows * k));
+  w.scale_off = align256((size_t)(m_rows * fp8_pitch(k)));
   w.total = align256(w.scale_off + (size_t)rows_scale_bytes(m_rows, k));
   return w;
 }
@@ -60,6 +60,7 @@ Fp8RowsParams rows_params(const void* x, int dtype, void* q, void* scale, int64_
   p.scale = static_cast<uint8_t*>(scale);
   p.m_rows = m_rows;
   p.k = (int32_t)k;
+  p.pitch = (int32_t)fp8_pitch(k);
   p.blocks = (int32_t)blocks_of(k);
   p.fp32 = dtype == MDG_FP32;
   return p;
@@ -80,7 +81,7 @@ MDG_API mdg_status grouped_fp8_quantize_rows(const void* x, int dtype, void* q, 
   if (st != MDG_OK) return status(st);
   if (!real_dtype(dtype) || (m_rows > 0 && (!x || !q || !scale))) return status(MDG_EINVAL);
   if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return status(MDG_EINVAL);
-  const Range rx = range_of(x, m_rows * k * dtype_bytes(dtype)), rq = range_of(q, m_rows * k);
+  const Range rx = range_of(x, m_rows * k * dtype_bytes(dtype)), rq = range_of(q, m_rows * fp8_pitch(k));
   const Range rs = range_of(scale, rows_scale_bytes(m_rows, k));
   if (overlaps(rq, rx) || overlaps(rs, rx) || overlaps(rq, rs)) return status(MDG_EOVERLAP);
   if (m_rows == 0) return status(MDG_OK);
@@ -96,11 +97,11 @@ MDG_API mdg_status grouped_fp8_quantize_weight(const void* w, int dtype, void* q
   int st = check_weight(num_groups, n, k);
   if (st != MDG_OK) return status(st);
   if (!real_dtype(dtype) || !w || !q || !scale || !q_t != !scale_t) return status(MDG_EINVAL);
-  if (q_t && n % kFp8KAlign != 0) return status(MDG_EUNSUPPORTED);
   if (!aligned16(w) || !aligned16(q) || !aligned16(q_t)) return status(MDG_EINVAL);
   const int64_t values = num_groups * n * k, scales = num_groups * blocks_of(n) * blocks_of(k);
   const Range in = range_of(w, values * dtype_bytes(dtype));
-  const Range out[4] = {range_of(q, values), range_of(scale, scales), range_of(q_t, q_t ? values : 0),
+  const Range out[4] = {range_of(q, num_groups * n * fp8_pitch(k)), range_of(scale, scales),
+                        range_of(q_t, q_t ? num_groups * k * fp8_pitch(n) : 0),
                         range_of(scale_t, scale_t ? scales : 0)};
   for (int i = 0; i < 4; ++i) {
     if (overlaps(out[i], in)) return status(MDG_EOVERLAP);
@@ -118,6 +119,8 @@ MDG_API mdg_status grouped_fp8_quantize_weight(const void* w, int dtype, void* q
   p.experts = num_groups;
   p.n = (int32_t)n;
   p.k = (int32_t)k;
+  p.pitch = (int32_t)fp8_pitch(k);
+  p.pitch_t = (int32_t)fp8_pitch(n);
   p.fp32 = dtype == MDG_FP32;
   return launched(launch_fp8_quantize_weight(p, static_cast<hipStream_t>(stream)));
 }
@@ -146,9 +149,9 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
     if (!workspace || workspace_bytes < xs.total) return status(MDG_EWORKSPACE);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return status(MDG_EINVAL);
   }
-  const Range in[5] = {range_of(x, m_rows * k * dtype_bytes(x_dtype)),
+  const Range in[5] = {range_of(x, m_rows * (quantized ? fp8_pitch(k) : k) * dtype_bytes(x_dtype)),
                        range_of(x_scale, quantized ? rows_scale_bytes(m_rows, k) : 0),
-                       range_of(w, num_groups * n * k),
+                       range_of(w, num_groups * n * fp8_pitch(k)),
                        range_of(w_scale, num_groups * blocks_of(n) * blocks_of(k)),
                        range_of(offs, (int64_t)num_groups * 4)};
   const Range ry = range_of(y, m_rows * n * 2), rws = range_of(workspace, (int64_t)xs.total);
@@ -169,7 +172,7 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
   p.y = static_cast<uint16_t*>(y);
   p.m_rows = m_rows;
   p.n = (int32_t)n;
-  p.k = (int32_t)k;
+  p.k = (int32_t)fp8_pitch(k);
   p.num_groups = num_groups;
   p.blocks = (int32_t)blocks_of(k);
   const int64_t active = std::min<int64_t>(num_groups, m_rows);  // groups with rows, at most

@@ -11,31 +11,34 @@ constexpr int kFp8Block = 128;   // values that share a scale along a row (weigh
 constexpr int kFp8SmallRows = 64; // rows of a unit of the small kernel
 constexpr int kFp8FewRows = 16;   // rows a group on average up to which the small kernel takes a launch alone
 constexpr int kFp8MidTile = 128;  // rows and columns of a unit of the middle kernel
-constexpr int kFp8KAlign = 16;   // k is a multiple of this: rows of whole 16-byte chunks
+
+// Rows of 8-bit values lie at a pitch of whole 16-byte chunks, zeros behind k.
+inline int64_t fp8_pitch(int64_t k) { return (k + 15) / 16 * 16; }
 
 // Scales of rows: e8m0 codes, four consecutive blocks of a row to a 32-bit word,
 // word [block / 4][row].
 struct Fp8RowsParams {
   const void* x;      // [m_rows, k] bf16 or fp32
-  uint8_t* q;         // [m_rows, k] e4m3
+  uint8_t* q;         // [m_rows, pitch] e4m3
   uint8_t* scale;     // [ceil(blocks / 4)][m_rows][4]
   int64_t m_rows;
-  int32_t k, blocks;  // blocks = ceil(k / 128)
+  int32_t k, pitch, blocks;  // blocks = ceil(k / 128)
   int32_t fp32;
 };
 
 struct Fp8WeightParams {
   const void* w;      // [experts, n, k] bf16 or fp32
-  uint8_t* q;         // [experts, n, k]
+  uint8_t* q;         // [experts, n, pitch]
   uint8_t* scale;     // [experts, ceil(n / 128), ceil(k / 128)]
-  uint8_t* qt;        // [experts, k, n] or nullptr
+  uint8_t* qt;        // [experts, k, pitch_t] or nullptr
   uint8_t* scale_t;   // [experts, ceil(k / 128), ceil(n / 128)]
   int32_t experts, n, k;
+  int32_t pitch, pitch_t;
   int32_t fp32;
 };
 
 struct Fp8GemmParams {
-  const uint8_t* x;       // [m_rows, k] e4m3
+  const uint8_t* x;       // [m_rows, k] e4m3, k the pitch
   const uint32_t* xs;     // [ceil(blocks / 4)][m_rows] words of 4 scales
   const uint8_t* w;       // [experts, n, k] e4m3
   const uint8_t* ws;      // [experts, ceil(n / 128), blocks]

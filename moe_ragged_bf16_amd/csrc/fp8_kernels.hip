@@ -53,14 +53,16 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
-// 16 consecutive values at p (bf16 or fp32, 16-byte aligned).
+// 16 consecutive values at p (bf16 or fp32, 16-byte aligned), of which `left` (a
+// multiple of 8) are there; zeros for the others.
 template <bool FP32>
-__device__ __forceinline__ void load16(float (&f)[16], const void* base, int64_t at) {
+__device__ __forceinline__ void load16(float (&f)[16], const void* base, int64_t at, int left) {
+  const bool whole = left >= 16;
   if constexpr (FP32) {
     const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f32x4 v = q[i];
+      const f32x4 v = i < 2 || whole ? q[i] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < 4; ++c) f[4 * i + c] = v[c];
     }
@@ -68,7 +70,7 @@ __device__ __forceinline__ void load16(float (&f)[16], const void* base, int64_t
     const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const u32x4 v = q[i];
+      const u32x4 v = i < 1 || whole ? q[i] : u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         f[8 * i + 2 * c] = __uint_as_float(v[c] << 16);
@@ -101,14 +103,14 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(Fp8RowsParams p) {
     float f[16];
     uint32_t m = 0;
     if (col < p.k) {
-      load16<FP32>(f, p.x, row * p.k + col);
+      load16<FP32>(f, p.x, row * p.k + col, p.k - col);
 #pragma unroll
       for (int i = 0; i < 16; ++i) m = max(m, magnitude(f[i]));
     }
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
     const uint32_t code = scale_code(m);
-    if (col < p.k) *reinterpret_cast<u32x4*>(p.q + row * p.k + col) = quantize16(f, code);
+    if (col < p.k) *reinterpret_cast<u32x4*>(p.q + row * p.pitch + col) = quantize16(f, code);
     uint8_t* s = p.scale + ((int64_t)(kb >> 2) * p.m_rows + row) * 4;
     if (l8 == 0) s[kb & 3] = (uint8_t)code;
     if (kb == p.blocks - 1 && l8 > (kb & 3) && l8 < 4) s[l8] = 0;  // the last word's unused scales
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(Fp8WeightParams p)
     const int row = bn * 128 + (t >> 3) + 32 * i;
 #pragma unroll
     for (int c = 0; c < 16; ++c) f[i][c] = 0.0f;
-    if (row < p.n && col < p.k) load16<FP32>(f[i], p.w, (e * p.n + row) * p.k + col);
+    if (row < p.n && col < p.k) load16<FP32>(f[i], p.w, (e * p.n + row) * p.k + col, p.k - col);
 #pragma unroll
     for (int c = 0; c < 16; ++c) m = max(m, magnitude(f[i][c]));
   }
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(Fp8WeightParams p)
   for (int i = 0; i < 4; ++i) {
     const int r = (t >> 3) + 32 * i, row = bn * 128 + r;
     const u32x4 q = quantize16(f[i], code);
-    if (row < p.n && col < p.k) *reinterpret_cast<u32x4*>(p.q + (e * p.n + row) * p.k + col) = q;
+    if (row < p.n && col < p.k) *reinterpret_cast<u32x4*>(p.q + (e * p.n + row) * p.pitch + col) = q;
     if constexpr (TRANSPOSE) *reinterpret_cast<u32x4*>(s_q + r * 144 + (t & 7) * 16) = q;
   }
   if constexpr (TRANSPOSE) {
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(Fp8WeightParams p)
         for (int b = 0; b < 4; ++b) v |= (uint32_t)s_q[((t & 7) * 16 + 4 * d + b) * 144 + c] << (8 * b);
         q[d] = v;
       }
-      if (k < p.k && n < p.n) *reinterpret_cast<u32x4*>(p.qt + (e * p.k + k) * p.n + n) = q;
+      if (k < p.k && n < p.n) *reinterpret_cast<u32x4*>(p.qt + (e * p.k + k) * p.pitch_t + n) = q;
     }
   }
 }

@@ -30,34 +30,55 @@ def _blocks(n: int) -> int:
     return -(-n // 128)
 
 
+def _new_q(new, *shape: int) -> torch.Tensor:
+    """8-bit values in rows at a pitch of whole 16 bytes (contiguous where the
+    row length is a multiple of 16)."""
+    pitch = -(-shape[-1] // 16) * 16
+    stride = (shape[-2] * pitch, pitch, 1)[3 - len(shape):]
+    q = new(shape[:-1] + (pitch,), stride, _E4M3)
+    return q if pitch == shape[-1] else q[..., :shape[-1]]
+
+
+def _check_q(t: torch.Tensor, name: str, ndim: int, like: Optional[torch.Tensor] = None) -> None:
+    """_check for 8-bit values laid out as by _new_q."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _E4M3 or t.dim() != ndim or t.shape[-1] % 16 == 0:
+        return _check(t, name, _E4M3, ndim, like)
+    pitch = -(-t.shape[-1] // 16) * 16
+    rows, stride = t.numel() // max(t.shape[-1], 1), (t.shape[-2] * pitch, pitch, 1)[3 - ndim:]
+    room = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+    if any(n > 1 and s != want for n, s, want in zip(t.shape, t.stride(), stride)) or room < rows * pitch:
+        raise ValueError(f"{name} must have its rows at a pitch of {pitch} bytes, zeros behind the values")
+    _check(t.as_strided(t.shape[:-1] + (pitch,), stride), name, _E4M3, ndim, like)
+
+
 class Fp8Rows(NamedTuple):
-    q: torch.Tensor                          # [M, K] float8_e4m3fn
+    q: torch.Tensor                          # [M, K] float8_e4m3fn; rows at a pitch of K rounded up to 16, zeros behind
     scale: torch.Tensor                      # [ceil(B / 4), M, 4] float8_e8m0fnu, B = ceil(K / 128): scale of block b of
                                              # row r at [b // 4, r, b % 4]
 
 
 class Fp8Weight(NamedTuple):
-    q: torch.Tensor                          # [E, N, K] float8_e4m3fn
+    q: torch.Tensor                          # [E, N, K] float8_e4m3fn, rows as in Fp8Rows
     scale: torch.Tensor                      # [E, ceil(N / 128), ceil(K / 128)] float8_e8m0fnu
     qt: Optional[torch.Tensor] = None        # [E, K, N]: q transposed (dgrad)
     scale_t: Optional[torch.Tensor] = None   # [E, ceil(K / 128), ceil(N / 128)]
 
 
 def quantize_fp8_rows(x: torch.Tensor) -> Fp8Rows:
-    """x [M, K] (bf16 or fp32; K a multiple of 16) in 8 bits."""
+    """x [M, K] (bf16 or fp32; K a multiple of 8) in 8 bits."""
     code = _need_float(x, "x")
     M, K = x.shape
     new = _allocator(x)
-    q = new((M, K), (K, 1), _E4M3)
+    q = _new_q(new, M, K)
     scale = new((-(-_blocks(K) // 4), M, 4), (4 * M, 4, 1), _E8M0)
     _call("grouped_fp8_quantize_rows", x, x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), M, K)
     return Fp8Rows(q, scale)
 
 
 def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weight:
-    """w [E, N, K] (bf16 or fp32; N a multiple of 8, K of 16) in 8 bits.
+    """w [E, N, K] (bf16 or fp32; N and K multiples of 8) in 8 bits.
     ``transpose``: also the transposed copy that ``grouped_fp8_gemm_dgrad``
-    reads (N a multiple of 16)."""
+    reads."""
     if not isinstance(w, torch.Tensor) or w.dtype not in _CODES:
         raise TypeError("w must be a bfloat16 or float32 tensor")
     if not isinstance(transpose, bool):
@@ -65,11 +86,11 @@ def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weigh
     _need(w, "w", w.dtype, 3)
     E, N, K = w.shape
     new, nb, kb = _allocator(w), _blocks(N), _blocks(K)
-    q = new((E, N, K), (N * K, K, 1), _E4M3)
+    q = _new_q(new, E, N, K)
     scale = new((E, nb, kb), (nb * kb, kb, 1), _E8M0)
     qt = scale_t = None
     if transpose:
-        qt = new((E, K, N), (N * K, N, 1), _E4M3)
+        qt = _new_q(new, E, K, N)
         scale_t = new((E, kb, nb), (nb * kb, nb, 1), _E8M0)
     _call("grouped_fp8_quantize_weight", w, w.data_ptr(), _CODES[w.dtype], q.data_ptr(), scale.data_ptr(),
           qt.data_ptr() if transpose else 0, scale_t.data_ptr() if transpose else 0, E, N, K)
@@ -92,7 +113,7 @@ def grouped_fp8_gemm_fwd(x: Union[torch.Tensor, Fp8Rows], wq: torch.Tensor, w_sc
     ``fp8_gemm_fwd_workspace_bytes()``) is allocated per call when not given."""
     xs_ptr = 0
     if isinstance(x, Fp8Rows):
-        _check(x.q, "x.q", _E4M3, 2)
+        _check_q(x.q, "x.q", 2)
         q, code = x.q, _capi.MDG_E4M3
         _check(x.scale, "x.scale", _E8M0, 3, q)
         if tuple(x.scale.shape) != (-(-_blocks(q.shape[1]) // 4), q.shape[0], 4):
@@ -102,7 +123,7 @@ def grouped_fp8_gemm_fwd(x: Union[torch.Tensor, Fp8Rows], wq: torch.Tensor, w_sc
         code = _need_float(x, "x")
         q = x
     M, K = q.shape
-    _check(wq, "wq", _E4M3, 3, q)
+    _check_q(wq, "wq", 3, q)
     E, N, K2 = wq.shape
     if K2 != K:
         raise ValueError(f"x has K={K} but wq has K={K2}")
@@ -173,7 +194,7 @@ def grouped_fp8_mm(x: torch.Tensor, w: torch.Tensor, offs: torch.Tensor, *,
     wgrad of this package (from x and G unquantised), in w's type.  Rows past
     offs[E-1] are zero.  ``w8``: ``quantize_fp8_weight(w, transpose=True)`` where
     the caller keeps it between steps; quantised by the call otherwise.  N and K
-    are multiples of 16."""
+    are multiples of 8."""
     _need(x, "x", torch.bfloat16, 2)
     _need(w, "w", torch.bfloat16, 3)
     if w8 is None:

@@ -324,3 +324,56 @@ def test_other_stream_and_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, run())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (3, 24, 136), (33, 136, 24), (200, 264, 1000), (70, 1000, 392), (9, 56, 2040)])
+def test_quantize_rows_that_end_inside_16_bytes(M, N, K, dtype):
+    """Rows at a pitch of 16 bytes, zeros behind the values."""
+    x, w = draw((M, K), M + K, dtype), draw((2, N, K), N + K, dtype)
+    r = mdg.quantize_fp8_rows(x)
+    q, c = ref.quantize_rows(h(x))
+    assert np.array_equal(row_codes(r, K), c) and np.array_equal(q_values(r.q), q)
+    w8 = mdg.quantize_fp8_weight(w, transpose=True)
+    q, c = ref.quantize_weight(h(w))
+    assert np.array_equal(codes(w8.scale), c) and np.array_equal(q_values(w8.q), q)
+    assert np.array_equal(codes(w8.scale_t), c.transpose(0, 2, 1))
+    assert np.array_equal(q_values(w8.qt), q.transpose(0, 2, 1))
+    for t in (r.q, w8.q, w8.qt):
+        n, pitch = t.shape[-1], -(-t.shape[-1] // 16) * 16
+        assert t.stride(-2) == pitch
+        whole = t.as_strided(t.shape[:-1] + (pitch,), t.stride()).view(torch.uint8)
+        assert torch.all(whole[..., n:] == 0)
+
+
+@pytest.mark.parametrize("sizes,N,K", [
+    ([1], 8, 8), ([0, 3, 1], 24, 136), ([9, 16], 1000, 1000), ([31, 33, 1], 264, 392), ([64, 65, 63], 520, 520),
+    ([300, 0, 700], 136, 1032), ([40, 900, 3], 776, 24), ([7, 520], 392, 2040), ([3000, 2000, 0, 5000], 2056, 648)])
+def test_product_and_dgrad_of_rows_that_end_inside_16_bytes(sizes, N, K):
+    M, E = int(np.sum(sizes)), len(sizes)
+    x, w, g = draw((M, K), 1, spread=False), draw((E, N, K), 2, spread=False), draw((M, N), 3, spread=False)
+    offs, w8, y = check_product(x, w, sizes)
+    assert torch.equal(mdg.grouped_fp8_gemm_fwd(mdg.quantize_fp8_rows(x), w8.q, w8.scale, offs), y)
+    t8 = mdg.quantize_fp8_weight(w, transpose=True)
+    wt = mdg.quantize_fp8_weight(w.transpose(1, 2).contiguous())
+    dx = mdg.grouped_fp8_gemm_dgrad(g, t8.qt, t8.scale_t, offs)
+    assert torch.equal(dx, mdg.grouped_fp8_gemm_fwd(g, wt.q, wt.scale, offs))
+    check_product(g, w.transpose(1, 2).contiguous(), sizes)
+    leaf = x.clone().requires_grad_()
+    mdg.grouped_fp8_mm(leaf, w, offs).backward(g)
+    assert torch.equal(leaf.grad, dx)
+
+
+def test_refuses_8_bit_rows_without_their_pitch():
+    x, w = draw((5, 24), 1, spread=False), draw((2, 16, 24), 2, spread=False)
+    offs = torch.tensor([2, 5], dtype=torch.int32, device=DEV)
+    w8, r = mdg.quantize_fp8_weight(w), mdg.quantize_fp8_rows(x)
+    with pytest.raises(ValueError, match="pitch of 32"):
+        mdg.grouped_fp8_gemm_fwd(x, w8.q.contiguous(), w8.scale, offs)
+    with pytest.raises(ValueError, match="pitch of 32"):
+        mdg.grouped_fp8_gemm_fwd(mdg.Fp8Rows(r.q.contiguous(), r.scale), w8.q, w8.scale, offs)
+    short = torch.empty(5 * 32 - 8, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn).as_strided((5, 24), (32, 1))
+    with pytest.raises(ValueError, match="pitch of 32"):
+        mdg.grouped_fp8_gemm_fwd(mdg.Fp8Rows(short, r.scale), w8.q, w8.scale, offs)
+    with pytest.raises(TypeError):
+        mdg.grouped_fp8_gemm_fwd(x, w, w8.scale, offs)
