@@ -66,7 +66,7 @@ def _need_float(t: torch.Tensor, name: str) -> int:
 
 def _allocator(like: torch.Tensor):
     """f(size, stride, dtype): an uninitialised tensor on like's device."""
-    if _empty_strided_cuda is not None and like.get_device() == torch.cuda.current_device():
+    if _empty_strided_cuda is not None and like.get_device() == torch._C._cuda_getDevice():
         return _empty_strided_cuda
     return lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device=like.device)
 
@@ -84,7 +84,7 @@ def _entry(name: str):
 def _call(name: str, t: torch.Tensor, *args) -> None:
     """Calls a library entry on t's device, with its current stream as the last argument."""
     index = t.get_device()
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         st = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):

@@ -377,3 +377,29 @@ def test_refuses_8_bit_rows_without_their_pitch():
         mdg.grouped_fp8_gemm_fwd(mdg.Fp8Rows(short, r.scale), w8.q, w8.scale, offs)
     with pytest.raises(TypeError):
         mdg.grouped_fp8_gemm_fwd(x, w, w8.scale, offs)
+
+
+@pytest.mark.parametrize("M,N,K", [(620_000, 136, 7176), (80_000, 32_776, 128)])
+def test_tensors_of_more_than_4_gib(M, N, K):
+    """x in 8 bits, then y, of more than 2^32 bytes: rows repeat with period P, so
+    outputs do within a group; a period's are checked against the oracle."""
+    P, split = 4096, M // 2 + 77
+    base, w = draw((P, K), 1, spread=False), draw((2, N, K), 2, spread=False)
+    x = base.repeat(-(-M // P), 1)[:M]
+    assert max(M * K, M * N * 2) > 2 ** 32
+    offs = torch.tensor([split, M], dtype=torch.int32, device=DEV)
+    w8 = mdg.quantize_fp8_weight(w)
+    y = mdg.grouped_fp8_gemm_fwd(x, w8.q, w8.scale, offs)
+    del x
+    for lo, hi in ((0, split), (split, M)):
+        for at in range(lo + P, hi, P):
+            n = min(P, hi - at)
+            assert torch.equal(y[at:at + n], y[lo:lo + n]), at
+    qw, cw = ref.quantize_weight(h(w))
+    wv = ref.dequantize(qw, cw, (128, 128))
+    for e, lo in ((0, 0), (1, split)):
+        rows = np.arange(lo, lo + P, 517)
+        qx, cx = ref.quantize_rows(h(base[torch.from_numpy(rows % P).to(DEV)]))
+        xv, one = ref.dequantize(qx, cx, (1, 128)), [len(rows)]
+        tol = (K + 8) * U * (np.abs(xv) @ np.abs(wv[e]).T) + group_bound(qx, cx, qw[e:e + 1], cw[e:e + 1], one)
+        assert inside(y[torch.from_numpy(rows).to(DEV)], xv @ wv[e].T, tol)

@@ -289,3 +289,41 @@ def test_other_stream_and_graph_replay():
         torch.cuda.synchronize()
         for a, b in zip(got, layer()):
             assert torch.equal(a, b)
+
+
+def test_rows_of_more_than_4_gib():
+    """Copies against indexing, sums at sampled tokens against fp64."""
+    T, k, E, H = 42_000, 8, 16, 7168
+    assert T * k * H * 2 > 2 ** 32
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    idx = torch.randint(-1, E, (T, k), generator=gen, device=DEV, dtype=torch.int32)
+    weight = torch.rand((T, k), generator=gen, device=DEV)
+    x = torch.randn((T, H), generator=gen, device=DEV, dtype=torch.bfloat16)
+    plan = mdg.moe_plan(idx, E)
+    have = plan.dest >= 0
+    assert torch.equal(have, idx >= 0) and int(plan.offs[-1]) == int(have.sum())
+    rows = mdg.moe_dispatch_fwd(x, plan)
+    for j in range(k):
+        t = have[:, j].nonzero()[:, 0]
+        assert torch.equal(rows[plan.dest[t, j].long()], x[t])
+    assert not rows[int(plan.offs[-1]):].any()
+
+    y = rows
+    out, dx = mdg.moe_combine_fwd(y, weight, plan), mdg.moe_dispatch_bwd(y, plan)
+    dy, dweight = mdg.moe_combine_bwd(x, y, weight, plan)
+    assert not dy[int(plan.offs[-1]):].any()
+    at = torch.cat([torch.arange(0, T, 691, device=DEV), torch.arange(T - 40, T, device=DEV)])
+    d, wt, xt = plan.dest[at], weight[at].double().cpu().numpy(), x[at].double().cpu().numpy()
+    real = (d >= 0).cpu().numpy()
+    ys = y[d.clamp(min=0).long()].double().cpu().numpy() * real[:, :, None]
+    terms = wt[:, :, None] * ys
+    assert inside(out[at], terms.sum(axis=1), (k + 2) * U * np.abs(terms).sum(axis=1))
+    assert inside(dx[at], ys.sum(axis=1), (k + 2) * U * np.abs(ys).sum(axis=1))
+    prod = xt[:, None, :] * ys
+    assert inside(dweight[at], prod.sum(axis=2), (H + 2) * U * np.abs(prod).sum(axis=2))
+    got = dy[d.clamp(min=0).long()]
+    want = (wt[:, :, None] * xt[:, None, :])
+    tol = 2 * U * np.abs(want)
+    got[~torch.from_numpy(real).to(DEV)] = 0
+    assert inside(got, want * real[:, :, None], tol * real[:, :, None])
