@@ -176,7 +176,6 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
   p.num_groups = num_groups;
   p.blocks = (int32_t)blocks_of(k);
   const int64_t active = std::min<int64_t>(num_groups, m_rows);  // groups with rows, at most
-  const bool few = m_rows <= kFp8FewRows * active;
   if (!quantized) {
     uint8_t* q = static_cast<uint8_t*>(workspace);
     if (launch_fp8_quantize_rows(rows_params(x, x_dtype, q, q + xs.scale_off, m_rows, k), s) != hipSuccess)
@@ -184,22 +183,29 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
     p.x = q;
     p.xs = reinterpret_cast<const uint32_t*>(q + xs.scale_off);
   }
-  // Groups of kFp8FewRows rows on average: the small kernel alone, a group of more
-  // rows than its units hold as several units.  Up to twice its units' rows on
-  // average: it takes the groups of at most one unit, the tile kernels the others.
-  // Above, groups that small are few and stay with the tile kernels.
-  if (few) return launched(launch_fp8_small(p, (int)(active + m_rows / kFp8SmallRows), INT32_MAX, s));
-  if (m_rows <= 2 * kFp8SmallRows * active) {
-    p.small_rows = kFp8SmallRows;
-    if (launch_fp8_small(p, (int)active, kFp8SmallRows, s) != hipSuccess) return status(MDG_EHIP);
-    if (m_rows <= kFp8SmallRows) return status(MDG_OK);  // no group has more rows
-  }
-  // Tiles of a size, at most: the whole row tiles and a partial one of every group.
-  const auto tiles = [&](int64_t tile) { return ((m_rows + tile - 1) / tile + active) * ((n + tile - 1) / tile); };
-  if (tiles(kFp8MidTile) > INT32_MAX) return status(MDG_EUNSUPPORTED);
   const int64_t cus = dev.cus > 0 ? dev.cus : 256;
-  if (tiles(kTileI) < 2 * cus) return launched(launch_fp8_mid(p, (int)(tiles(kFp8MidTile) + 7) / 8 * 8, s));
-  return launched(launch_fp8_gemm(p, (int)std::min(tiles(kTileI), cus), s));
+  // Pieces of a kernel's rows, at most: whole ones and a partial one of every group.
+  const auto pieces = [&](int64_t rows) { return (m_rows + rows - 1) / rows + active; };
+  const auto columns = [&](int64_t cols) { return (n + cols - 1) / cols; };
+  // Few rows: the weights are read at the memory's rate either way, and the small
+  // kernel starts and ends faster; with more rows it reads weights that the middle
+  // kernel would read once again, and x through the caches.  64 groups of 1536 x 2048,
+  // small against middle: 2 rows on average 33 / 40 us, 8 rows 44 / 44, 16 rows
+  // 51 / 44; where all its units run at once it gains at more rows: 1 group of
+  // 4096 x 4096, 128 rows 16 / 23, 200 rows 26 / 23; 16 of 1000 x 2000, 20 rows 12 / 15.
+  const int64_t small = active + m_rows / kFp8SmallRows;
+  if (m_rows <= 8 * active || (m_rows <= 128 * active && small * columns(kFp8SmallCols) <= 3 * cus))
+    return launched(launch_fp8_small(p, (int)small, s));
+  // The tile kernel where groups fill half a tile on average and its tiles (half of
+  // each group's last one, on average, is counted) 5/8 of the CUs.  Middle against
+  // tile: 64 groups of 1536 x 2048, 96 rows on average 57 / 65 us, 128 rows 68 / 67, 512
+  // rows 159 / 129; 8 of 4096 x 4096, 128 rows (128 tiles) 48 / 57, 192 rows (160 tiles)
+  // 65 / 59, 384 rows 86 / 65.
+  const int64_t mid = (pieces(kFp8MidTile) * columns(kFp8MidTile) + 7) / 8 * 8;
+  const bool fits = mid * 256 <= UINT32_MAX;  // a launch's work-items; the tile kernel walks its tiles
+  if (fits && (m_rows < 128 * active || (m_rows / 128 + active) * columns(kTileJ) * 4 < 5 * cus))
+    return launched(launch_fp8_mid(p, (int)mid, s));
+  return launched(launch_fp8_gemm(p, (int)std::min(pieces(kTileI) * columns(kTileJ), cus), s));
 }
 
 }  // extern "C"

@@ -9,7 +9,7 @@ namespace mdg {
 
 constexpr int kFp8Block = 128;   // values that share a scale along a row (weights: 128 x 128)
 constexpr int kFp8SmallRows = 64; // rows of a unit of the small kernel
-constexpr int kFp8FewRows = 16;   // rows a group on average up to which the small kernel takes a launch alone
+constexpr int kFp8SmallCols = 32; // ... and columns
 constexpr int kFp8MidTile = 128;  // rows and columns of a unit of the middle kernel
 
 // Rows of 8-bit values lie at a pitch of whole 16-byte chunks, zeros behind k.
@@ -46,12 +46,11 @@ struct Fp8GemmParams {
   uint16_t* y;            // [m_rows, n] bf16
   int64_t m_rows;
   int32_t n, k, num_groups, blocks;
-  int32_t small_rows;     // groups of at most so many rows are the small kernel's, the others the tile kernel's
 };
 
 hipError_t launch_fp8_quantize_rows(const Fp8RowsParams& p, hipStream_t s);
 hipError_t launch_fp8_quantize_weight(const Fp8WeightParams& p, hipStream_t s);
-hipError_t launch_fp8_small(const Fp8GemmParams& p, int units, int most, hipStream_t s);
+hipError_t launch_fp8_small(const Fp8GemmParams& p, int pieces, hipStream_t s);
 hipError_t launch_fp8_mid(const Fp8GemmParams& p, int grid, hipStream_t s);
 hipError_t launch_fp8_gemm(const Fp8GemmParams& p, int grid, hipStream_t s);
 

@@ -430,8 +430,6 @@ __device__ __forceinline__ void store_tile(const Acc& acc, const OutTile& t, uin
 }
 
 // Thread t handles groups 4 t .. 4 t + 3: clamped ends and the prefix of units.
-// Groups the small kernel takes have none.
-template <int TILE>
 __device__ __forceinline__ int fp8_group_table(const Fp8GemmParams& p, int n_j, int* s_end, int* s_uprefix,
                                                int* scratch) {
   const int E = p.num_groups, M = (int)p.m_rows, t = threadIdx.x;
@@ -448,7 +446,7 @@ __device__ __forceinline__ int fp8_group_table(const Fp8GemmParams& p, int n_j, 
   for (int q = 0; q < 4; ++q) {
     const int end = max(before, endv[q]);
     const int rows = end - start;
-    units[q] = 4 * t + q < E && rows > p.small_rows ? (rows + TILE - 1) / TILE * n_j : 0;
+    units[q] = 4 * t + q < E ? (rows + kTileI - 1) / kTileI * n_j : 0;
     if (4 * t + q < E) s_end[4 * t + q] = end;
     sum += units[q];
     start = end;
@@ -495,7 +493,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
   __shared__ int s_uprefix[kMaxGroups + 1];
   __shared__ int s_scratch[4];
   const int n_j = (p.n + kTileJ - 1) / kTileJ;
-  const int total = uniform(fp8_group_table<kTileI>(p, n_j, s_end, s_uprefix, s_scratch));
+  const int total = uniform(fp8_group_table(p, n_j, s_end, s_uprefix, s_scratch));
   const int P = gridDim.x, bid = blockIdx.x;
   const int vb = (P % 8 == 0) ? (bid % 8) * (P / 8) + bid / 8 : bid;
   Fp8Pipe pipe;
@@ -559,22 +557,22 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
 // share the reduction out in pieces of 4 blocks (512 bytes of each weight row),
 // each wave loading weights straight from memory to registers, 16 KiB in flight at
 // once, without LDS or barriers; rows of x come from the caches.  The waves' sums
-// are added in wave order through LDS.  (Quantising bf16 rows in each wave instead
-// of a launch before took as long: 29.8 against 28.8 us for one token.)  Measured: 2 experts' 14336 x 4096 weights at 4.8 TB/s, 64 experts'
-// 1536 x 2048 at 4.9 TB/s (a large copy: 4.9).  (The non-temporal hint lost 7 %: a
-// lane group's two halves of a cache line are two loads.)
-constexpr int kSmallCols = 32;
+// are added in wave order through LDS.  The memory's rate bounds it: 2 experts'
+// 14336 x 4096 weights in 24 us, 4.8 TB/s, 64 experts' 1536 x 2048 (488 rows) in 40 us,
+// 4.9 TB/s (a large copy: 4.9).  (Quantising bf16 rows in each wave instead of a
+// launch before took as long: 29.8 against 28.8 us for one token.  The non-temporal
+// hint lost 7 %: a lane group's two halves of a cache line are two loads.)
+constexpr int kSmallCols = kFp8SmallCols;
 
-// Row pieces of TILE rows, group by group (groups of more than `most` rows, and of
-// at most `least`, have none).  A wave finds the piece that holds unit `slot` of
-// `per` units to a piece: expert, first row, rows, and the unit's number within
-// its group; returns the number of units, which slot reaches where there is none.
+// Row pieces of TILE rows, group by group.  A wave finds the piece that holds unit
+// `slot` of `per` units to a piece: expert, its first row and rows, and the unit's
+// number within its group; returns the number of units, which slot reaches where there is none.
 // (64 groups at a time with shuffles: no LDS, no barrier.)
 struct Piece {
   int e, start, rows, unit;
 };
 template <int TILE>
-__device__ __forceinline__ int find_piece(const Fp8GemmParams& p, int slot, int per, int least, int most, Piece* out) {
+__device__ __forceinline__ int find_piece(const Fp8GemmParams& p, int slot, int per, Piece* out) {
   const int lane = threadIdx.x & 63, E = p.num_groups, M = (int)p.m_rows;
   int carry = 0, before = 0;
   for (int base = 0; base < E; base += 64) {
@@ -583,7 +581,7 @@ __device__ __forceinline__ int find_piece(const Fp8GemmParams& p, int slot, int 
     int prev = __shfl_up(incl, 1, 64);
     if (lane == 0) prev = carry;
     const int m = incl - prev;
-    const int units = m > least && m <= most ? (m + TILE - 1) / TILE * per : 0;
+    const int units = (m + TILE - 1) / TILE * per;
     const int upto = before + wave_incl_sum(units);
     const uint64_t over = __ballot(slot < upto);
     if (over != 0 && slot >= before) {
@@ -712,10 +710,10 @@ __device__ __forceinline__ void small_unit(const Fp8GemmParams& p, int e, int ro
   small_store<MB>(p, row0, rows, n0, acc, s_acc);
 }
 
-__global__ __launch_bounds__(256, 3) void fp8_small_kernel(Fp8GemmParams p, int most) {
+__global__ __launch_bounds__(256, 3) void fp8_small_kernel(Fp8GemmParams p) {
   __shared__ f32x4 s_acc[kFp8SmallRows / 16 * 2 * 4 * 64];
   Piece u;
-  if ((int)blockIdx.y >= find_piece<kFp8SmallRows>(p, blockIdx.y, 1, 0, most, &u)) return;
+  if ((int)blockIdx.y >= find_piece<kFp8SmallRows>(p, blockIdx.y, 1, &u)) return;
   const int row0 = u.start + u.unit * kFp8SmallRows, rows = min(kFp8SmallRows, u.rows - u.unit * kFp8SmallRows);
   const int n0 = blockIdx.x * kSmallCols;
   if (rows <= 16) small_unit<1>(p, u.e, row0, rows, n0, s_acc);
@@ -726,7 +724,8 @@ __global__ __launch_bounds__(256, 3) void fp8_small_kernel(Fp8GemmParams p, int 
 // ---------------------------------------------------------------------------
 // the middle kernel: 128 x 128 tiles
 // ---------------------------------------------------------------------------
-// For launches whose 256 x 256 tiles would leave most CUs idle.  Four waves of
+// For groups too small for 256 x 256 tiles, or launches too small to fill the GPU
+// with them.  Four waves of
 // 64 x 64, the same stages and LDS layout as the tile kernel's at half the rows
 // (16 KiB an operand), two buffers, two workgroups to a CU, one of which computes
 // while the other waits.  A CU's stages then move 64 bytes per clock of matrix work,
@@ -751,10 +750,10 @@ __global__ __launch_bounds__(256, 2) void fp8_mid_kernel(Fp8GemmParams p) {
   // weights and rows), an eighth of them all.  The grid is an upper bound, so this
   // goes by the units there are: by the grid's size the first XCDs would get more.
   Piece u;
-  const int total = find_piece<kMidTile>(p, -1, n_j, p.small_rows, INT32_MAX, &u), share = (total + 7) / 8;
+  const int total = find_piece<kMidTile>(p, -1, n_j, &u), share = (total + 7) / 8;
   const int v = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= share || v >= total) return;
-  find_piece<kMidTile>(p, v, n_j, p.small_rows, INT32_MAX, &u);
+  find_piece<kMidTile>(p, v, n_j, &u);
   const int e = u.e, gs = u.start, gm = u.rows;
   int rt, ct;
   panel_order(u.unit, (gm + kMidTile - 1) / kMidTile, n_j, 4, &rt, &ct);
@@ -806,11 +805,9 @@ __global__ __launch_bounds__(256, 2) void fp8_mid_kernel(Fp8GemmParams p) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // Stage kt (S = kt % 4, buffer S % BUFS): wait for its loads (those of the next
-  // BUFS - 1, or 2 of 4 buffers', 8 each, follow them) and read its fragments.
-  // BUFS == 4: behind the barrier every wave is done with stage kt - 1, whose
-  // buffer takes stage kt + 3.  BUFS == 2: a second barrier after the reads frees
-  // stage kt's own buffer for stage kt + 2.
+  // Stage kt (S = kt % 4, buffer S % 2): wait for its loads (the next stage's 8
+  // follow them) and read its fragments; a second barrier after the reads frees its
+  // buffer for stage kt + 2.
   auto step = [&](auto number, int kt) {
     constexpr int S = decltype(number)::value, B = S & 1;
     wait_vm_lgkm<8>();
@@ -903,9 +900,9 @@ hipError_t launch_fp8_quantize_weight(const Fp8WeightParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_small(const Fp8GemmParams& p, int units, int most, hipStream_t s) {
-  const dim3 g((p.n + kSmallCols - 1) / kSmallCols, units), b(256);
-  hipLaunchKernelGGL(fp8_small_kernel, g, b, 0, s, p, most);
+hipError_t launch_fp8_small(const Fp8GemmParams& p, int pieces, hipStream_t s) {
+  const dim3 g((p.n + kSmallCols - 1) / kSmallCols, pieces), b(256);
+  hipLaunchKernelGGL(fp8_small_kernel, g, b, 0, s, p);
   return hipGetLastError();
 }
 

@@ -187,6 +187,14 @@ def test_product_of_many_tiles(E, rows, N, K):
     check_product(draw((int(sizes.sum()) + 5, K), 1, spread=False), draw((E, N, K), 2, spread=False), sizes, 5)
 
 
+@pytest.mark.parametrize("sizes,N,K", [
+    ([0] * 60 + [300], 264, 400), ([500] + [0] * 61 + [1], 40, 1100 // 8 * 8), ([0] * 30 + [65, 0, 1, 64, 33, 16, 17], 96, 2560),
+    ([0] * 300 + [2000], 8, 136), ([100, 28], 1000, 256), ([0, 0, 0, 191], 776, 640)])
+def test_one_large_group_among_empty_ones(sizes, N, K):
+    """Few rows on average, all in one group (several pieces of it)."""
+    check_product(draw((int(np.sum(sizes)) + 2, K), 1, spread=False), draw((len(sizes), N, K), 2, spread=False), sizes, 2)
+
+
 @pytest.mark.parametrize("sizes,N,K", [([40, 0, 300], 264, 400), ([7, 9], 128, 2048), ([20, 520], 384, 128)])
 def test_product_of_blocks_of_different_size(sizes, N, K):
     """Each block of 128 under a scale of its own, rows and weights alike."""
