@@ -81,9 +81,11 @@ def copy_calibration(mib: int) -> None:
 
 def kernel_source_digest() -> str:
     import hashlib
-    path = os.path.join(ROOT, "moe_ragged_bf16_amd", "csrc", "grouped_gemm_kernels.hip")
-    with open(path, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
+    digest = hashlib.sha256()
+    for name in ("grouped_gemm_kernels.hip", "kernel_common.h", "tile_epilogue.h"):
+        with open(os.path.join(ROOT, "moe_ragged_bf16_amd", "csrc", name), "rb") as f:
+            digest.update(f.read())
+    return digest.hexdigest()
 
 
 def measured_traffic(workload: str, kernel: str):
