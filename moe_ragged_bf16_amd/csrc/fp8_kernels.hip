@@ -496,12 +496,13 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& p, const int* s
 // largest 8-bit products here reach 3.1), 32768 over 64 experts' 1536 x 2048 116 us:
 // 1.78 PFLOP/s of the rows' own products, 2.2 with those of partly filled tiles.
 // What bounds it: a step's matrix work is 2048 cycles and it takes about 3200.  With
-// its loads left out the first takes 15 % less, with the fragments' LDS reads left
-// out 2 %, with all data zero (the clock then holds; the card's power limits it
-// otherwise, to about 1.9 of 2.4 GHz) 13 %.  Results that left between the products of
-// the steps around a unit's end, rather than behind its last one, gained nothing,
-// nor did tails of up to 128 rows given to the middle kernel (776 to 798 us, 132 to
-// 138: their weights are read once more).
+// its loads left out the first takes 15 % less, with loads that always hit the L2 7 %,
+// with the fragments' LDS reads left out 2 %, with all data zero (the clock then
+// holds; the card's power limits it otherwise, to about 1.9 of 2.4 GHz) 13 %.
+// Results that left between the products of the steps around a unit's end, rather
+// than behind its last one, gained nothing; tails of up to 128 rows given to the
+// middle kernel lost 3 to 5 % (their weights are read once more), and so did a half
+// tile for them here.
 __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) {
   __shared__ int s_end[kMaxGroups];
   __shared__ int s_uprefix[kMaxGroups + 1];
