@@ -98,7 +98,9 @@ def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weigh
 
 
 def fp8_gemm_fwd_workspace_bytes(m_rows: int, n: int, k: int, num_groups: int, x_dtype=torch.bfloat16) -> int:
-    code = _capi.MDG_E4M3 if x_dtype == _E4M3 else _CODES[x_dtype]
+    code = _capi.MDG_E4M3 if x_dtype == _E4M3 else _CODES.get(x_dtype)
+    if code is None:
+        raise TypeError(f"x_dtype must be bfloat16, float32 or float8_e4m3fn, got {x_dtype}")
     return int(_capi.load_library().grouped_fp8_gemm_fwd_workspace_bytes(m_rows, n, k, num_groups, code))
 
 

@@ -88,6 +88,9 @@ def test_binding_refusals():
         mdg.quantize_fp8_weight(w.double())
     with pytest.raises(TypeError):
         mdg.quantize_fp8_weight(w, transpose=1)
+    with pytest.raises(TypeError):
+        mdg.fp8_gemm_fwd_workspace_bytes(10, 32, 64, 2, torch.float64)
+    assert mdg.fp8_gemm_fwd_workspace_bytes(10, 32, 64, 2, torch.float8_e4m3fn) == 0
 
 
 def test_oracle_rounds_to_the_nearest_e4m3_value():
