@@ -148,3 +148,24 @@ def status_string(status: int) -> str:
 def check(entry: str, status: int) -> None:
     if status != MDG_OK:
         raise MdgError(entry, status, status_string(status))
+
+
+class _Native:
+    """The calls of binding.cpp (``native.plan(idx, num_experts)``, ...), bound
+    at the first use to the library's entries."""
+
+    def __getattr__(self, name: str):
+        import torch
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError(f"{_build.BINDING_PATH} is missing or does not load ({e}): build it first "
+                              "(python -m moe_ragged_bf16_amd.build)") from e
+        lib = load_library()
+        _binding.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _binding.entries()},
+                       torch._C._cuda_getCurrentRawStream, check)
+        self.__dict__.update({n: f for n, f in vars(_binding).items() if callable(f)})
+        return self.__dict__[name]
+
+
+native = _Native()

@@ -1,7 +1,8 @@
 """Ahead-of-time build of the gfx950 HIP library ``libmoe_ragged_bf16.so``.
 
 One ``hipcc`` invocation compiles the kernels and the C ABI for gfx950 only and
-links them into the package directory.  Run ``python -m moe_ragged_bf16_amd.build``.
+links them into the package directory; a C++ one compiles ``_binding.so``, the Python
+calls of the operators around the products.  Run ``python -m moe_ragged_bf16_amd.build``.
 """
 from __future__ import annotations
 
@@ -36,6 +37,9 @@ HIP_FLAGS = [
     # export only the entry points the public header marks MDG_API
     "-fvisibility=hidden",
 ]
+
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 LLVM_BIN = "/opt/rocm/llvm/bin"
 DEVICE_TARGET = "hipv4-amdgcn-amd-amdhsa--gfx950"
@@ -174,6 +178,30 @@ def build_c_smoke(verbose: bool = False) -> str:
     return C_SMOKE_BIN
 
 
+def build_binding(verbose: bool = False) -> str:
+    """Compile binding.cpp (host code only) against torch and return its path."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE]
+    for path in include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-I", path]
+    cmd += [BINDING_SRC, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+            "-ltorch", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("the C++ compiler failed building %s" % BINDING_PATH)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_binding(verbose=True))
     print(build_c_smoke(verbose=True))

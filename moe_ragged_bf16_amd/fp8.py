@@ -17,38 +17,13 @@ from typing import NamedTuple, Optional, Union
 import torch
 
 from . import _capi, ops
-from .moe import _CODES, _allocator, _call, _check, _entry, _need_float, _scratch
-from .ops import _need, _offs_ptr, _same_device, _workspace, _written
+from ._capi import native
+from .ops import _need
 
 __all__ = ["Fp8Rows", "Fp8Weight", "quantize_fp8_rows", "quantize_fp8_weight", "fp8_gemm_fwd_workspace_bytes",
            "grouped_fp8_gemm_fwd", "grouped_fp8_gemm_dgrad", "grouped_fp8_mm"]
 
-_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
-
-
-def _blocks(n: int) -> int:
-    return -(-n // 128)
-
-
-def _new_q(new, *shape: int) -> torch.Tensor:
-    """8-bit values in rows at a pitch of whole 16 bytes (contiguous where the
-    row length is a multiple of 16)."""
-    pitch = -(-shape[-1] // 16) * 16
-    stride = (shape[-2] * pitch, pitch, 1)[3 - len(shape):]
-    q = new(shape[:-1] + (pitch,), stride, _E4M3)
-    return q if pitch == shape[-1] else q[..., :shape[-1]]
-
-
-def _check_q(t: torch.Tensor, name: str, ndim: int, like: Optional[torch.Tensor] = None) -> None:
-    """_check for 8-bit values laid out as by _new_q."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _E4M3 or t.dim() != ndim or t.shape[-1] % 16 == 0:
-        return _check(t, name, _E4M3, ndim, like)
-    pitch = -(-t.shape[-1] // 16) * 16
-    rows, stride = t.numel() // max(t.shape[-1], 1), (t.shape[-2] * pitch, pitch, 1)[3 - ndim:]
-    room = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
-    if any(n > 1 and s != want for n, s, want in zip(t.shape, t.stride(), stride)) or room < rows * pitch:
-        raise ValueError(f"{name} must have its rows at a pitch of {pitch} bytes, zeros behind the values")
-    _check(t.as_strided(t.shape[:-1] + (pitch,), stride), name, _E4M3, ndim, like)
+_CODES = {torch.bfloat16: _capi.MDG_BF16, torch.float32: _capi.MDG_FP32, torch.float8_e4m3fn: _capi.MDG_E4M3}
 
 
 class Fp8Rows(NamedTuple):
@@ -66,39 +41,18 @@ class Fp8Weight(NamedTuple):
 
 def quantize_fp8_rows(x: torch.Tensor) -> Fp8Rows:
     """x [M, K] (bf16 or fp32; K a multiple of 8) in 8 bits."""
-    code = _need_float(x, "x")
-    M, K = x.shape
-    new = _allocator(x)
-    q = _new_q(new, M, K)
-    scale = new((-(-_blocks(K) // 4), M, 4), (4 * M, 4, 1), _E8M0)
-    _call("grouped_fp8_quantize_rows", x, x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), M, K)
-    return Fp8Rows(q, scale)
+    return Fp8Rows(*native.quantize_rows(x))
 
 
 def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weight:
     """w [E, N, K] (bf16 or fp32; N and K multiples of 8) in 8 bits.
     ``transpose``: also the transposed copy that ``grouped_fp8_gemm_dgrad``
     reads."""
-    if not isinstance(w, torch.Tensor) or w.dtype not in _CODES:
-        raise TypeError("w must be a bfloat16 or float32 tensor")
-    if not isinstance(transpose, bool):
-        raise TypeError("transpose must be a bool")
-    _need(w, "w", w.dtype, 3)
-    E, N, K = w.shape
-    new, nb, kb = _allocator(w), _blocks(N), _blocks(K)
-    q = _new_q(new, E, N, K)
-    scale = new((E, nb, kb), (nb * kb, kb, 1), _E8M0)
-    qt = scale_t = None
-    if transpose:
-        qt = _new_q(new, E, K, N)
-        scale_t = new((E, kb, nb), (nb * kb, nb, 1), _E8M0)
-    _call("grouped_fp8_quantize_weight", w, w.data_ptr(), _CODES[w.dtype], q.data_ptr(), scale.data_ptr(),
-          qt.data_ptr() if transpose else 0, scale_t.data_ptr() if transpose else 0, E, N, K)
-    return Fp8Weight(q, scale, qt, scale_t)
+    return Fp8Weight(*native.quantize_weight(w, transpose))
 
 
 def fp8_gemm_fwd_workspace_bytes(m_rows: int, n: int, k: int, num_groups: int, x_dtype=torch.bfloat16) -> int:
-    code = _capi.MDG_E4M3 if x_dtype == _E4M3 else _CODES.get(x_dtype)
+    code = _CODES.get(x_dtype)
     if code is None:
         raise TypeError(f"x_dtype must be bfloat16, float32 or float8_e4m3fn, got {x_dtype}")
     return int(_capi.load_library().grouped_fp8_gemm_fwd_workspace_bytes(m_rows, n, k, num_groups, code))
@@ -113,47 +67,8 @@ def grouped_fp8_gemm_fwd(x: Union[torch.Tensor, Fp8Rows], wq: torch.Tensor, w_sc
     offs as in ``grouped_det_gemm_fwd``; rows past offs[E-1] of a freshly
     allocated Y are left uninitialised.  ``workspace`` (uint8, at least
     ``fp8_gemm_fwd_workspace_bytes()``) is allocated per call when not given."""
-    xs_ptr = 0
-    if isinstance(x, Fp8Rows):
-        _check_q(x.q, "x.q", 2)
-        q, code = x.q, _capi.MDG_E4M3
-        _check(x.scale, "x.scale", _E8M0, 3, q)
-        if tuple(x.scale.shape) != (-(-_blocks(q.shape[1]) // 4), q.shape[0], 4):
-            raise ValueError("x.scale does not belong to x.q")
-        xs_ptr = x.scale.data_ptr()
-    else:
-        code = _need_float(x, "x")
-        q = x
-    M, K = q.shape
-    _check_q(wq, "wq", 3, q)
-    E, N, K2 = wq.shape
-    if K2 != K:
-        raise ValueError(f"x has K={K} but wq has K={K2}")
-    _check(w_scale, "w_scale", _E8M0, 3, q)
-    if tuple(w_scale.shape) != (E, _blocks(N), _blocks(K)):
-        raise ValueError(f"w_scale must have shape {(E, _blocks(N), _blocks(K))}")
-    given, new = out is not None, _allocator(q)
-    if given:
-        _check(out, "out", torch.bfloat16, 2, q)
-        if tuple(out.shape) != (M, N):
-            raise ValueError(f"out must have shape {(M, N)}")
-    else:
-        out = new((M, N), (N, 1), torch.bfloat16)
-    op = _offs_ptr(offs, E)
-    if offs.get_device() != q.get_device():
-        _same_device(q, offs)
-    need = _entry("grouped_fp8_gemm_fwd_workspace_bytes")(M, N, K, E, code)
-    if workspace is None:
-        ws, wp = _scratch(new, need)
-    else:
-        ws = _workspace(workspace, need, q.device)
-        _same_device(q, ws)
-        wp, need = ws.data_ptr(), ws.numel()
-    _call("grouped_fp8_gemm_fwd", q, q.data_ptr(), code, xs_ptr, wq.data_ptr(), w_scale.data_ptr(), op,
-          out.data_ptr(), M, N, K, E, wp, need)
-    if given:
-        _written(out)
-    return out
+    q, x_scale = x if isinstance(x, Fp8Rows) else (x, None)
+    return native.fp8_gemm_fwd(q, x_scale, wq, w_scale, offs, out, workspace)
 
 
 def grouped_fp8_gemm_dgrad(g: Union[torch.Tensor, Fp8Rows], wqt: torch.Tensor, w_scale_t: torch.Tensor,
