@@ -2,8 +2,8 @@
 // outputs and workspaces from torch's allocator, and the C entry on the tensors'
 // device and its current stream.  In C++ because a call is short: with the same
 // checks in Python and ctypes, three tokens' dispatch took 7.5 us of host time, of
-// which the launch is 3.4; here it takes 3.9 (plan 7.4 and 4.8, combine's gradient
-// 10.1 and 4.8).
+// which the launch is 3.4; here it takes 3.9 (plan 7.4 and 4.6, combine's gradient
+// 10.1 and 4.8, one token's route 9.3 and 4.9).
 //
 // The C entries are those of the library that the package has loaded; setup()
 // takes their addresses.
