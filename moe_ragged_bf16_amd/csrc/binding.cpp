@@ -184,6 +184,13 @@ struct Address {
 };
 Address ptr(const Tensor& t) { return Address{t.defined() ? t.data_ptr() : nullptr}; }
 
+[[noreturn]] void raise_status(const char* entry, int st) {
+  PyObject* r = PyObject_CallFunction(g_check, "si", entry, st);
+  if (r) PyErr_Format(PyExc_RuntimeError, "%s: status %d", entry, st);
+  Py_XDECREF(r);
+  throw Raised();
+}
+
 // Calls an entry on t's device with its current stream as the last argument.
 template <class F, class... A>
 void call(const char* name, F entry, const Tensor& t, A... a) {
@@ -199,12 +206,7 @@ void call(const char* name, F entry, const Tensor& t, A... a) {
   Py_BEGIN_ALLOW_THREADS
   st = (int)entry(a..., stream);
   Py_END_ALLOW_THREADS
-  if (st != MDG_OK) {
-    PyObject* r = PyObject_CallFunction(g_check, "si", name, st);
-    Py_XDECREF(r);
-    if (r) PyErr_Format(PyExc_RuntimeError, "%s: status %d", name, st);
-    throw Raised();
-  }
+  if (st != MDG_OK) raise_status(name, st);
 }
 
 template <class... T>
@@ -307,6 +309,7 @@ PyObject* plan(PyObject* const* a) {
   const int64_t E = integer(a[1], "num_experts"), T = idx.size(0), k = idx.size(1);
   if (k < 1 || E < 1)
     refuse(PyExc_ValueError, "idx needs at least one column and num_experts at least one expert");
+  if (E > (1 << 20)) raise_status("moe_plan", MDG_EUNSUPPORTED);  // (as the entry would, before offs of that size)
   const Parts<2> out(idx, {{{E}, ScalarType::Int}, {{T, k}, ScalarType::Int}});
   const auto& [offs, dest] = out.t;
   const size_t need = g.moe_plan_workspace_bytes(T, size32(k), size32(E));

@@ -411,3 +411,35 @@ def test_tensors_of_more_than_4_gib(M, N, K):
         xv, one = ref.dequantize(qx, cx, (1, 128)), [len(rows)]
         tol = (K + 8) * U * (np.abs(xv) @ np.abs(wv[e]).T) + group_bound(qx, cx, qw[e:e + 1], cw[e:e + 1], one)
         assert inside(y[torch.from_numpy(rows).to(DEV)], xv @ wv[e].T, tol)
+
+
+def test_binding_refusals_and_workspace():
+    x, w = draw((7, 256), 1, spread=False), draw((3, 64, 256), 2, spread=False)
+    offs = torch.tensor([2, 2, 7], dtype=torch.int32, device=DEV)
+    w8, r = mdg.quantize_fp8_weight(w), mdg.quantize_fp8_rows(x)
+    need = mdg.fp8_gemm_fwd_workspace_bytes(7, 64, 256, 3)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    want = mdg.grouped_fp8_gemm_fwd(x, w8.q, w8.scale, offs)
+    out = torch.empty_like(want)
+    assert mdg.grouped_fp8_gemm_fwd(x, w8.q, w8.scale, offs, out, ws) is out and out._version == 1
+    assert torch.equal(out, want)
+    fwd = mdg.grouped_fp8_gemm_fwd
+    for kind, match, f in (
+            (ValueError, "K=128 but wq has K=256", lambda: fwd(x[:, :128].contiguous(), w8.q, w8.scale, offs)),
+            (ValueError, "w_scale must have shape \\(3, 1, 2\\)", lambda: fwd(x, w8.q, w8.scale[:2], offs)),
+            (TypeError, "w_scale must be torch.float8_e8m0fnu", lambda: fwd(x, w8.q, w8.scale.view(torch.uint8), offs)),
+            (TypeError, "offs must be a 1-D int32 device tensor", lambda: fwd(x, w8.q, w8.scale, offs.long())),
+            (TypeError, "offs must be a 1-D int32 device tensor", lambda: fwd(x, w8.q, w8.scale, offs.cpu())),
+            (ValueError, "offs has 2 entries; expected E=3", lambda: fwd(x, w8.q, w8.scale, offs[:2])),
+            (ValueError, "out must have shape \\(7, 64\\)", lambda: fwd(x, w8.q, w8.scale, offs, out[:6])),
+            (TypeError, "out must be torch.bfloat16", lambda: fwd(x, w8.q, w8.scale, offs, out.float())),
+            (ValueError, "workspace too small", lambda: fwd(x, w8.q, w8.scale, offs, None, ws[:need - 1])),
+            (ValueError, "contiguous uint8", lambda: fwd(x, w8.q, w8.scale, offs, None, ws.view(torch.int8))),
+            (ValueError, "x.scale does not belong", lambda: fwd(mdg.Fp8Rows(r.q, r.scale[:, :5].contiguous()), w8.q, w8.scale, offs)),
+            (TypeError, "x.q must be torch.float8_e4m3fn", lambda: fwd(mdg.Fp8Rows(x, r.scale), w8.q, w8.scale, offs)),
+            (mdg.MdgError, "status 2", lambda: mdg.quantize_fp8_rows(x[:, :4].contiguous())),
+            (mdg.MdgError, "status 2", lambda: mdg.quantize_fp8_weight(w[:, :4].contiguous())),
+            (ValueError, "w must be 3-D", lambda: mdg.quantize_fp8_weight(w[0]))):
+        with pytest.raises(kind, match=match):
+            f()
+    torch.cuda.synchronize()

@@ -327,3 +327,65 @@ def test_rows_of_more_than_4_gib():
     tol = 2 * U * np.abs(want)
     got[~torch.from_numpy(real).to(DEV)] = 0
     assert inside(got, want * real[:, :, None], tol * real[:, :, None])
+
+
+def test_binding_refusals_on_the_device():
+    l = torch.randn((6, 8), device=DEV)
+    x = torch.randn((6, 64), device=DEV)
+    r = mdg.moe_route_fwd(l, 2)
+    plan = mdg.moe_plan(r.idx, 8)
+    y = mdg.moe_dispatch_fwd(x, plan)
+    other = mdg.moe_plan(r.idx[:5].contiguous(), 8)
+    mask = torch.ones(6, dtype=torch.bool, device=DEV)
+    strided = torch.randn((64, 6), device=DEV).t()
+    for kind, match, f in (
+            (ValueError, "top_k must be between 1", lambda: mdg.moe_route_fwd(l, 9)),
+            (ValueError, "top_k must be between 1", lambda: mdg.moe_route_fwd(l, 0)),
+            (TypeError, "top_k must be an int", lambda: mdg.moe_route_fwd(l, 2.0)),
+            (TypeError, "top_k must be an int", lambda: mdg.moe_route_fwd(l, True)),
+            (TypeError, "normalize must be a bool", lambda: mdg.moe_route_fwd(l, 2, normalize=1)),
+            (ValueError, "2-D, got shape \\(8,\\)", lambda: mdg.moe_route_fwd(l[0], 2)),
+            (ValueError, "6 entries", lambda: mdg.moe_route_fwd(l, 2, token_mask=mask[:5])),
+            (TypeError, "torch.bool, got torch.int32", lambda: mdg.moe_route_fwd(l, 2, token_mask=mask.int())),
+            (ValueError, "ROCm device", lambda: mdg.moe_route_fwd(l, 2, token_mask=mask.cpu())),
+            (ValueError, "contiguous", lambda: mdg.moe_route_fwd(l[:, ::2], 2)),
+            (ValueError, "does not belong", lambda: mdg.moe_route_bwd(r.weight, r.loss, l[:5], r)),
+            (ValueError, "dweight must have shape \\(6, 2\\)", lambda: mdg.moe_route_bwd(r.weight[:5], None, l, r)),
+            (ValueError, "dloss must be 0-D", lambda: mdg.moe_route_bwd(None, r.balance, l, r)),
+            (TypeError, "num_experts must be an int", lambda: mdg.moe_plan(r.idx, 8.0)),
+            (ValueError, "at least one", lambda: mdg.moe_plan(r.idx, 0)),
+            (mdg.MdgError, "status 2", lambda: mdg.moe_plan(r.idx, 5000)),
+            (OverflowError, None, lambda: mdg.moe_plan(r.idx, 1 << 70)),
+            (mdg.MdgError, "status 2", lambda: mdg.moe_plan(r.idx, 1 << 40)),
+            (TypeError, "torch.int32, got torch.int64", lambda: mdg.moe_plan(r.idx.long(), 8)),
+            (TypeError, "bfloat16 or float32, got torch.float64", lambda: mdg.moe_dispatch_fwd(x.double(), plan)),
+            (ValueError, "x must have 5 rows, got 6", lambda: mdg.moe_dispatch_fwd(x, other)),
+            (ValueError, "contiguous", lambda: mdg.moe_dispatch_fwd(strided, plan)),
+            (mdg.MdgError, "status 2", lambda: mdg.moe_dispatch_fwd(x[:, :3].contiguous(), plan)),
+            (ValueError, "drows must have 10 rows", lambda: mdg.moe_dispatch_bwd(y, other)),
+            (ValueError, "weight must have shape \\(6, 2\\)", lambda: mdg.moe_combine_fwd(y, r.weight[:5], plan)),
+            (TypeError, "weight must be torch.float32", lambda: mdg.moe_combine_fwd(y, r.weight.bfloat16(), plan)),
+            (TypeError, "dout must be torch.float32, got torch.bfloat16",
+             lambda: mdg.moe_combine_bwd(x.bfloat16(), y, r.weight, plan)),
+            (ValueError, "dout must have shape \\(6, 64\\)", lambda: mdg.moe_combine_bwd(x[:5], y, r.weight, plan))):
+        with pytest.raises(kind, match=match):
+            f()
+    assert isinstance(r, mdg.MoeRoute) and isinstance(plan, mdg.MoePlan)
+    torch.cuda.synchronize()
+
+
+def test_outputs_are_tensors_of_their_own():
+    """The small outputs share an allocation, not their values or versions."""
+    l = torch.randn((5, 3), device=DEV)
+    r = mdg.moe_route_fwd(l, 2)
+    kept = [t.clone() for t in r]
+    for i, t in enumerate(r):
+        assert t.data_ptr() % 256 == 0 and t.is_contiguous() and t._version == 0
+        t.fill_(1)
+        for j, u in enumerate(r):
+            assert torch.equal(u, kept[j]) or j <= i
+    assert [t._version for t in r] == [1] * 5
+    plan = mdg.moe_plan(r.idx, 3)
+    dest = plan.dest.clone()
+    plan.offs.zero_()
+    assert torch.equal(plan.dest, dest) and plan.dest._version == 0
