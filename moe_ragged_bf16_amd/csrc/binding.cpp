@@ -3,7 +3,9 @@
 // device and its current stream.  In C++ because a call is short: with the same
 // checks in Python and ctypes, three tokens' dispatch took 7.5 us of host time, of
 // which the launch is 3.4; here it takes 3.9 (plan 7.4 and 4.6, combine's gradient
-// 10.1 and 4.8, one token's route 9.3 and 4.9).
+// 10.1 and 4.8).  One token's route, whose five outputs are allocated one by one,
+// takes 7.4 (5.8 when they shared a storage, which their owner could then not
+// save or free one by one).
 //
 // The C entries are those of the library that the package has loaded; setup()
 // takes their addresses.
@@ -140,6 +142,7 @@ bool boolean(PyObject* o, const char* name) {
   return o == Py_True;
 }
 
+// A tensor with a storage of its own.
 Tensor fresh(const Tensor& like, at::IntArrayRef shape, ScalarType type) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
@@ -147,32 +150,6 @@ Tensor fresh(const Tensor& like, at::IntArrayRef shape, ScalarType type) {
 Tensor scratch(const Tensor& like, size_t bytes) {
   return bytes ? fresh(like, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
 }
-
-// Several small outputs in one allocation (each costs 0.5 us of host time), every
-// one at a multiple of 256 bytes: tensors of their own that share a storage.
-template <size_t N>
-struct Parts {
-  struct Part {
-    std::vector<int64_t> shape;
-    ScalarType type;
-  };
-  Tensor t[N];
-  Parts(const Tensor& like, const Part (&parts)[N]) {
-    int64_t at[N], bytes = 0;
-    for (size_t i = 0; i < N; ++i) {
-      at[i] = bytes;
-      bytes += (c10::multiply_integers(parts[i].shape) * (int64_t)c10::elementSize(parts[i].type) + 255) / 256 * 256;
-    }
-    const Tensor block = fresh(like, {bytes}, ScalarType::Byte);
-    for (size_t i = 0; i < N; ++i) {
-      auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(),
-                                                       c10::scalarTypeToTypeMeta(parts[i].type));
-      impl->set_storage_offset(at[i] / (int64_t)c10::elementSize(parts[i].type));
-      impl->set_sizes_contiguous(parts[i].shape);
-      t[i] = Tensor(std::move(impl));
-    }
-  }
-};
 
 // An address as whatever pointer an entry takes.
 struct Address {
@@ -268,9 +245,9 @@ PyObject* route_fwd(PyObject* const* a) {
     if (m.size(0) != T) refuse(PyExc_ValueError, "token_mask must have %lld entries", (long long)T);
     mask = ptr(m);
   }
-  const Parts<5> out(logits, {{{T, k}, ScalarType::Float}, {{T, k}, ScalarType::Int}, {{E}, ScalarType::Int},
-                              {{}, ScalarType::Float}, {{E}, ScalarType::Float}});
-  const auto& [weight, idx, counts, loss, balance] = out.t;
+  const Tensor weight = fresh(logits, {T, k}, ScalarType::Float), idx = fresh(logits, {T, k}, ScalarType::Int);
+  const Tensor counts = fresh(logits, {E}, ScalarType::Int), loss = fresh(logits, {}, ScalarType::Float);
+  const Tensor balance = fresh(logits, {E}, ScalarType::Float);
   const size_t need = g.moe_route_fwd_workspace_bytes(T, size32(E));
   const Tensor ws = scratch(logits, need);
   call("moe_route_fwd", g.moe_route_fwd, logits, ptr(logits), code, mask, ptr(weight), ptr(idx), ptr(counts),
@@ -310,8 +287,7 @@ PyObject* plan(PyObject* const* a) {
   if (k < 1 || E < 1)
     refuse(PyExc_ValueError, "idx needs at least one column and num_experts at least one expert");
   if (E > (1 << 20)) raise_status("moe_plan", MDG_EUNSUPPORTED);  // (as the entry would, before offs of that size)
-  const Parts<2> out(idx, {{{E}, ScalarType::Int}, {{T, k}, ScalarType::Int}});
-  const auto& [offs, dest] = out.t;
+  const Tensor offs = fresh(idx, {E}, ScalarType::Int), dest = fresh(idx, {T, k}, ScalarType::Int);
   const size_t need = g.moe_plan_workspace_bytes(T, size32(k), size32(E));
   const Tensor ws = scratch(idx, need);
   call("moe_plan", g.moe_plan, idx, ptr(idx), ptr(offs), ptr(dest), T, size32(k), size32(E), ptr(ws), need);
