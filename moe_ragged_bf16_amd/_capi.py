@@ -10,6 +10,8 @@ import os
 import threading
 from typing import Optional
 
+from torch._C import _is_tracing
+
 from . import build as _build
 
 MDG_OK, MDG_EINVAL, MDG_EUNSUPPORTED, MDG_EOVERLAP, MDG_EWORKSPACE, MDG_EHIP, MDG_ENOMEM = range(7)
@@ -148,6 +150,13 @@ def status_string(status: int) -> str:
 def check(entry: str, status: int) -> None:
     if status != MDG_OK:
         raise MdgError(entry, status, status_string(status))
+
+
+def refuse_tracing(call: str) -> None:
+    """Raises under torch.jit.trace: it would record only the allocation of the
+    outputs, not the library's call that fills them."""
+    if _is_tracing():
+        raise NotImplementedError(f"{call} cannot be traced by torch.jit.trace")
 
 
 class _Native:

@@ -16,6 +16,10 @@ sums run in fp32, and the result is rounded to bf16 once.  Before that rounding 
 is off by at most 7 * 2^-13 * sum over the groups of 8 of 2^E times the scales,
 plus (K + 8) * 2^-24 * sum |products|: more than fp32 sums throughout would allow.  A
 small product beside a large one of its 8 is lost even if the large one cancels.
+
+All calls but ``grouped_fp8_mm`` record nothing for autograd, and all raise
+NotImplementedError under ``torch.jit.trace``, which cannot see the library's
+calls (and would keep ``grouped_fp8_mm``'s 8-bit weights as constants).
 """
 from __future__ import annotations
 
@@ -24,7 +28,7 @@ from typing import NamedTuple, Optional, Union
 import torch
 
 from . import _capi, ops
-from ._capi import native
+from ._capi import native, refuse_tracing
 from .ops import _need
 
 __all__ = ["Fp8Rows", "Fp8Weight", "quantize_fp8_rows", "quantize_fp8_weight", "fp8_gemm_fwd_workspace_bytes",
@@ -48,6 +52,7 @@ class Fp8Weight(NamedTuple):
 
 def quantize_fp8_rows(x: torch.Tensor) -> Fp8Rows:
     """x [M, K] (bf16 or fp32; K a multiple of 8) in 8 bits."""
+    refuse_tracing("quantize_fp8_rows")
     return Fp8Rows(*native.quantize_rows(x))
 
 
@@ -55,6 +60,7 @@ def quantize_fp8_weight(w: torch.Tensor, *, transpose: bool = False) -> Fp8Weigh
     """w [E, N, K] (bf16 or fp32; N and K multiples of 8) in 8 bits.
     ``transpose``: also the transposed copy that ``grouped_fp8_gemm_dgrad``
     reads."""
+    refuse_tracing("quantize_fp8_weight")
     return Fp8Weight(*native.quantize_weight(w, transpose))
 
 
@@ -75,6 +81,7 @@ def grouped_fp8_gemm_fwd(x: Union[torch.Tensor, Fp8Rows], wq: torch.Tensor, w_sc
     offs as in ``grouped_det_gemm_fwd``; rows past offs[E-1] of a freshly
     allocated Y are left uninitialised.  ``workspace`` (uint8, at least
     ``fp8_gemm_fwd_workspace_bytes()``) is allocated per call when not given."""
+    refuse_tracing("grouped_fp8_gemm_fwd")
     q, x_scale = x if isinstance(x, Fp8Rows) else (x, None)
     return native.fp8_gemm_fwd(q, x_scale, wq, w_scale, offs, out, workspace)
 
@@ -85,6 +92,7 @@ def grouped_fp8_gemm_dgrad(g: Union[torch.Tensor, Fp8Rows], wqt: torch.Tensor, w
     """dX[s_e:t_e] = G[s_e:t_e] @ W[e], bf16 [M, K], with G in 8 bits (as x in
     ``grouped_fp8_gemm_fwd``) and W what wqt [E, K, N] and w_scale_t
     (``quantize_fp8_weight(w, transpose=True)``'s qt and scale_t) stand for."""
+    refuse_tracing("grouped_fp8_gemm_dgrad")
     return grouped_fp8_gemm_fwd(g, wqt, w_scale_t, offs, out, workspace)
 
 
@@ -120,6 +128,7 @@ def grouped_fp8_mm(x: torch.Tensor, w: torch.Tensor, offs: torch.Tensor, *,
     offs[E-1] are zero.  ``w8``: ``quantize_fp8_weight(w, transpose=True)`` where
     the caller keeps it between steps; quantised by the call otherwise.  N and K
     are multiples of 8."""
+    refuse_tracing("grouped_fp8_mm")
     _need(x, "x", torch.bfloat16, 2)
     _need(w, "w", torch.bfloat16, 3)
     if w8 is None:

@@ -65,6 +65,7 @@ class GroupedDetGemmLaunch:
         """Enqueue the bound kernels on the current stream; returns the output."""
         if self._h is None:
             raise RuntimeError(f"{self._entry}: launch used after close()")
+        _capi.refuse_tracing("launch")
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
                 st = self._lib.grouped_det_gemm_launch(self._h, _stream_handle(self.out))

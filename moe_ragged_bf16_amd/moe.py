@@ -8,9 +8,12 @@
 
 ``moe_route``, ``moe_dispatch`` and ``moe_combine`` are differentiable (``weight``
 and ``loss`` by the logits; rows by x; ``out`` by y and the weights); the
-``_fwd`` / ``_bwd`` functions are the single calls they are made of.  Every
+``_fwd`` / ``_bwd`` functions are the single calls they are made of, which record
+nothing for autograd (neither gradients nor forward-mode tangents).  Every
 step runs in the library's gfx950 kernels, reads the routing on the device only
-(no host synchronisation) and is bitwise reproducible.
+(no host synchronisation) and is bitwise reproducible.  ``torch.jit.trace``
+cannot see the library's calls: ``moe_plan`` and the single calls raise
+NotImplementedError under it.
 """
 from __future__ import annotations
 
@@ -18,7 +21,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from ._capi import native
+from ._capi import native, refuse_tracing
 
 __all__ = ["MoeRoute", "MoePlan", "moe_route", "moe_route_fwd", "moe_route_bwd", "moe_plan", "moe_dispatch",
            "moe_dispatch_fwd", "moe_dispatch_bwd", "moe_combine", "moe_combine_fwd", "moe_combine_bwd"]
@@ -53,6 +56,7 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, *, normalize: bool = True,
     tokens that have an expert and S_e their summed probability of e (0 without
     such tokens); it is 1 when the routing is even.
     """
+    refuse_tracing("moe_route_fwd")
     return _named(MoeRoute, native.route_fwd(logits, top_k, normalize, token_mask))
 
 
@@ -62,13 +66,14 @@ def moe_route_bwd(dweight: Optional[torch.Tensor], dloss: Optional[torch.Tensor]
     ``route.weight`` (fp32 [tokens, top_k]) and ``route.loss`` (fp32 scalar on
     the device); either may be None (zero).  ``route`` is what
     ``moe_route_fwd(logits, ..., normalize=normalize)`` returned."""
+    refuse_tracing("moe_route_bwd")
     return native.route_bwd(dweight, dloss, logits, route.weight, route.idx, route.balance, normalize)
 
 
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_k, normalize, token_mask):
-        r = moe_route_fwd(logits, top_k, normalize=normalize, token_mask=token_mask)
+        r = _named(MoeRoute, native.route_fwd(logits, top_k, normalize, token_mask))
         ctx.save_for_backward(logits, *r)
         ctx.normalize = normalize
         ctx.mark_non_differentiable(r.idx, r.counts, r.balance)
@@ -98,23 +103,27 @@ def moe_plan(idx: torch.Tensor, num_experts: int) -> MoePlan:
     keeping their order within an expert: ``offs`` [num_experts] as the grouped
     products take it and ``dest`` [tokens, top_k], each slot's row.  Entries
     outside [0, num_experts) have no row (dest -1)."""
+    refuse_tracing("moe_plan")
     return _named(MoePlan, native.plan(idx, num_experts))
 
 
 def moe_dispatch_fwd(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     """rows [tokens * top_k, hidden]: rows[dest[t, j]] = x[t] (bf16 or fp32);
     rows from offs[E-1] on, which no slot has, are zero."""
+    refuse_tracing("moe_dispatch_fwd")
     return native.dispatch_fwd(x, plan.offs, plan.dest)
 
 
 def moe_dispatch_bwd(drows: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     """dx [tokens, hidden] = sum_j drows[dest[t, j]], in fp32, rounded once."""
+    refuse_tracing("moe_dispatch_bwd")
     return native.dispatch_bwd(drows, plan.offs, plan.dest)
 
 
 def moe_combine_fwd(y: torch.Tensor, weight: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     """out [tokens, hidden] = sum_j weight[t, j] y[dest[t, j]], in fp32, rounded
     once; slots without a row add nothing."""
+    refuse_tracing("moe_combine_fwd")
     return native.combine_fwd(y, weight, plan.offs, plan.dest)
 
 
@@ -122,6 +131,7 @@ def moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor,
                     plan: MoePlan) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dy, dweight): dy[dest[t, j]] = weight[t, j] dout[t] (rows no slot has:
     zero) and dweight[t, j] = <dout[t], y[dest[t, j]]> in fp32."""
+    refuse_tracing("moe_combine_bwd")
     return native.combine_bwd(dout, y, weight, plan.offs, plan.dest)
 
 
@@ -129,7 +139,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, offs, dest):
         ctx.save_for_backward(offs, dest)
-        return moe_dispatch_fwd(x, MoePlan(offs, dest))
+        return native.dispatch_fwd(x, offs, dest)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -141,7 +151,7 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weight, offs, dest):
         ctx.save_for_backward(y, weight, offs, dest)
-        return moe_combine_fwd(y, weight, MoePlan(offs, dest))
+        return native.combine_fwd(y, weight, offs, dest)
 
     @staticmethod
     @torch.autograd.function.once_differentiable

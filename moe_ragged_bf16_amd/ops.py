@@ -3,6 +3,8 @@
 Each function marshals pointers, sizes and the current HIP stream and calls the
 library; every step of the computation runs in the gfx950 kernels.  torch
 supplies device memory (outputs and the wgrad workspace) and the stream.
+``torch.jit.trace`` cannot see the library's calls: under it these functions
+raise NotImplementedError.
 
 Signatures follow the one-shot functions of the Cake ragged BF16 grouped GEMM
 API page and flashinfer PR #8924 ("Deterministic weight-gradient
@@ -97,6 +99,7 @@ def grouped_det_gemm_fwd(x: torch.Tensor, w: torch.Tensor, offs: torch.Tensor,
     """Y[s_e:t_e] = X[s_e:t_e] @ W[e]^T, bf16 [M, N].  Rows past offs[E-1] of a
     freshly allocated Y are left uninitialised.  `workspace` (uint8, at least
     fwd_workspace_bytes()) is allocated per call when not given."""
+    _capi.refuse_tracing("grouped_det_gemm_fwd")
     _need(x, "x", torch.bfloat16, 2)
     _need(w, "w", torch.bfloat16, 3)
     M, K = x.shape
@@ -128,6 +131,7 @@ def grouped_det_gemm_dgrad(g: torch.Tensor, w: torch.Tensor, offs: torch.Tensor,
                            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX[s_e:t_e] = G[s_e:t_e] @ W[e], bf16 [M, K].  `workspace` (uint8, at
     least dgrad_workspace_bytes()) is allocated per call when not given."""
+    _capi.refuse_tracing("grouped_det_gemm_dgrad")
     _need(g, "g", torch.bfloat16, 2)
     _need(w, "w", torch.bfloat16, 3)
     M, N = g.shape
@@ -174,6 +178,7 @@ def grouped_det_gemm_wgrad(g: torch.Tensor, x: torch.Tensor, offs: torch.Tensor,
     from ``out``, else ``num_groups``, else the length of ``offs``.
     ``workspace`` (uint8 device tensor) is allocated when not given.
     """
+    _capi.refuse_tracing("grouped_det_gemm_wgrad")
     if not isinstance(accumulate, bool):
         raise TypeError("accumulate must be a bool")
     _need(g, "g", torch.bfloat16, 2)
@@ -221,6 +226,7 @@ def grouped_det_gemm_wgrad(g: torch.Tensor, x: torch.Tensor, offs: torch.Tensor,
 def zero_pad_rows(out: torch.Tensor, offs: torch.Tensor, num_groups: int) -> torch.Tensor:
     """Writes zeros over the rows of ``out`` [M, C] at or past offs[E-1] (rows
     that belong to no group), reading offs on the device only."""
+    _capi.refuse_tracing("zero_pad_rows")
     if not isinstance(out, torch.Tensor) or out.dim() != 2 or out.device.type != "cuda":
         raise ValueError("out must be a 2-D device tensor")
     if not out.is_contiguous():
