@@ -69,6 +69,7 @@ def build(verbose: bool = False) -> str:
     try:
         check_no_packed_fp32(tmp)
         check_mfma_sources(tmp)
+        check_mfma_results(tmp)
     except Exception:
         os.unlink(tmp)
         raise
@@ -126,31 +127,111 @@ def _registers(operand: str) -> set:
     return out
 
 
-def mfma_source_hazards(asm: str) -> list:
-    """Scaled matrix instructions of a disassembly with a source register that one
-    of the two instructions before wrote as a vector instruction (the hardware
-    needs two wait states there; the compiler adds them for its own instructions,
-    not around the asm statements of the 8-bit kernels)."""
-    bad, before = [], []           # before: (wait states, registers written, text) of the latest instructions
+class _Instruction:
+    """A line of a disassembly: what it is, the registers it names and which
+    instructions may run next or may have run before (indexes in its function)."""
+    __slots__ = ("name", "text", "operands", "states", "next", "before")
+
+    def __init__(self, text: str):
+        name, _, args = text.partition(" ")
+        self.name, self.text, self.next, self.before = name, text, [], []
+        self.operands = [_registers(o) for o in re.split(r",\s*(?![^\[]*\])", args)] if args else []
+        self.states = 1 + (int(args, 0) if name == "s_nop" else 0)  # wait states it lets pass
+
+    @property
+    def mfma(self) -> bool:
+        return self.name.startswith(("v_mfma", "v_smfma"))
+
+
+def _functions(asm: str) -> list:
+    """The instructions of each function of a disassembly, with the branches
+    between them (a branch names its target as <function+offset>)."""
+    out, here, at, name, base = [], [], {}, None, 0
+
+    def finish():
+        for i, (ins, target) in enumerate(here):
+            falls = ins.name not in ("s_branch", "s_endpgm", "s_setpc_b64")
+            to = ([i + 1] if falls and i + 1 < len(here) else []) + ([at[target]] if target in at else [])
+            ins.next = to
+            for j in to:
+                here[j][0].before.append(i)
+        if here:
+            out.append([ins for ins, _ in here])
+
     for line in asm.splitlines():
-        text = line.split("//")[0].strip()
-        m = re.match(r"([a-z]\w+)\s*(.*)", text)
-        if not m or text.endswith(":"):
-            before = []            # a label: another path may lead here, whose last instructions are its own
+        m = re.match(r"([0-9a-f]+) <(.*)>:$", line)
+        if m:
+            finish()
+            here, at, base, name = [], {}, int(m.group(1), 16), m.group(2)
             continue
-        name, args = m.group(1), m.group(2)
-        operands = re.split(r",\s*(?![^\[]*\])", args)
-        if name.startswith("v_mfma_scale"):
-            sources, states = set().union(*(_registers(o) for o in operands[1:])), 0
-            for waits, written, what in reversed(before):
-                if states >= 2:
-                    break
-                if written & sources:
-                    bad.append("%s; %s" % (what, text))
-                states += waits
-        valu = name.startswith("v_") and not name.startswith("v_mfma") and not name.startswith("v_cmp")
-        waits = 1 + (int(args, 0) if name == "s_nop" else 0)
-        before = before[-3:] + [(waits, _registers(operands[0]) if valu else set(), text)]
+        text, _, comment = line.partition("//")
+        text = re.sub(r"\s+", " ", text).strip()
+        if not re.match(r"[a-z]\w+( |$)", text):
+            continue
+        m = re.match(r"\s*([0-9A-F]+):", comment)
+        if m:
+            at[int(m.group(1), 16)] = len(here)
+        target = None
+        if text.startswith(("s_branch", "s_cbranch")):
+            m = re.search(r"<%s(?:\+0x([0-9a-f]+))?>" % re.escape(name or ""), comment)
+            target = base + int(m.group(1) or "0", 16) if m else None
+        here.append((_Instruction(text), target))
+    finish()
+    return out
+
+
+def _within(function: list, i: int, states: int, edges: str):
+    """The instructions that instruction i reaches along `edges` (\"next\", \"before\")
+    with fewer than `states` wait states between them."""
+    todo, best = [(j, 0) for j in getattr(function[i], edges)], {}
+    while todo:
+        j, passed = todo.pop()
+        if passed >= states or best.get(j, states) <= passed:
+            continue
+        best[j] = passed
+        yield function[j]
+        todo += [(k, passed + function[j].states) for k in getattr(function[j], edges)]
+
+
+def mfma_source_hazards(asm: str) -> list:
+    """Scaled matrix instructions of a disassembly with a source register that a
+    vector instruction wrote within two wait states before (the hardware
+    needs two there; the compiler adds them for its own instructions,
+    not around the asm statements of the 8-bit kernels)."""
+    bad = []
+    for f in _functions(asm):
+        for i, ins in enumerate(f):
+            if not ins.name.startswith("v_mfma_scale"):
+                continue
+            sources = set().union(*ins.operands[1:])
+            for w in _within(f, i, 2, "before"):
+                if w.name.startswith("v_") and not w.mfma and not w.name.startswith("v_cmp") and w.operands \
+                        and w.operands[0] & sources:
+                    bad.append("%s; %s" % (w.text, ins.text))
+    return bad
+
+
+# Wait states between a matrix instruction of 8 passes (the longest here: 16x16x128 in
+# 8 bits) and another instruction's access of its result: passes + 4 on gfx950.
+MFMA_RESULT_STATES = 12
+
+
+def mfma_result_hazards(asm: str) -> list:
+    """Accesses of a matrix instruction's result that come before it is there: by
+    another instruction than a matrix instruction that accumulates onto all of it
+    (which the hardware waits for), within MFMA_RESULT_STATES."""
+    bad = []
+    for f in _functions(asm):
+        for i, ins in enumerate(f):
+            if not ins.mfma:
+                continue
+            result = ins.operands[0]
+            for r in _within(f, i, MFMA_RESULT_STATES, "next"):
+                if r.mfma and r.operands[3] == result and not result & set().union(*r.operands[1:3]) and \
+                        (r.operands[0] == result or not r.operands[0] & result):
+                    continue
+                if result & set().union(*r.operands):
+                    bad.append("%s; %s" % (ins.text, r.text))
     return bad
 
 
@@ -158,6 +239,12 @@ def check_mfma_sources(lib_path: str = LIB_PATH) -> None:
     bad = mfma_source_hazards(device_assembly(lib_path))
     if bad:
         raise RuntimeError("a matrix instruction too close behind a write of its source: %d, e.g. %s" % (len(bad), bad[0]))
+
+
+def check_mfma_results(lib_path: str = LIB_PATH) -> None:
+    bad = mfma_result_hazards(device_assembly(lib_path))
+    if bad:
+        raise RuntimeError("an access of a matrix instruction's result before it is there: %d, e.g. %s" % (len(bad), bad[0]))
 
 
 C_SMOKE_SRC = os.path.join(ROOT, "tests", "c_abi_smoke.cpp")

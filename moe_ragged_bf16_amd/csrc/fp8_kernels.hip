@@ -215,8 +215,8 @@ __device__ __forceinline__ uint8_t* buf_b() {
 // tile kernel's 256 accumulators stay in AGPRs, in place.  The compiler does not see
 // that a source written by a vector instruction needs two wait states before its
 // use here: operands come from LDS (which it waits for), and scales through
-// settle().  The build checks the generated code for it.  (An s_nop in front of each
-// product cost 2 %.)
+// settle().  Nor does it see when the result is there: settle_results().  The build
+// checks the generated code for both.  (An s_nop in front of each product cost 2 %.)
 #define MDG_MFMA(REGS, SEL)                                                                            \
   asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL : REGS(c) : "v"(b), "v"(a), \
                "v"(sb), "v"(sa))
@@ -243,6 +243,21 @@ __device__ __forceinline__ void settle(uint32_t (&x)[N], uint32_t& w) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i]));
   asm volatile("s_nop 1" : "+v"(w));
+}
+
+// The wait states between the last products and the first other access of their
+// results (12 for this instruction; the compiler does not see the need around the asm
+// statements, and left alone it moves the reads up to the products).  Results in
+// VGPRs are tied to the place; those in AGPRs are read by statements that stay behind
+// it anyway.  The build checks the generated code.
+__device__ __forceinline__ void settle_results() { asm volatile("s_nop 15"); }
+template <int I, int J>
+__device__ __forceinline__ void settle_results(f32x4 (&acc)[I][J]) {
+  settle_results();
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+#pragma unroll
+    for (int j = 0; j < J; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
 
 // Waits until all of this wave's LDS reads have returned.
@@ -560,6 +575,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(Fp8GemmParams p) 
     pipe.load_scales(sc, p, nx, 0);
     const int ln = lane_here();
     const OutTile ot = out_tile(p.y + (int64_t)u.row0 * p.n + u.j0, p.n, u.i_valid, u.j_valid, pipe.wi, pipe.wj, ln, 2);
+    settle_results();
     store_tile(acc, ot, s_out[pipe.w], ln);
     if (nk & 1) {
       // the last step's fragments came from buffer 1; the next unit's stage 0 is in
@@ -875,6 +891,7 @@ __global__ __launch_bounds__(256, 2) void fp8_mid_kernel(Fp8GemmParams p) {
   }
   wait_vm_lgkm<0>();
   __syncthreads();
+  settle_results(acc);
   // 16 rows x 64 columns of a wave at a time through LDS to 128-byte row segments
   uint8_t* xo = mid_buffer<0, 0>() + w * 2048;
 #pragma unroll
