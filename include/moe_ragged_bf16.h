@@ -417,7 +417,14 @@ MDG_API mdg_status moe_combine_bwd(const void* dout, const void* y, const float*
  * which is more than a sum in fp32 throughout would allow.  (On operands drawn
  * from a normal distribution about one bf16 output in 50 differs from that of fp32
  * sums.)
- * Every output element is summed in one fixed order: bitwise reproducible.
+ * Order.  Without atomics; the same for all rows and columns of a call, whatever
+ * the other rows hold and however offs cuts them, so a call repeats bit for bit.
+ * With few rows (a function of m_rows, n, num_groups and the device's number of
+ * CUs) k is dealt to four partial sums in pieces of 512, which are added at the
+ * end; otherwise, and for k <= 512 in any case, it is summed from 0 on.  So with k > 512
+ * the same row can get different bits in calls of different sizes (a decode step
+ * and a prompt, or with more experts), within the bound above: results are not
+ * invariant under batching.
  */
 MDG_API mdg_status grouped_fp8_quantize_rows(const void* x, int dtype, void* q, void* scale, int64_t m_rows,
                                              int64_t k, void* stream);
