@@ -193,6 +193,10 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
   // small against middle: 2 rows on average 33 / 40 us, 8 rows 44 / 44, 16 rows
   // 51 / 44; where all its units run at once it gains at more rows: 1 group of
   // 4096 x 4096, 128 rows 16 / 23, 200 rows 26 / 23; 16 of 1000 x 2000, 20 rows 12 / 15.
+  // The rules go by the most groups that can have rows, as offs is not read here.  Where
+  // all rows are one group's, the small kernel reads that group's weight once for each
+  // 64 of them: 1536 x 2048, 300 rows in one of 64 groups 9 us (in a call of that group alone,
+  // by the middle kernel, 14), 512 rows 14 (14), 2000 rows in one of 256 groups 80 (15).
   const int64_t small = active + m_rows / kFp8SmallRows;
   if (m_rows <= 8 * active || (m_rows <= 128 * active && small * columns(kFp8SmallCols) <= 3 * cus))
     return launched(launch_fp8_small(p, (int)small, s));

@@ -177,7 +177,7 @@ MDG_API mdg_status moe_route_fwd(const void* logits, int dtype, const uint8_t* t
   p.top_k = top_k;
   p.normalize = normalize != 0;
   p.fp32 = dtype == MDG_FP32;
-  p.vec = aligned16(logits) && experts % route_values(experts) == 0;
+  p.vec = aligned16(logits) && experts % route_values(experts) == 0;  // (both sides' times: the kernels' LogitBits)
   p.blocks = cut.blocks;
   if (cut.blocks > 1) {
     char* ws = static_cast<char*>(workspace);

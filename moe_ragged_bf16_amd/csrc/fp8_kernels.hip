@@ -519,8 +519,10 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& p, const int* s
 // 16384 rows over 8 experts' 14336 x 4096 take 738 us, 2.61 PFLOP/s (the library's
 // largest 8-bit products here reach 3.1), 32768 over 64 experts' 1536 x 2048 116 us:
 // 1.78 PFLOP/s of the rows' own products, 2.2 with those of partly filled tiles.
-// What bounds it: a step's matrix work is 2048 cycles and it takes about 3200.  With
-// its loads left out the first takes 15 % less, with loads that always hit the L2 7 %,
+// What bounds it: a step's matrix work is 2048 cycles and it takes about 2900 (the
+// counters have the matrix pipe busy 71 % of the cycles in the first, 50 % in the
+// second, whose units have 12 or 16 steps).  In copies of the kernel, with
+// its loads left out the first took 15 % less, with loads that always hit the L2 7 %,
 // with the fragments' LDS reads left out 2 %, with all data zero (the clock then
 // holds; the card's power limits it otherwise, to about 1.9 of 2.4 GHz) 13 %.
 // Results that left between the products of the steps around a unit's end, rather

@@ -2,8 +2,9 @@
 // layer: routing with counts and balance loss, the plan that sorts slots by
 // expert, rows dispatched by the plan and combined back, and the gradients.
 //
-// All sums run in fp32 (integers where they count) in one fixed order and no
-// floating-point atomics are used, so every output is bitwise reproducible.
+// All sums run in fp32 (integers where they count; the loss's last sum in 64 bits) in
+// one fixed order and no floating-point atomics are used, so every output is bitwise
+// reproducible.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -41,6 +42,11 @@ __device__ __forceinline__ float sum_over_groups(float v) {
 }
 
 // V consecutive logits of a row from column c0, in their bits (bf16: two to a word).
+// With `vec` (rows start on 16 bytes and experts are a multiple of V) in 16-byte
+// pieces; else element by element, and the gradient's stores likewise.  65536 rows, top-4,
+// forward with its second launch / gradient in us: 128 experts fp32 22.3 / 15.4, 127
+// 27.6 / 43.8, 100 24.9 / 34.6; bf16 20.6 / 13.1, 24.6 / 31.1, 23.9 / 26.3; 64 experts
+// fp32 14.9 / 9.4, 60 17.0 / 18.6; bf16 14.4 / 8.0, 16.2 / 11.5.
 template <int V, bool FP32>
 struct LogitBits {
   static constexpr int kWords = FP32 ? V : V / 2;
@@ -148,7 +154,10 @@ __device__ __forceinline__ uint32_t choose(uint32_t (&key)[V], int c0, uint32_t 
 
 // e^x for x <= 0, to about 1.5 units in the last place: 2^t with t = x log2(e) in two
 // parts (t rounded, and what rounding left, which enters by its first-order term).
-// Below -200 the result is 0; the clamp also keeps -inf - (-inf) out (and loses NaN).
+// Results below the smallest normal number (x < -87.3) are 0, so a chosen expert that
+// unlikely gets weight 0; the clamp keeps -inf - (-inf) out (and loses NaN).  The gradient
+// takes the library's exponential, so its softmax may differ from the forward's in
+// the last place.
 __device__ __forceinline__ float exp_nonpositive(float x) {
   constexpr float kLog2e = 1.44269502162933349609375f;    // log2(e) rounded to fp32
   constexpr float kLog2eLow = 1.925963033500011079e-08f;  // log2(e) - kLog2e
@@ -183,9 +192,10 @@ constexpr int own_slots() {
 // in registers and DPP moves; the first round's value is the softmax maximum; lanes
 // that hold a chosen expert write its slot.  Each lane adds the probabilities of its
 // columns over all rows of its block in registers; the next row's logits load while
-// a row is worked on.  Memory and the launch bound it: 65536 rows of 128 fp32 logits,
-// top-4, take 17.2 us (12.3 us with one round in place of four); the library
-// exponential and passing each round's choice to the slot's lane made it 18.6 us.
+// a row is worked on.  Latency bounds it, one row in flight per lane group and 16 waves to
+// a CU: 65536 rows of 128 fp32 logits, top-4, take 17 to 20 us, 1.8 TB/s (12.3 us with
+// one round in place of four); the library exponential and passing each round's choice
+// to the slot's lane made it 1.4 us longer.
 template <int L, int V, bool FP32>
 __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p) {
   extern __shared__ uint8_t smem[];
@@ -313,8 +323,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteParams p)
 // Adds the route blocks' partial sums and writes counts, balance and loss.  A
 // workgroup takes kFinishCols experts, its threads as columns x row groups, so
 // that all of the table's loads are in flight at once (one workgroup walking
-// [256 blocks, 256 experts] alone took 60 us, these 4.4 us); the last workgroup to
-// finish adds the shares of the loss in workgroup order.
+// [256 blocks, 256 experts] alone took 60 us, these 4.4 us).  The order of an expert's
+// sum is fixed: row group g of 64 adds blocks g, g + 64, ..., a wave's 4 groups are added by
+// shuffles, then the 16 waves.  The last workgroup to finish adds the workgroups'
+// shares of the loss.
 constexpr int kFinishCols = 16;
 constexpr int kFinishRows = kRouteThreads / kFinishCols;  // row groups
 static_assert(kRouteMaxExperts <= 64 * kFinishCols, "a lane for every workgroup's share");
@@ -598,8 +610,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_rank_kernel(PlanParams p) {
 // 16-byte pieces.  Bytes bound all of these: each row is read once and written
 // once, wherever the plan puts it.  4095 tokens x 8 rows of 7168 bf16 (0.53 GB moved a
 // pass, 1 GB by the gradient): dispatch 93 us (5.7 TB/s, mostly writes), the weighted
-// sum 123 us (4.3 TB/s, mostly reads; reads alone reach 4.0 in a large sum), the
-// gradient 179 us (5.6 TB/s).  A wave instead of four for short rows (TEAM 64).
+// sum 123 us (4.3 TB/s, mostly reads: one 16-byte load in flight per thread, slot after
+// slot; kernels here that load ahead read at 4.9), the gradient 179 us (5.6 TB/s).  A
+// wave instead of four for short rows (TEAM 64).
 
 // Rows from offs[E-1] on belong to no slot: zeros, shared out over the blocks.
 __device__ __forceinline__ void zero_rest(const RowsParams& p) {
