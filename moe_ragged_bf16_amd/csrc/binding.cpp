@@ -2,10 +2,10 @@
 // outputs and workspaces from torch's allocator, and the C entry on the tensors'
 // device and its current stream.  In C++ because a call is short: with the same
 // checks in Python and ctypes, three tokens' dispatch took 7.5 us of host time, of
-// which the launch is 3.4; here it takes 3.9 (plan 7.4 and 4.6, combine's gradient
-// 10.1 and 4.8).  One token's route, whose five outputs are allocated one by one,
-// takes 7.4 (5.8 when they shared a storage, which their owner could then not
-// save or free one by one).
+// which the launch is 3.4; here it takes 3.9 to 4.9 (plan 7.4 and 4.6 to 5.4, the 8-bit
+// product 13.5 and 7.1 to 8.5).  One token's route, whose five outputs are allocated
+// one by one, takes 7.4 to 8.1 (1.6 less when they shared a storage, which their
+// owner could then not save or free one by one).
 //
 // The C entries are those of the library that the package has loaded; setup()
 // takes their addresses.
