@@ -82,7 +82,7 @@ def copy_calibration(mib: int) -> None:
 def kernel_source_digest() -> str:
     import hashlib
     digest = hashlib.sha256()
-    for name in ("grouped_gemm_kernels.hip", "kernel_common.h", "tile_epilogue.h"):
+    for name in ("grouped_gemm_kernels.hip", "kernel_common.h", "tile_epilogue.h", "tile_pipe.h"):
         with open(os.path.join(ROOT, "moe_ragged_bf16_amd", "csrc", name), "rb") as f:
             digest.update(f.read())
     return digest.hexdigest()
