@@ -438,6 +438,50 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
                                         int64_t n, int64_t k, int32_t num_groups, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
+/*
+ * The experts' gated feed-forward.  For every expert e with rows s_e:t_e (offs as above):
+ *
+ *   fwd    a = X W_gate[e]^T, b = X W_up[e]^T, h = act(a) b
+ *   dgrad  dh = dY W_down[e], da = dh b act'(a), db = dh act(a)
+ *
+ * with act(a) = a s(q(a)), s the logistic function: MDG_SILU, q(a) = a; MDG_GELU_TANH,
+ * q(a) = 2 sqrt(2 / pi) (a + 0.044715 a^3), the tanh form of GELU.
+ *
+ *   x        [m_rows, k] bf16, read.
+ *   w        [num_groups, 2 f, k] bf16, read: rows 0 .. f-1 of an expert are W_gate, rows
+ *            f .. 2f-1 W_up.
+ *   h        [m_rows, f] bf16, written: act(a) b from the fp32 sums a and b, rounded once.
+ *   gate_up  fwd: [m_rows, 2 f] bf16, written: a and b rounded (what grouped_det_gemm_fwd
+ *            gives for x and w), which the gradient needs; NULL: not kept, with the same h.
+ *            dgrad: the same, read; a and b are those bf16 values.
+ *   dy       [m_rows, n] bf16, read: the gradient of y = h W_down^T.
+ *   w_down   [num_groups, n, f] bf16, read.
+ *   dgate_up [m_rows, 2 f] bf16, written: da and db from the fp32 dh, rounded once.  The
+ *            rest of the block's backward pass is the products': dx = dgrad(dgate_up, w),
+ *            dw = wgrad(dgate_up, x), dw_down = wgrad(dy, h).
+ *
+ * k, f and n are multiples of 8, 2 f <= 2^20, 2 f k and 2 f n < 2^31; 1 <= num_groups <= 1024.
+ * Rows at or past the last group's end are left as they are, and malformed offs are read
+ * as for the products.  s is off by at most 2^-23 (|q| + 3) of its value, which bf16's
+ * rounding hides, and 0 below 2^-126.  A value of a or b that is not finite reaches its own h, da and db only;
+ * act(-inf), and act' at either infinity, are NaN.
+ * workspace: at least grouped_gated_gemm_{fwd,dgrad}_workspace_bytes() bytes (a function of
+ * the sizes; 0 for invalid ones), 256-byte aligned, used until the stream has passed the
+ * call.  The sums' order is fixed by the sizes and offs: a call repeats bit for bit, and
+ * the same row can get different bits in calls of other sizes.  m_rows == 0 enqueues nothing.
+ */
+typedef enum { MDG_SILU = 0, MDG_GELU_TANH = 1 } mdg_activation;
+
+MDG_API size_t grouped_gated_gemm_fwd_workspace_bytes(int64_t m_rows, int64_t f, int64_t k, int32_t num_groups);
+MDG_API mdg_status grouped_gated_gemm_fwd(const void* x, const void* w, const int32_t* offs, void* h, void* gate_up,
+                                          int activation, int64_t m_rows, int64_t f, int64_t k, int32_t num_groups,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+MDG_API size_t grouped_gated_gemm_dgrad_workspace_bytes(int64_t m_rows, int64_t n, int64_t f, int32_t num_groups);
+MDG_API mdg_status grouped_gated_gemm_dgrad(const void* dy, const void* w_down, const void* gate_up,
+                                            const int32_t* offs, void* dgate_up, int activation, int64_t m_rows,
+                                            int64_t n, int64_t f, int32_t num_groups, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

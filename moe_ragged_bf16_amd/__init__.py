@@ -50,3 +50,11 @@ from .fp8 import (  # noqa: F401
     quantize_fp8_rows,
     quantize_fp8_weight,
 )
+from .gated import (  # noqa: F401
+    GatedRows,
+    gated_gemm_dgrad_workspace_bytes,
+    gated_gemm_fwd_workspace_bytes,
+    grouped_gated_ffn,
+    grouped_gated_gemm_dgrad,
+    grouped_gated_gemm_fwd,
+)

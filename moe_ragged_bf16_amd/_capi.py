@@ -16,6 +16,7 @@ from . import build as _build
 
 MDG_OK, MDG_EINVAL, MDG_EUNSUPPORTED, MDG_EOVERLAP, MDG_EWORKSPACE, MDG_EHIP, MDG_ENOMEM = range(7)
 MDG_BF16, MDG_FP32, MDG_E4M3 = range(3)
+MDG_SILU, MDG_GELU_TANH = range(2)
 
 EXPORTED = (
     "grouped_det_gemm_abi_version",
@@ -48,6 +49,10 @@ EXPORTED = (
     "grouped_fp8_quantize_weight",
     "grouped_fp8_gemm_fwd",
     "grouped_fp8_gemm_fwd_workspace_bytes",
+    "grouped_gated_gemm_fwd",
+    "grouped_gated_gemm_fwd_workspace_bytes",
+    "grouped_gated_gemm_dgrad",
+    "grouped_gated_gemm_dgrad_workspace_bytes",
 )
 
 
@@ -136,7 +141,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                 ("grouped_fp8_quantize_rows", st, [vp, st, vp, vp, i64, i64, vp]),
                 ("grouped_fp8_quantize_weight", st, [vp, st, vp, vp, vp, vp, i32, i64, i64, vp]),
                 ("grouped_fp8_gemm_fwd_workspace_bytes", sz, [i64, i64, i64, i32, st]),
-                ("grouped_fp8_gemm_fwd", st, [vp, st, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, sz, vp])):
+                ("grouped_fp8_gemm_fwd", st, [vp, st, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, sz, vp]),
+                ("grouped_gated_gemm_fwd_workspace_bytes", sz, [i64, i64, i64, i32]),
+                ("grouped_gated_gemm_fwd", st, [vp, vp, vp, vp, vp, st, i64, i64, i64, i32, vp, sz, vp]),
+                ("grouped_gated_gemm_dgrad_workspace_bytes", sz, [i64, i64, i64, i32]),
+                ("grouped_gated_gemm_dgrad", st, [vp, vp, vp, vp, vp, st, i64, i64, i64, i32, vp, sz, vp])):
             f = getattr(lib, name)
             f.restype, f.argtypes = res, args
         _lib = lib

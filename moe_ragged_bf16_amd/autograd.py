@@ -86,11 +86,11 @@ def _elements_overlap(t: torch.Tensor) -> bool:
     return False
 
 
-def _main_grad(w: torch.Tensor, where: str) -> torch.Tensor:
+def _main_grad(w: torch.Tensor, where: str, call: str = "cake_grouped_det_mm") -> torch.Tensor:
     mg = getattr(w, "main_grad", None)
     if not isinstance(mg, torch.Tensor):
         raise ValueError(
-            f"cake_grouped_det_mm(fuse_wgrad_accumulation=True) at the {where}: w has no main_grad tensor "
+            f"{call}(fuse_wgrad_accumulation=True) at the {where}: w has no main_grad tensor "
             "(a reentrant checkpoint passes a detached copy of w; use use_reentrant=False)")
     if mg.dtype not in _MAIN_GRAD_DTYPES:
         raise TypeError(f"w.main_grad must be float32 or bfloat16, got {mg.dtype}")
@@ -113,6 +113,25 @@ def _accumulate_into(main_grad: torch.Tensor, dy, x, offs) -> None:
     tmp = main_grad.contiguous()
     ops.grouped_det_gemm_wgrad(dy, x, offs, out=tmp, num_groups=E, accumulate=True)
     main_grad.copy_(tmp)
+
+
+def _fused_main_grad(w_obj, call: str, others) -> torch.Tensor:
+    """w's main_grad at the backward, apart from the tensors that pass reads."""
+    mg = _main_grad(w_obj, "backward", call)
+    for name, t in others:
+        if _shares_memory(mg, t):
+            raise ValueError(f"w.main_grad shares memory with {name}")
+    return mg
+
+
+def _fused_wgrad(w_obj, mg, dy, x, offs):
+    """Adds the weight gradient into main_grad; what the backward returns for w."""
+    _accumulate_into(mg, dy, x, offs)
+    if not hasattr(w_obj, "grad_added_to_main_grad"):
+        return None
+    w_obj.grad_added_to_main_grad = True
+    make = torch.zeros if getattr(w_obj, "zero_out_wgrad", False) else torch.empty
+    return make(w_obj.shape, dtype=w_obj.dtype, device=w_obj.device)
 
 
 class CakeGroupedDetMm(torch.autograd.Function):
@@ -162,23 +181,14 @@ class CakeGroupedDetMm(torch.autograd.Function):
         E = w.shape[0]
         dx = dw = None
         if ctx.fuse and need_w:
-            w_obj = ctx.w_obj
-            mg = _main_grad(w_obj, "backward")
-            for name, t in (("the output gradient", dy), ("x", x), ("offs", offs), ("w", w)):
-                if _shares_memory(mg, t):
-                    raise ValueError(f"w.main_grad shares memory with {name}")
+            mg = _fused_main_grad(ctx.w_obj, "cake_grouped_det_mm",
+                                  (("the output gradient", dy), ("x", x), ("offs", offs), ("w", w)))
         if need_x:
             dx = ops.grouped_det_gemm_dgrad(dy, w, offs)
             ops.zero_pad_rows(dx, offs, E)
         if need_w:
             if ctx.fuse:
-                _accumulate_into(mg, dy, x, offs)
-                if hasattr(w_obj, "grad_added_to_main_grad"):
-                    w_obj.grad_added_to_main_grad = True
-                    if getattr(w_obj, "zero_out_wgrad", False):
-                        dw = torch.zeros(w_obj.shape, dtype=w_obj.dtype, device=w_obj.device)
-                    else:
-                        dw = torch.empty(w_obj.shape, dtype=w_obj.dtype, device=w_obj.device)
+                dw = _fused_wgrad(ctx.w_obj, mg, dy, x, offs)
             else:
                 dw = ops.grouped_det_gemm_wgrad(dy, x, offs, out_dtype=w.dtype, num_groups=E)
         return dx, dw, None, None, None

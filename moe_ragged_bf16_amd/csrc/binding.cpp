@@ -31,7 +31,9 @@ using at::Tensor;
 #define MDG_ENTRIES(X)                                                                                         \
   X(moe_route_fwd_workspace_bytes) X(moe_route_fwd) X(moe_route_bwd) X(moe_plan_workspace_bytes) X(moe_plan)   \
   X(moe_dispatch_fwd) X(moe_dispatch_bwd) X(moe_combine_fwd) X(moe_combine_bwd) X(grouped_fp8_quantize_rows)   \
-  X(grouped_fp8_quantize_weight) X(grouped_fp8_gemm_fwd_workspace_bytes) X(grouped_fp8_gemm_fwd)
+  X(grouped_fp8_quantize_weight) X(grouped_fp8_gemm_fwd_workspace_bytes) X(grouped_fp8_gemm_fwd)               \
+  X(grouped_gated_gemm_fwd_workspace_bytes) X(grouped_gated_gemm_fwd)                                          \
+  X(grouped_gated_gemm_dgrad_workspace_bytes) X(grouped_gated_gemm_dgrad)
 
 struct Entries {
 #define X(name) decltype(&::name) name = nullptr;
@@ -405,6 +407,48 @@ const Tensor& q_tensor(PyObject* o, const char* name, int dims, const Tensor* li
   return t;
 }
 
+// The E cumulative end offsets of a tensor in either form.
+const int32_t* need_offs(PyObject* o, int64_t E, const Tensor& like) {
+  const Tensor& offs = any_tensor(o, "offs");
+  if (offs.scalar_type() != ScalarType::Int || offs.dim() != 1 || !offs.is_cuda())
+    refuse(PyExc_TypeError, "offs must be a 1-D int32 device tensor");
+  if (!offs.is_contiguous()) refuse(PyExc_ValueError, "offs must be contiguous");
+  need_device(offs, "offs", &like);
+  if (offs.size(0) != E && offs.size(0) != E + 1)
+    refuse(PyExc_ValueError, "offs has %lld entries; expected E=%lld (offs) or E+1 (m_indptr)",
+           (long long)offs.size(0), (long long)E);
+  const int32_t* p = ptr(offs);
+  return p + (offs.size(0) - E);  // (skips m_indptr's leading zero)
+}
+
+// The caller's workspace (checked; *need becomes its size) or a fresh one.
+Tensor need_workspace(PyObject* o, size_t* need, const Tensor& like) {
+  if (o == Py_None) return scratch(like, *need);
+  const Tensor& ws = any_tensor(o, "workspace");
+  if (ws.scalar_type() != ScalarType::Byte || !ws.is_contiguous())
+    refuse(PyExc_ValueError, "workspace must be a contiguous uint8 tensor");
+  if ((size_t)ws.numel() < *need)
+    refuse(PyExc_ValueError, "workspace too small: %lld < %lld bytes", (long long)ws.numel(), (long long)*need);
+  need_device(ws, "workspace", &like);
+  *need = (size_t)ws.numel();
+  return ws;
+}
+
+// The caller's bf16 output of this shape or a fresh one; wrote() is what a call returns
+// for it.
+Tensor need_out(PyObject* o, const Tensor& like, std::initializer_list<int64_t> shape) {
+  if (o == Py_None) return fresh(like, shape, ScalarType::BFloat16);
+  const Tensor& out = tensor(o, "out", ScalarType::BFloat16, (int)shape.size(), &like);
+  need_shape(out, "out", shape);
+  return out;
+}
+PyObject* wrote(PyObject* o, const Tensor& out) {
+  if (o == Py_None) return THPVariable_Wrap(out);
+  if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+  Py_INCREF(o);
+  return o;
+}
+
 // x -> q, scale
 PyObject* quantize_rows(PyObject* const* a) {
   int code;
@@ -452,43 +496,66 @@ PyObject* fp8_gemm_fwd(PyObject* const* a) {
     refuse(PyExc_ValueError, "x has K=%lld but wq has K=%lld", (long long)K, (long long)w.size(2));
   const Tensor& ws_ = tensor(a[3], "w_scale", kE8M0, 3, &x);
   need_shape(ws_, "w_scale", {E, blocks(N), blocks(K)});
-  const Tensor& offs = any_tensor(a[4], "offs");
-  if (offs.scalar_type() != ScalarType::Int || offs.dim() != 1 || !offs.is_cuda())
-    refuse(PyExc_TypeError, "offs must be a 1-D int32 device tensor");
-  if (!offs.is_contiguous()) refuse(PyExc_ValueError, "offs must be contiguous");
-  need_device(offs, "offs", &x);
-  if (offs.size(0) != E && offs.size(0) != E + 1)
-    refuse(PyExc_ValueError, "offs has %lld entries; expected E=%lld (offs) or E+1 (m_indptr)",
-           (long long)offs.size(0), (long long)E);
-  const int32_t* op = ptr(offs);
-  op += offs.size(0) - E;  // (skips m_indptr's leading zero)
-  const bool given = a[5] != Py_None;
-  Tensor out;
-  if (given) {
-    out = tensor(a[5], "out", ScalarType::BFloat16, 2, &x);
-    need_shape(out, "out", {M, N});
-  } else {
-    out = fresh(x, {M, N}, ScalarType::BFloat16);
-  }
+  const int32_t* op = need_offs(a[4], E, x);
+  const Tensor out = need_out(a[5], x, {M, N});
   size_t need = g.grouped_fp8_gemm_fwd_workspace_bytes(M, N, K, size32(E), code);
-  Tensor ws;
-  if (a[6] == Py_None) {
-    ws = scratch(x, need);
-  } else {
-    ws = any_tensor(a[6], "workspace");
-    if (ws.scalar_type() != ScalarType::Byte || !ws.is_contiguous())
-      refuse(PyExc_ValueError, "workspace must be a contiguous uint8 tensor");
-    if ((size_t)ws.numel() < need)
-      refuse(PyExc_ValueError, "workspace too small: %lld < %lld bytes", (long long)ws.numel(), (long long)need);
-    need_device(ws, "workspace", &x);
-    need = (size_t)ws.numel();
-  }
+  const Tensor ws = need_workspace(a[6], &need, x);
   call("grouped_fp8_gemm_fwd", g.grouped_fp8_gemm_fwd, x, ptr(x), code, xs, ptr(w), ptr(ws_), op, ptr(out), M, N, K,
        size32(E), ptr(ws), need);
-  if (!given) return THPVariable_Wrap(out);
-  if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
-  Py_INCREF(a[5]);
-  return a[5];
+  return wrote(a[5], out);
+}
+
+// ---------------------------------------------------------------------------
+// the gated feed-forward
+// ---------------------------------------------------------------------------
+// x, w, offs, activation's code, keep, out or None, workspace or None -> h[, gate_up]
+PyObject* gated_fwd(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x", ScalarType::BFloat16, 2);
+  const Tensor& w = tensor(a[1], "w", ScalarType::BFloat16, 3, &x);
+  const int64_t M = x.size(0), K = x.size(1), E = w.size(0), F = w.size(1) / 2;
+  if (w.size(2) != K)
+    refuse(PyExc_ValueError, "x has K=%lld but w has K=%lld", (long long)K, (long long)w.size(2));
+  if (w.size(1) % 2) refuse(PyExc_ValueError, "w must have an even number of rows (gate and up), got %lld", (long long)w.size(1));
+  const int32_t* offs = need_offs(a[2], E, x);
+  const int act = (int)integer(a[3], "activation");
+  const bool keep = boolean(a[4], "keep");
+  const Tensor out = need_out(a[5], x, {M, F});
+  const Tensor kept = keep ? fresh(x, {M, 2 * F}, ScalarType::BFloat16) : Tensor();
+  size_t need = g.grouped_gated_gemm_fwd_workspace_bytes(M, F, K, size32(E));
+  const Tensor ws = need_workspace(a[6], &need, x);
+  call("grouped_gated_gemm_fwd", g.grouped_gated_gemm_fwd, x, ptr(x), ptr(w), offs, ptr(out), ptr(kept), act, M, F, K,
+       size32(E), ptr(ws), need);
+  PyObject* h = wrote(a[5], out);
+  if (!h) throw Raised();
+  PyObject* r = PyTuple_New(2);
+  PyObject* k = r ? (keep ? THPVariable_Wrap(kept) : (Py_INCREF(Py_None), Py_None)) : nullptr;
+  if (!k) {
+    Py_DECREF(h);
+    Py_XDECREF(r);
+    throw Raised();
+  }
+  PyTuple_SET_ITEM(r, 0, h);
+  PyTuple_SET_ITEM(r, 1, k);
+  return r;
+}
+
+// dy, w_down, gate_up, offs, activation's code, out or None, workspace or None -> dgate_up
+PyObject* gated_dgrad(PyObject* const* a) {
+  const Tensor& dy = tensor(a[0], "dy", ScalarType::BFloat16, 2);
+  const Tensor& w = tensor(a[1], "w_down", ScalarType::BFloat16, 3, &dy);
+  const int64_t M = dy.size(0), N = dy.size(1), E = w.size(0), F = w.size(2);
+  if (w.size(1) != N)
+    refuse(PyExc_ValueError, "dy has N=%lld but w_down has N=%lld", (long long)N, (long long)w.size(1));
+  const Tensor& gate_up = tensor(a[2], "gate_up", ScalarType::BFloat16, 2, &dy);
+  need_shape(gate_up, "gate_up", {M, 2 * F});
+  const int32_t* offs = need_offs(a[3], E, dy);
+  const int act = (int)integer(a[4], "activation");
+  const Tensor out = need_out(a[5], dy, {M, 2 * F});
+  size_t need = g.grouped_gated_gemm_dgrad_workspace_bytes(M, N, F, size32(E));
+  const Tensor ws = need_workspace(a[6], &need, dy);
+  call("grouped_gated_gemm_dgrad", g.grouped_gated_gemm_dgrad, dy, ptr(dy), ptr(w), ptr(gate_up), offs, ptr(out), act,
+       M, N, F, size32(E), ptr(ws), need);
+  return wrote(a[5], out);
 }
 
 // addresses of the entries by name, f(device index) -> stream, f(entry, status)
@@ -534,6 +601,7 @@ PyMethodDef methods[] = {METHOD(setup, 3),         METHOD(entries, 0),        ME
                          METHOD(route_bwd, 7),     METHOD(plan, 2),           METHOD(dispatch_fwd, 3),
                          METHOD(dispatch_bwd, 3),  METHOD(combine_fwd, 4),    METHOD(combine_bwd, 5),
                          METHOD(quantize_rows, 1), METHOD(quantize_weight, 2), METHOD(fp8_gemm_fwd, 7),
+                         METHOD(gated_fwd, 7),     METHOD(gated_dgrad, 7),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,33 @@
+// Internal interface between the C ABI (capi_gated.cpp) and the gfx950 kernels of
+// the experts' gated feed-forward (gated_kernels.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "grouped_gemm.h"
+
+namespace mdg {
+
+constexpr int kGatedCols = kTileJ / 2;  // hidden columns of a fwd tile: gate and up of each
+
+struct GatedParams {
+  // The product.  fwd: a = x, b = w, out = h, n = 2 f, k; dgrad: a = dy, b = w_down,
+  // out = dgate_up, n, k = f.
+  GemmParams g;
+  const uint16_t* gate_up;  // dgrad: [m_rows, 2 f] as fwd kept them
+  uint16_t* keep;           // fwd: [m_rows, 2 f] the projections, or nullptr
+  int32_t f;
+  float q0, q1;             // q(a) = a (q0 + q1 a^2) of the activation a s(q(a))
+};
+
+// Where a split tail unit's tile goes (written by the tile kernel, read by the
+// reduce kernel; in place of GemmParams' TailUnit).
+struct GatedTail {
+  int32_t row0, f0, i_valid, f_valid;
+};
+
+hipError_t launch_gated(Op op, const GatedParams& p, int grid, hipStream_t s);
+hipError_t launch_gated_reduce(Op op, const GatedParams& p, int grid_x, int grid_y, hipStream_t s);
+
+}  // namespace mdg
