@@ -482,6 +482,74 @@ MDG_API mdg_status grouped_gated_gemm_dgrad(const void* dy, const void* w_down, 
                                             int64_t n, int64_t f, int32_t num_groups, void* workspace,
                                             size_t workspace_bytes, void* stream);
 
+/*
+ * The norms before and after a block, with the block's gate and the scaled residual.  For
+ * token t, with rms(v) = sqrt(sum v^2 / hidden + eps):
+ *
+ *   z = y, or with post_weight y / rms(y) * post_weight
+ *   out = residual + scale gate[t] z                 (gate NULL: ones), rounded to dtype
+ *   normed = out / rms(out) * weight                 of out as rounded, with weight
+ *
+ *   residual, y, out, normed  [tokens, hidden] of dtype (MDG_BF16 or MDG_FP32).  y NULL: only the norm of
+ *                         the residual; post_weight, gate and out are NULL and weight is not.
+ *   weight, post_weight   [hidden] of weight_dtype, or NULL.
+ *   gate                  [tokens] fp32.
+ *   rstd, post_rstd       [tokens] fp32, written with weight / post_weight (else NULL): 1 / rms(out), 1 / rms(y).
+ *
+ * block_norm_bwd: the gradients for dout and dnormed (either may be NULL: zeros; not both),
+ * with out, rstd and post_rstd as the forward gave them (out: the residual where there was no y):
+ *   dresidual, dy         [tokens, hidden] of dtype, rounded once from fp32.
+ *   dweight, dpost_weight [hidden] of weight_dtype: sums over the tokens in fp32, rounded once.
+ *   dgate                 [tokens] fp32.
+ * Each may be NULL (not wanted).  out and rstd may be NULL without dnormed, y without post_weight and gate.
+ * workspace: block_norm_bwd_workspace_bytes() bytes, 256-byte aligned, where dweight or
+ * dpost_weight is wanted.  tokens == 0: both are zeros, nothing else is enqueued.
+ *
+ * hidden is a multiple of 8 up to 16384.  Rows, weights and their gradients are 16-byte
+ * aligned.  Sums are in fp32 in an order fixed by the sizes; a row whose squares overflow
+ * fp32 is divided by infinity.
+ */
+MDG_API mdg_status block_norm_fwd(const void* residual, const void* y, const void* weight, const void* post_weight,
+                                  const float* gate, void* out, void* normed, float* rstd, float* post_rstd,
+                                  int64_t tokens, int64_t hidden, int dtype, int weight_dtype, float scale, float eps,
+                                  void* stream);
+MDG_API size_t block_norm_bwd_workspace_bytes(int64_t tokens, int64_t hidden);
+MDG_API mdg_status block_norm_bwd(const void* dout, const void* dnormed, const void* out, const void* y,
+                                  const void* weight, const void* post_weight, const float* gate, const float* rstd,
+                                  const float* post_rstd, void* dresidual, void* dy, void* dweight, void* dpost_weight,
+                                  float* dgate, int64_t tokens, int64_t hidden, int dtype, int weight_dtype,
+                                  float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The norm of many gradients, sqrt(sum of g^2), and the gradients clipped by it.
+ *
+ *   gradients   `count` (up to 65536) tensors, in HOST memory, read before the call returns: data (read) and
+ *               out (written by grad_clip; out == data: in place) of `elements` values of dtype MDG_BF16 or
+ *               MDG_FP32 on the device, aligned to their type.  Pointers of empty tensors may be NULL.
+ *   norm        one fp32 value on the device, written: the norm, squares and sums in 64 bits.
+ *   norm_in     grad_clip: one fp32 value on the device to clip by; NULL: the gradients' norm, which
+ *               norm receives (norm is NULL otherwise).
+ *
+ * grad_clip: out = g * min(1, max_norm / (norm + 1e-6)), the factor rounded to fp32 and the
+ * product once to the type; max_norm >= 0.  A norm that is not finite counts as a factor of
+ * 1; with that factor a copy keeps every bit, and in place nothing is written.  Outputs share no
+ * memory with each other or with another tensor's data.
+ * workspace: grad_norm_workspace_bytes(count) bytes, 256-byte aligned (none with norm_in).
+ */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t elements;
+  int32_t dtype;
+  int32_t reserved;
+} mdg_gradient;
+
+MDG_API size_t grad_norm_workspace_bytes(int64_t count);
+MDG_API mdg_status grad_norm(const mdg_gradient* gradients, int64_t count, float* norm, void* workspace,
+                             size_t workspace_bytes, void* stream);
+MDG_API mdg_status grad_clip(const mdg_gradient* gradients, int64_t count, float max_norm, const float* norm_in,
+                             float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -58,3 +58,11 @@ from .gated import (  # noqa: F401
     grouped_gated_gemm_dgrad,
     grouped_gated_gemm_fwd,
 )
+from .norm import (  # noqa: F401
+    BlockNorm,
+    BlockNormGrads,
+    block_norm,
+    block_norm_bwd,
+    block_norm_fwd,
+)
+from .clip import clip_grads, grad_norm  # noqa: F401

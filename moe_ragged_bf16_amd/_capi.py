@@ -53,6 +53,12 @@ EXPORTED = (
     "grouped_gated_gemm_fwd_workspace_bytes",
     "grouped_gated_gemm_dgrad",
     "grouped_gated_gemm_dgrad_workspace_bytes",
+    "block_norm_fwd",
+    "block_norm_bwd",
+    "block_norm_bwd_workspace_bytes",
+    "grad_norm",
+    "grad_norm_workspace_bytes",
+    "grad_clip",
 )
 
 
@@ -62,6 +68,13 @@ class LaunchInfo(ctypes.Structure):
                 ("gemm_grid", ctypes.c_int32), ("dw_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
                 ("chunk_rows", ctypes.c_int32), ("tail_slots", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+class Gradient(ctypes.Structure):
+    """mdg_gradient of the C header."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("elements", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -127,7 +140,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.grouped_det_gemm_launch_info.argtypes = [vp, ctypes.POINTER(LaunchInfo)]
         lib.grouped_det_gemm_launch_free.restype = None
         lib.grouped_det_gemm_launch_free.argtypes = [vp]
-        st = ctypes.c_int
+        st, f32 = ctypes.c_int, ctypes.c_float
         for name, res, args in (
                 ("moe_route_fwd_workspace_bytes", sz, [i64, i32]),
                 ("moe_route_fwd", st, [vp, st, vp, vp, vp, vp, vp, vp, i64, i32, i32, st, vp, sz, vp]),
@@ -145,7 +158,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                 ("grouped_gated_gemm_fwd_workspace_bytes", sz, [i64, i64, i64, i32]),
                 ("grouped_gated_gemm_fwd", st, [vp, vp, vp, vp, vp, st, i64, i64, i64, i32, vp, sz, vp]),
                 ("grouped_gated_gemm_dgrad_workspace_bytes", sz, [i64, i64, i64, i32]),
-                ("grouped_gated_gemm_dgrad", st, [vp, vp, vp, vp, vp, st, i64, i64, i64, i32, vp, sz, vp])):
+                ("grouped_gated_gemm_dgrad", st, [vp, vp, vp, vp, vp, st, i64, i64, i64, i32, vp, sz, vp]),
+                ("block_norm_fwd", st, [vp] * 9 + [i64, i64, st, st, f32, f32, vp]),
+                ("block_norm_bwd_workspace_bytes", sz, [i64, i64]),
+                ("block_norm_bwd", st, [vp] * 14 + [i64, i64, st, st, f32, vp, sz, vp]),
+                ("grad_norm_workspace_bytes", sz, [i64]),
+                ("grad_norm", st, [ctypes.POINTER(Gradient), i64, vp, vp, sz, vp]),
+                ("grad_clip", st, [ctypes.POINTER(Gradient), i64, f32, vp, vp, vp, sz, vp])):
             f = getattr(lib, name)
             f.restype, f.argtypes = res, args
         _lib = lib

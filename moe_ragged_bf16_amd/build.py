@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoe_ragged_bf16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["grouped_gemm_kernels.hip", "moe_kernels.hip", "fp8_kernels.hip", "gated_kernels.hip",
-           "capi.cpp", "capi_moe.cpp", "capi_fp8.cpp", "capi_gated.cpp"]
+           "norm_kernels.hip", "clip_kernels.hip", "capi.cpp", "capi_moe.cpp", "capi_fp8.cpp", "capi_gated.cpp",
+           "capi_norm.cpp", "capi_clip.cpp"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950",

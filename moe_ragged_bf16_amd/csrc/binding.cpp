@@ -16,6 +16,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <exception>
 #include <string>
 #include <vector>
@@ -33,7 +34,8 @@ using at::Tensor;
   X(moe_dispatch_fwd) X(moe_dispatch_bwd) X(moe_combine_fwd) X(moe_combine_bwd) X(grouped_fp8_quantize_rows)   \
   X(grouped_fp8_quantize_weight) X(grouped_fp8_gemm_fwd_workspace_bytes) X(grouped_fp8_gemm_fwd)               \
   X(grouped_gated_gemm_fwd_workspace_bytes) X(grouped_gated_gemm_fwd)                                          \
-  X(grouped_gated_gemm_dgrad_workspace_bytes) X(grouped_gated_gemm_dgrad)
+  X(grouped_gated_gemm_dgrad_workspace_bytes) X(grouped_gated_gemm_dgrad) X(block_norm_fwd) X(block_norm_bwd)   \
+  X(block_norm_bwd_workspace_bytes) X(grad_norm_workspace_bytes) X(grad_norm) X(grad_clip)
 
 struct Entries {
 #define X(name) decltype(&::name) name = nullptr;
@@ -188,12 +190,14 @@ void call(const char* name, F entry, const Tensor& t, A... a) {
   if (st != MDG_OK) raise_status(name, st);
 }
 
+// (None for a tensor that is not there)
 template <class... T>
 PyObject* tuple(const T&... t) {
   PyObject* out = PyTuple_New(sizeof...(t));
   if (!out) throw Raised();
   Py_ssize_t i = 0;
-  const bool ok = ((PyTuple_SET_ITEM(out, i, THPVariable_Wrap(t)), PyTuple_GET_ITEM(out, i++) != nullptr) && ...);
+  const auto wrap = [](const Tensor& x) { return x.defined() ? THPVariable_Wrap(x) : (Py_INCREF(Py_None), Py_None); };
+  const bool ok = ((PyTuple_SET_ITEM(out, i, wrap(t)), PyTuple_GET_ITEM(out, i++) != nullptr) && ...);
   if (!ok) {
     Py_DECREF(out);
     throw Raised();
@@ -525,17 +529,13 @@ PyObject* gated_fwd(PyObject* const* a) {
   const Tensor ws = need_workspace(a[6], &need, x);
   call("grouped_gated_gemm_fwd", g.grouped_gated_gemm_fwd, x, ptr(x), ptr(w), offs, ptr(out), ptr(kept), act, M, F, K,
        size32(E), ptr(ws), need);
-  PyObject* h = wrote(a[5], out);
-  if (!h) throw Raised();
-  PyObject* r = PyTuple_New(2);
-  PyObject* k = r ? (keep ? THPVariable_Wrap(kept) : (Py_INCREF(Py_None), Py_None)) : nullptr;
-  if (!k) {
-    Py_DECREF(h);
-    Py_XDECREF(r);
-    throw Raised();
+  PyObject* r = tuple(out, kept);
+  if (a[5] != Py_None) {  // (the caller's own object)
+    PyObject* h = wrote(a[5], out);
+    PyObject* old = PyTuple_GET_ITEM(r, 0);
+    PyTuple_SET_ITEM(r, 0, h);
+    Py_DECREF(old);
   }
-  PyTuple_SET_ITEM(r, 0, h);
-  PyTuple_SET_ITEM(r, 1, k);
   return r;
 }
 
@@ -556,6 +556,203 @@ PyObject* gated_dgrad(PyObject* const* a) {
   call("grouped_gated_gemm_dgrad", g.grouped_gated_gemm_dgrad, dy, ptr(dy), ptr(w), ptr(gate_up), offs, ptr(out), act,
        M, N, F, size32(E), ptr(ws), need);
   return wrote(a[5], out);
+}
+
+// ---------------------------------------------------------------------------
+// the norms around a block
+// ---------------------------------------------------------------------------
+float real(PyObject* o, const char* name) {
+  const double v = PyFloat_Check(o) ? PyFloat_AS_DOUBLE(o) : PyLong_Check(o) && !PyBool_Check(o) ? PyLong_AsDouble(o) : NAN;
+  if (PyErr_Occurred()) throw Raised();
+  if (std::isnan(v)) refuse(PyExc_TypeError, "%s must be a number", name);
+  return (float)v;
+}
+
+// A tensor of the type and shape of the rows it goes with, or nothing.
+Tensor optional_rows(PyObject* o, const char* name, const Tensor& like) {
+  if (o == Py_None) return Tensor();
+  const Tensor& t = tensor(o, name, like.scalar_type(), 2, &like);
+  if (t.sizes() != like.sizes()) refuse(PyExc_ValueError, "%s must have shape %s", name, shape_name(like.sizes()).c_str());
+  return t;
+}
+Tensor optional_of_tokens(PyObject* o, const char* name, const Tensor& like) {
+  if (o == Py_None) return Tensor();
+  const Tensor& t = tensor(o, name, ScalarType::Float, 1, &like);
+  need_shape(t, name, {like.size(0)});
+  return t;
+}
+
+struct NormWeights {
+  Tensor weight, post_weight;
+  int code = MDG_FP32;
+};
+NormWeights need_norm_weights(PyObject* weight, PyObject* post_weight, const Tensor& like) {
+  NormWeights w;
+  int code[2];
+  if (weight != Py_None) {
+    w.weight = float_tensor(weight, "weight", 1, &code[0]);
+    need_device(w.weight, "weight", &like);
+    need_shape(w.weight, "weight", {like.size(1)});
+    w.code = code[0];
+  }
+  if (post_weight != Py_None) {
+    w.post_weight = float_tensor(post_weight, "post_weight", 1, &code[1]);
+    need_device(w.post_weight, "post_weight", &like);
+    need_shape(w.post_weight, "post_weight", {like.size(1)});
+    if (w.weight.defined() && code[0] != code[1])
+      refuse(PyExc_TypeError, "weight and post_weight must be of one type");
+    w.code = code[1];
+  }
+  return w;
+}
+
+// residual, y, weight, post_weight, gate (each but the first may be None), scale, eps -> out, normed, rstd, post_rstd
+PyObject* norm_fwd(PyObject* const* a) {
+  int code;
+  const Tensor& r = float_tensor(a[0], "residual", 2, &code);
+  const Tensor y = optional_rows(a[1], "y", r);
+  const NormWeights w = need_norm_weights(a[2], a[3], r);
+  const Tensor gate = optional_of_tokens(a[4], "gate", r);
+  const float scale = real(a[5], "scale"), eps = real(a[6], "eps");
+  if (!y.defined() && (w.post_weight.defined() || gate.defined()))
+    refuse(PyExc_ValueError, "post_weight and gate go with y");
+  if (!y.defined() && !w.weight.defined()) refuse(PyExc_ValueError, "without y a weight is needed");
+  const int64_t T = r.size(0), H = r.size(1);
+  Tensor out, normed, rstd, post_rstd;
+  if (y.defined()) out = fresh(r, {T, H}, r.scalar_type());
+  if (w.weight.defined()) {
+    normed = fresh(r, {T, H}, r.scalar_type());
+    rstd = fresh(r, {T}, ScalarType::Float);
+  }
+  if (w.post_weight.defined()) post_rstd = fresh(r, {T}, ScalarType::Float);
+  call("block_norm_fwd", g.block_norm_fwd, r, ptr(r), ptr(y), ptr(w.weight), ptr(w.post_weight), ptr(gate), ptr(out),
+       ptr(normed), ptr(rstd), ptr(post_rstd), T, H, code, w.code, scale, eps);
+  PyObject* got = tuple(out, normed, rstd, post_rstd);
+  if (!out.defined()) {  // (the residual itself)
+    PyObject* none = PyTuple_GET_ITEM(got, 0);
+    Py_INCREF(a[0]);
+    PyTuple_SET_ITEM(got, 0, a[0]);
+    Py_DECREF(none);
+  }
+  return got;
+}
+
+// dout, dnormed, out, rstd, post_rstd, y, weight, post_weight, gate, scale, what is wanted (bits)
+// -> dresidual, dy, dweight, dpost_weight, dgate
+PyObject* norm_bwd(PyObject* const* a) {
+  int code;
+  const Tensor& out = float_tensor(a[2], "norm.out", 2, &code);
+  const Tensor dout = optional_rows(a[0], "dout", out), dnormed = optional_rows(a[1], "dnormed", out);
+  if (!dout.defined() && !dnormed.defined()) refuse(PyExc_ValueError, "dout or dnormed is needed");
+  const Tensor rstd = optional_of_tokens(a[3], "norm.rstd", out), post_rstd = optional_of_tokens(a[4], "norm.post_rstd", out);
+  const Tensor y = optional_rows(a[5], "y", out);
+  const NormWeights w = need_norm_weights(a[6], a[7], out);
+  const Tensor gate = optional_of_tokens(a[8], "gate", out);
+  const float scale = real(a[9], "scale");
+  const int64_t need = integer(a[10], "need"), T = out.size(0), H = out.size(1);
+  if (dnormed.defined() && !w.weight.defined()) refuse(PyExc_ValueError, "dnormed goes with a weight");
+  if (w.weight.defined() != rstd.defined() || w.post_weight.defined() != post_rstd.defined())
+    refuse(PyExc_ValueError, "norm does not belong to these weights");
+  if ((w.post_weight.defined() || gate.defined()) && !y.defined()) refuse(PyExc_ValueError, "post_weight and gate go with y");
+  const ScalarType wt = w.code == MDG_FP32 ? ScalarType::Float : ScalarType::BFloat16;
+  Tensor dr, dy, dw, dp, dg;
+  if (need & 1) dr = fresh(out, {T, H}, out.scalar_type());
+  if (need & 2) dy = fresh(out, {T, H}, out.scalar_type());
+  if (need & 4) dw = fresh(out, {H}, wt);
+  if (need & 8) dp = fresh(out, {H}, wt);
+  if (need & 16) dg = fresh(out, {T}, ScalarType::Float);
+  const size_t bytes = (need & 12) ? g.block_norm_bwd_workspace_bytes(T, H) : 0;
+  const Tensor ws = scratch(out, bytes);
+  call("block_norm_bwd", g.block_norm_bwd, out, ptr(dout), ptr(dnormed), ptr(out), ptr(y), ptr(w.weight),
+       ptr(w.post_weight), ptr(gate), ptr(rstd), ptr(post_rstd), ptr(dr), ptr(dy), ptr(dw), ptr(dp), ptr(dg), T, H, code,
+       w.code, scale, ptr(ws), bytes);
+  return tuple(dr, dy, dw, dp, dg);
+}
+
+// ---------------------------------------------------------------------------
+// the gradients' norm and clipping
+// ---------------------------------------------------------------------------
+struct Items {  // a sequence's items, held while the call runs (a list could change meanwhile)
+  PyObject* items;
+  Items(PyObject* o, const char* name) {
+    if (THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a sequence of tensors, not one tensor", name);
+    items = PySequence_Tuple(o);
+    if (!items) throw Raised();
+  }
+  Items(const Items&) = delete;
+  ~Items() { Py_DECREF(items); }
+  Py_ssize_t size() const { return PyTuple_GET_SIZE(items); }
+  PyObject* operator[](Py_ssize_t i) const { return PyTuple_GET_ITEM(items, i); }
+};
+
+const Tensor& need_gradient(PyObject* o, const char* name, const Tensor* like, int* code) {
+  const Tensor& t = any_tensor(o, name);
+  *code = dtype_code(t, name);
+  if (t.layout() != at::kStrided) refuse(PyExc_ValueError, "%s must be dense", name);
+  need_device(t, name, like);
+  if (!t.is_non_overlapping_and_dense()) refuse(PyExc_ValueError, "%s must have no gaps or overlaps between its elements", name);
+  return t;
+}
+
+std::vector<mdg_gradient> need_gradients(const Items& grads) {
+  if (grads.size() == 0) refuse(PyExc_ValueError, "no gradients");
+  std::vector<mdg_gradient> list((size_t)grads.size());
+  const Tensor* like = nullptr;
+  for (Py_ssize_t i = 0; i < grads.size(); ++i) {
+    int code;
+    const Tensor& t = need_gradient(grads[i], "a gradient", like, &code);
+    if (!like) like = &t;
+    list[i] = mdg_gradient{t.data_ptr(), t.data_ptr(), t.numel(), code, 0};
+  }
+  return list;
+}
+
+// grads -> norm
+PyObject* grad_norm(PyObject* const* a) {
+  const Items grads(a[0], "grads");
+  const std::vector<mdg_gradient> list = need_gradients(grads);
+  const Tensor& first = THPVariable_Unpack(grads[0]);
+  const Tensor norm = fresh(first, {}, ScalarType::Float);
+  const size_t need = g.grad_norm_workspace_bytes((int64_t)list.size());
+  const Tensor ws = scratch(first, need);
+  call("grad_norm", g.grad_norm, first, list.data(), (int64_t)list.size(), (float*)ptr(norm), (void*)ptr(ws), need);
+  return THPVariable_Wrap(norm);
+}
+
+// grads, max_norm, norm or None, out or None -> norm
+PyObject* clip_grads(PyObject* const* a) {
+  const Items grads(a[0], "grads");
+  std::vector<mdg_gradient> list = need_gradients(grads);
+  const Tensor& first = THPVariable_Unpack(grads[0]);
+  const float max_norm = real(a[1], "max_norm");
+  if (max_norm < 0.0f) refuse(PyExc_ValueError, "max_norm must not be negative");
+  const bool given = a[2] != Py_None;
+  Tensor norm;
+  if (given) norm = tensor(a[2], "norm", ScalarType::Float, 0, &first);
+  const Items outs(a[3] == Py_None ? grads.items : a[3], "out");
+  if (a[3] != Py_None) {
+    if (outs.size() != grads.size())
+      refuse(PyExc_ValueError, "out has %zd tensors, grads has %zd", outs.size(), grads.size());
+    for (Py_ssize_t i = 0; i < outs.size(); ++i) {
+      int code;
+      const Tensor &t = need_gradient(outs[i], "an output", &first, &code), &x = THPVariable_Unpack(grads[i]);
+      if (t.scalar_type() != x.scalar_type() || t.sizes() != x.sizes() || t.strides() != x.strides())
+        refuse(PyExc_ValueError, "out[%zd] must have its gradient's type, shape and strides", i);
+      list[i].out = t.data_ptr();
+    }
+  }
+  if (!given) norm = fresh(first, {}, ScalarType::Float);
+  const size_t need = given ? 0 : g.grad_norm_workspace_bytes((int64_t)list.size());
+  const Tensor ws = scratch(first, need);
+  call("grad_clip", g.grad_clip, first, list.data(), (int64_t)list.size(), max_norm, given ? (float*)ptr(norm) : nullptr,
+       given ? nullptr : (float*)ptr(norm), (void*)ptr(ws), need);
+  for (Py_ssize_t i = 0; i < outs.size(); ++i) {
+    const Tensor& t = THPVariable_Unpack(outs[i]);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+  if (!given) return THPVariable_Wrap(norm);
+  Py_INCREF(a[2]);
+  return a[2];
 }
 
 // addresses of the entries by name, f(device index) -> stream, f(entry, status)
@@ -601,7 +798,8 @@ PyMethodDef methods[] = {METHOD(setup, 3),         METHOD(entries, 0),        ME
                          METHOD(route_bwd, 7),     METHOD(plan, 2),           METHOD(dispatch_fwd, 3),
                          METHOD(dispatch_bwd, 3),  METHOD(combine_fwd, 4),    METHOD(combine_bwd, 5),
                          METHOD(quantize_rows, 1), METHOD(quantize_weight, 2), METHOD(fp8_gemm_fwd, 7),
-                         METHOD(gated_fwd, 7),     METHOD(gated_dgrad, 7),
+                         METHOD(gated_fwd, 7),     METHOD(gated_dgrad, 7),    METHOD(norm_fwd, 7),
+                         METHOD(norm_bwd, 11),     METHOD(grad_norm, 1),      METHOD(clip_grads, 4),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,34 @@
+// Internal interface between the C ABI (capi_clip.cpp) and the gfx950 kernels of
+// the gradient norm and clipping (clip_kernels.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mdg {
+
+constexpr int kClipTensors = 128;       // tensors of one launch (its arguments stay below 4 KiB)
+constexpr int kClipUnitBytes = 32768;   // bytes of a tensor that a workgroup takes at a time
+constexpr int kClipBlocks = 1024;       // workgroups of a launch, at most
+
+// The tensors of one launch, by value.
+struct ClipTable {
+  const void* src[kClipTensors];
+  void* dst[kClipTensors];              // scaling only
+  int64_t elements[kClipTensors];       // the type in bit 0: 2 elements + (1: fp32)
+  int32_t count;
+  int32_t blocks;                       // of the norm kernel (and partial sums of this launch)
+  int32_t first;                        // partial sums of the launches before it
+  int32_t partials;                     // of all launches
+  double* partial;                      // [partials]
+  const float* norm_in;                 // scaling: the norm, or nullptr: from the partial sums
+  float* norm_out;                      // scaling and finishing: where the norm goes, or nullptr
+  float max_norm, eps;
+};
+static_assert(sizeof(ClipTable) <= 4096, "kernel arguments");
+
+hipError_t launch_clip_norm(const ClipTable& t, hipStream_t s);
+hipError_t launch_clip_finish(const ClipTable& t, hipStream_t s);
+hipError_t launch_clip_scale(const ClipTable& t, int blocks, hipStream_t s);
+
+}  // namespace mdg
