@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoe_ragged_bf16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["grouped_gemm_kernels.hip", "moe_kernels.hip", "fp8_kernels.hip", "gated_kernels.hip",
+SOURCES = ["grouped_gemm_kernels.hip", "moe_kernels.hip", "fp8_kernels.hip", "gated_kernels.hip", "gated_few_kernels.hip",
            "norm_kernels.hip", "clip_kernels.hip", "capi.cpp", "capi_moe.cpp", "capi_fp8.cpp", "capi_gated.cpp",
            "capi_norm.cpp", "capi_clip.cpp"]
 
@@ -215,19 +215,21 @@ def mfma_source_hazards(asm: str) -> list:
 # Wait states between a matrix instruction of 8 passes (the longest here: 16x16x128 in
 # 8 bits) and another instruction's access of its result: passes + 4 on gfx950.
 MFMA_RESULT_STATES = 12
+# and where it has 4 (what the compiler keeps for its own).
+MFMA_RESULT_STATES_OF = {"v_mfma_f32_16x16x32_bf16": 8}
 
 
 def mfma_result_hazards(asm: str) -> list:
     """Accesses of a matrix instruction's result that come before it is there: by
     another instruction than a matrix instruction that accumulates onto all of it
-    (which the hardware waits for), within MFMA_RESULT_STATES."""
+    (which the hardware waits for), within that many wait states."""
     bad = []
     for f in _functions(asm):
         for i, ins in enumerate(f):
             if not ins.mfma:
                 continue
             result = ins.operands[0]
-            for r in _within(f, i, MFMA_RESULT_STATES, "next"):
+            for r in _within(f, i, MFMA_RESULT_STATES_OF.get(ins.name, MFMA_RESULT_STATES), "next"):
                 if r.mfma and r.operands[3] == result and not result & set().union(*r.operands[1:3]) and \
                         (r.operands[0] == result or not r.operands[0] & result):
                     continue

@@ -45,24 +45,66 @@ size_t workspace_of(Op op, int64_t m_rows, int64_t n, int64_t f, int32_t num_gro
   return (size_t)kTailHeadBytes + (size_t)slots_of(units_of(op, m_rows, f, num_groups)) * kTileI * kTileJ * sizeof(float);
 }
 
+enum Kernel { kSmall, kMid, kTile };
+
+// Which kernel takes a launch (one takes all of its groups).  The rules go by the most
+// groups that can have rows, as offs is not read here.  Times in us, weights from memory.
+Kernel kernel_of(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, int64_t cus) {
+  if (op == kFwd) {
+    // Few rows: the small kernel starts and ends faster and fills the GPU where the middle
+    // one has too few tiles; with more rows it reads weights again for each 64 of them and
+    // x through the caches, and with many units the middle kernel streams as well.  Small
+    // against middle: 16 rows of one group of 2 x 4096 x 4096 20 / 42, 30 of 2 x 8192 x 4096
+    // 41 / 46, 64 of them 62 / 48; 100 over 8 of 2 x 512 x 1024 8 / 13; 40 over 8 of 2 x 2048 x
+    // 2048 30 / 35, 200 42 / 35; 2 over 8 of 2 x 14336 x 4096 84 / 92, 16 310 / 303; 512 over 64
+    // of 2 x 1536 x 2048 152 / 140.
+    const int64_t units = (active + m_rows / kGatedSmallRows) * ((f + kGatedSmallCols - 1) / kGatedSmallCols);
+    if ((m_rows <= 32 * active && units <= 2 * cus) || (m_rows <= 16 * active && units <= 8 * cus)) return kSmall;
+    // Groups that fill a 256-row tile on average: the tile kernel.  Middle against tile: 64
+    // groups of 2 x 1536 x 2048, 128 rows on average 200 / 226, 256 rows 295 / 289; 4 and 8 of
+    // 2 x 4096 x 4096, 500 rows 175 / 163 and 329 / 287; 16 of 2 x 1000 x 2000, 188 rows 63 / 80.
+    return m_rows < 256 * active ? kMid : kTile;
+  }
+  // dgrad, whose tiles have twice the hidden columns.  Middle against tile: 64 groups of
+  // 2048 x 1536, 64 rows on average 113 / 131, 128 rows 147 / 144, 256 rows 198 / 187; 16 of 2000 x
+  // 1000, 188 rows 49 / 44; 8 of 1024 x 512, 125 rows 20 / 30.  Where the middle kernel's tiles leave
+  // CUs idle, it takes 0.9 us for each 64 of n; the tile kernel cuts n: one group of
+  // 4096 x 4096, 300 rows 58 / 43.
+  const int64_t tiles = (m_rows / kGatedMidTile + active) * ((f + kGatedMidTile - 1) / kGatedMidTile);
+  if (tiles < cus) return n <= 2048 ? kMid : kTile;
+  return m_rows < 96 * active ? kMid : kTile;
+}
+
 int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, void* workspace, void* stream) {
   DeviceInfo dev;
   int device = -1;
   const int st = query_device(&dev, &device);
   if (st != MDG_OK) return st;
   if (!dev.gfx950) return MDG_EUNSUPPORTED;
-  const int64_t units = units_of(op, m_rows, f, num_groups), slots = slots_of(units);
-  char* ws = static_cast<char*>(workspace);
-  p->g.tail_head = reinterpret_cast<int32_t*>(ws);
-  p->g.partial = reinterpret_cast<float*>(ws + kTailHeadBytes);
-  p->g.tail_slots = (int32_t)slots;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  int64_t grid = std::min<int64_t>(units + slots, dev.cus > 0 ? dev.cus : 256);
-  if (grid >= 8) grid -= grid % 8;
-  if (launch_gated(op, *p, (int)grid, s) != hipSuccess) return MDG_EHIP;
-  if (slots < 2) return MDG_OK;
-  const int reduce = (int)std::min<int64_t>(kBalanceSlots / 2, slots / 2);
-  return launch_gated_reduce(op, *p, 8, reduce, s) == hipSuccess ? MDG_OK : MDG_EHIP;
+  const int64_t cus = dev.cus > 0 ? dev.cus : 256, active = std::min<int64_t>(num_groups, m_rows);
+  const int64_t cols = op == kFwd ? kGatedMidTile / 2 : kGatedMidTile;
+  const int64_t mid = ((m_rows + kGatedMidTile - 1) / kGatedMidTile + active) * ((f + cols - 1) / cols);
+  Kernel which = kernel_of(op, m_rows, p->g.n, f, active, cus);
+  if (which == kMid && (mid + 7) / 8 * 8 * 256 > UINT32_MAX) which = kTile;  // (a launch's work-items)
+  hipError_t err = hipSuccess;
+  if (which == kSmall) {
+    err = launch_gated_small(*p, (int)(active + m_rows / kGatedSmallRows), s);
+  } else if (which == kMid) {
+    err = launch_gated_mid(op, *p, (int)((mid + 7) / 8 * 8), s);
+  } else {
+    const int64_t units = units_of(op, m_rows, f, num_groups), slots = slots_of(units);
+    char* ws = static_cast<char*>(workspace);
+    p->g.tail_head = reinterpret_cast<int32_t*>(ws);
+    p->g.partial = reinterpret_cast<float*>(ws + kTailHeadBytes);
+    p->g.tail_slots = (int32_t)slots;
+    int64_t grid = std::min<int64_t>(units + slots, cus);
+    if (grid >= 8) grid -= grid % 8;
+    err = launch_gated(op, *p, (int)grid, s);
+    if (err == hipSuccess && slots >= 2)
+      err = launch_gated_reduce(op, *p, 8, (int)std::min<int64_t>(kBalanceSlots / 2, slots / 2), s);
+  }
+  return err == hipSuccess ? MDG_OK : MDG_EHIP;
 }
 
 int check_workspace(const void* workspace, size_t bytes, size_t need) {

@@ -11,6 +11,10 @@ namespace mdg {
 
 constexpr int kGatedCols = kTileJ / 2;  // hidden columns of a fwd tile: gate and up of each
 
+constexpr int kGatedSmallCols = 16;         // hidden columns of the small kernel's units
+constexpr int kGatedSmallRows = 64;         // and their rows, at most
+constexpr int kGatedMidTile = 128;          // rows, and columns of operand B, of the middle kernel's tiles
+
 struct GatedParams {
   // The product.  fwd: a = x, b = w, out = h, n = 2 f, k; dgrad: a = dy, b = w_down,
   // out = dgate_up, n, k = f.
@@ -28,6 +32,8 @@ struct GatedTail {
 };
 
 hipError_t launch_gated(Op op, const GatedParams& p, int grid, hipStream_t s);
+hipError_t launch_gated_small(const GatedParams& p, int pieces, hipStream_t s);  // fwd
+hipError_t launch_gated_mid(Op op, const GatedParams& p, int grid, hipStream_t s);
 hipError_t launch_gated_reduce(Op op, const GatedParams& p, int grid_x, int grid_y, hipStream_t s);
 
 }  // namespace mdg
