@@ -35,7 +35,10 @@ using at::Tensor;
   X(grouped_fp8_quantize_weight) X(grouped_fp8_gemm_fwd_workspace_bytes) X(grouped_fp8_gemm_fwd)               \
   X(grouped_gated_gemm_fwd_workspace_bytes) X(grouped_gated_gemm_fwd)                                          \
   X(grouped_gated_gemm_dgrad_workspace_bytes) X(grouped_gated_gemm_dgrad) X(block_norm_fwd) X(block_norm_bwd)   \
-  X(block_norm_bwd_workspace_bytes) X(grad_norm_workspace_bytes) X(grad_norm) X(grad_clip)
+  X(block_norm_bwd_workspace_bytes) X(grad_norm_workspace_bytes) X(grad_norm) X(grad_clip)                     \
+  X(grouped_det_gemm_fwd_workspace_bytes) X(grouped_det_gemm_fwd) X(grouped_det_gemm_dgrad_workspace_bytes)    \
+  X(grouped_det_gemm_dgrad) X(grouped_det_gemm_wgrad_workspace_bytes) X(grouped_det_gemm_wgrad)                \
+  X(grouped_det_gemm_zero_pad_rows)
 
 struct Entries {
 #define X(name) decltype(&::name) name = nullptr;
@@ -512,23 +515,41 @@ PyObject* fp8_gemm_fwd(PyObject* const* a) {
 // ---------------------------------------------------------------------------
 // the gated feed-forward
 // ---------------------------------------------------------------------------
-// x, w, offs, activation's code, keep, out or None, workspace or None -> h[, gate_up]
+// h (and gate_up) of operands that are known to fit; `out`, `ws_given`: the caller's, or None.
+Tensor gated_h(const Tensor& x, const Tensor& w, const int32_t* offs, int act, bool keep, Tensor* kept,
+               PyObject* out = Py_None, PyObject* ws_given = Py_None) {
+  const int64_t M = x.size(0), K = x.size(1), E = w.size(0), F = w.size(1) / 2;
+  const Tensor h = need_out(out, x, {M, F});
+  if (keep) *kept = fresh(x, {M, 2 * F}, ScalarType::BFloat16);
+  size_t need = g.grouped_gated_gemm_fwd_workspace_bytes(M, F, K, size32(E));
+  const Tensor ws = need_workspace(ws_given, &need, x);
+  call("grouped_gated_gemm_fwd", g.grouped_gated_gemm_fwd, x, ptr(x), ptr(w), offs, ptr(h), ptr(*kept), act, M, F, K,
+       size32(E), ptr(ws), need);
+  return h;
+}
+Tensor gated_d(const Tensor& dy, const Tensor& w, const Tensor& gate_up, const int32_t* offs, int act, Tensor out,
+               PyObject* ws_given = Py_None) {
+  const int64_t M = dy.size(0), N = dy.size(1), E = w.size(0), F = w.size(2);
+  if (!out.defined()) out = fresh(dy, {M, 2 * F}, ScalarType::BFloat16);
+  size_t need = g.grouped_gated_gemm_dgrad_workspace_bytes(M, N, F, size32(E));
+  const Tensor ws = need_workspace(ws_given, &need, dy);
+  call("grouped_gated_gemm_dgrad", g.grouped_gated_gemm_dgrad, dy, ptr(dy), ptr(w), ptr(gate_up), offs, ptr(out), act,
+       M, N, F, size32(E), ptr(ws), need);
+  return out;
+}
+
+// x, w, offs, activation's code, keep, out or None, workspace or None -> h, gate_up (None unless kept)
 PyObject* gated_fwd(PyObject* const* a) {
   const Tensor& x = tensor(a[0], "x", ScalarType::BFloat16, 2);
   const Tensor& w = tensor(a[1], "w", ScalarType::BFloat16, 3, &x);
-  const int64_t M = x.size(0), K = x.size(1), E = w.size(0), F = w.size(1) / 2;
-  if (w.size(2) != K)
-    refuse(PyExc_ValueError, "x has K=%lld but w has K=%lld", (long long)K, (long long)w.size(2));
+  if (w.size(2) != x.size(1))
+    refuse(PyExc_ValueError, "x has K=%lld but w has K=%lld", (long long)x.size(1), (long long)w.size(2));
   if (w.size(1) % 2) refuse(PyExc_ValueError, "w must have an even number of rows (gate and up), got %lld", (long long)w.size(1));
-  const int32_t* offs = need_offs(a[2], E, x);
+  const int32_t* offs = need_offs(a[2], w.size(0), x);
   const int act = (int)integer(a[3], "activation");
   const bool keep = boolean(a[4], "keep");
-  const Tensor out = need_out(a[5], x, {M, F});
-  const Tensor kept = keep ? fresh(x, {M, 2 * F}, ScalarType::BFloat16) : Tensor();
-  size_t need = g.grouped_gated_gemm_fwd_workspace_bytes(M, F, K, size32(E));
-  const Tensor ws = need_workspace(a[6], &need, x);
-  call("grouped_gated_gemm_fwd", g.grouped_gated_gemm_fwd, x, ptr(x), ptr(w), offs, ptr(out), ptr(kept), act, M, F, K,
-       size32(E), ptr(ws), need);
+  Tensor kept;
+  const Tensor out = gated_h(x, w, offs, act, keep, &kept, a[5], a[6]);
   PyObject* r = tuple(out, kept);
   if (a[5] != Py_None) {  // (the caller's own object)
     PyObject* h = wrote(a[5], out);
@@ -543,19 +564,96 @@ PyObject* gated_fwd(PyObject* const* a) {
 PyObject* gated_dgrad(PyObject* const* a) {
   const Tensor& dy = tensor(a[0], "dy", ScalarType::BFloat16, 2);
   const Tensor& w = tensor(a[1], "w_down", ScalarType::BFloat16, 3, &dy);
-  const int64_t M = dy.size(0), N = dy.size(1), E = w.size(0), F = w.size(2);
-  if (w.size(1) != N)
-    refuse(PyExc_ValueError, "dy has N=%lld but w_down has N=%lld", (long long)N, (long long)w.size(1));
+  const int64_t M = dy.size(0), F = w.size(2);
+  if (w.size(1) != dy.size(1))
+    refuse(PyExc_ValueError, "dy has N=%lld but w_down has N=%lld", (long long)dy.size(1), (long long)w.size(1));
   const Tensor& gate_up = tensor(a[2], "gate_up", ScalarType::BFloat16, 2, &dy);
   need_shape(gate_up, "gate_up", {M, 2 * F});
-  const int32_t* offs = need_offs(a[3], E, dy);
+  const int32_t* offs = need_offs(a[3], w.size(0), dy);
   const int act = (int)integer(a[4], "activation");
   const Tensor out = need_out(a[5], dy, {M, 2 * F});
-  size_t need = g.grouped_gated_gemm_dgrad_workspace_bytes(M, N, F, size32(E));
-  const Tensor ws = need_workspace(a[6], &need, dy);
-  call("grouped_gated_gemm_dgrad", g.grouped_gated_gemm_dgrad, dy, ptr(dy), ptr(w), ptr(gate_up), offs, ptr(out), act,
-       M, N, F, size32(E), ptr(ws), need);
+  gated_d(dy, w, gate_up, offs, act, out, a[6]);
   return wrote(a[5], out);
+}
+
+// The products of the block's other steps, on operands that are known to fit.
+Tensor det_fwd(const Tensor& x, const Tensor& w, const int32_t* offs) {
+  const int64_t M = x.size(0), E = w.size(0), N = w.size(1), K = w.size(2);
+  const Tensor y = fresh(x, {M, N}, ScalarType::BFloat16);
+  const size_t need = g.grouped_det_gemm_fwd_workspace_bytes(M, N, K, size32(E));
+  const Tensor ws = scratch(x, need);
+  call("grouped_det_gemm_fwd", g.grouped_det_gemm_fwd, x, ptr(x), ptr(w), offs, ptr(y), M, N, K, size32(E), ptr(ws), need);
+  return y;
+}
+Tensor det_dgrad(const Tensor& d, const Tensor& w, const int32_t* offs) {
+  const int64_t M = d.size(0), E = w.size(0), N = w.size(1), K = w.size(2);
+  const Tensor dx = fresh(d, {M, K}, ScalarType::BFloat16);
+  const size_t need = g.grouped_det_gemm_dgrad_workspace_bytes(M, N, K, size32(E));
+  const Tensor ws = scratch(d, need);
+  call("grouped_det_gemm_dgrad", g.grouped_det_gemm_dgrad, d, ptr(d), ptr(w), offs, ptr(dx), M, N, K, size32(E), ptr(ws),
+       need);
+  return dx;
+}
+Tensor det_wgrad(const Tensor& d, const Tensor& x, int64_t E, const int32_t* offs) {
+  const int64_t M = d.size(0), N = d.size(1), K = x.size(1);
+  const Tensor dw = fresh(d, {E, N, K}, ScalarType::BFloat16);
+  const size_t need = g.grouped_det_gemm_wgrad_workspace_bytes(M, N, K, size32(E));
+  const Tensor ws = scratch(d, need);
+  call("grouped_det_gemm_wgrad", g.grouped_det_gemm_wgrad, d, ptr(d), ptr(x), offs, ptr(dw), (int)MDG_BF16, 0, M, N, K,
+       size32(E), ptr(ws), need);
+  return dw;
+}
+void zero_rows(const Tensor& t, int64_t E, const int32_t* offs) {
+  call("grouped_det_gemm_zero_pad_rows", g.grouped_det_gemm_zero_pad_rows, t, ptr(t), offs, t.size(0), t.size(1) * 2,
+       size32(E));
+}
+
+// x, w, w_down, offs, activation's code, keep -> y (zeros in rows of no group), h, gate_up (None unless kept)
+PyObject* ffn_fwd(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x", ScalarType::BFloat16, 2);
+  const Tensor& w = tensor(a[1], "w_gate_up", ScalarType::BFloat16, 3, &x);
+  const Tensor& w2 = tensor(a[2], "w_down", ScalarType::BFloat16, 3, &x);
+  const int64_t E = w.size(0), F = w2.size(2);
+  if (w.size(2) != x.size(1))
+    refuse(PyExc_ValueError, "x has K=%lld but w_gate_up has K=%lld", (long long)x.size(1), (long long)w.size(2));
+  if (w2.size(0) != E || w.size(1) != 2 * F)
+    refuse(PyExc_ValueError, "w_gate_up %s and w_down %s do not belong together: [E, 2 F, K] and [E, N, F]",
+           shape_name(w.sizes()).c_str(), shape_name(w2.sizes()).c_str());
+  const int32_t* offs = need_offs(a[3], E, x);
+  const int act = (int)integer(a[4], "activation");
+  const bool keep = boolean(a[5], "keep");
+  Tensor kept;
+  const Tensor h = gated_h(x, w, offs, act, keep, &kept);
+  const Tensor y = det_fwd(h, w2, offs);
+  zero_rows(y, E, offs);
+  return keep ? tuple(y, h, kept) : tuple(y, Tensor(), Tensor());
+}
+
+// dy, w_down, gate_up, offs, activation's code, x, w, h, what is wanted (1: dx, 2: dw, 4: dw_down; 8: dgate_up)
+// -> dx (zeros in rows of no group), dw, dw_down, dgate_up
+PyObject* ffn_bwd(PyObject* const* a) {
+  const Tensor& dy = tensor(a[0], "the output gradient", ScalarType::BFloat16, 2);
+  const Tensor& w2 = tensor(a[1], "w_down", ScalarType::BFloat16, 3, &dy);
+  const Tensor& gate_up = tensor(a[2], "gate_up", ScalarType::BFloat16, 2, &dy);
+  const Tensor& x = tensor(a[5], "x", ScalarType::BFloat16, 2, &dy);
+  const Tensor& w = tensor(a[6], "w_gate_up", ScalarType::BFloat16, 3, &dy);
+  const Tensor& h = tensor(a[7], "h", ScalarType::BFloat16, 2, &dy);
+  const int64_t M = dy.size(0), E = w2.size(0), F = w2.size(2), want = integer(a[8], "need");
+  need_shape(dy, "the output gradient", {x.size(0), w2.size(1)});
+  need_shape(gate_up, "gate_up", {M, 2 * F});
+  need_shape(h, "h", {M, F});
+  need_shape(w, "w_gate_up", {E, 2 * F, x.size(1)});
+  const int32_t* offs = need_offs(a[3], E, dy);
+  const int act = (int)integer(a[4], "activation");
+  Tensor d, dx, dw, dw2;
+  if (want & 11) d = gated_d(dy, w2, gate_up, offs, act, Tensor());
+  if (want & 1) {
+    dx = det_dgrad(d, w, offs);
+    zero_rows(dx, E, offs);
+  }
+  if (want & 2) dw = det_wgrad(d, x, E, offs);
+  if (want & 4) dw2 = det_wgrad(dy, h, E, offs);
+  return tuple(dx, dw, dw2, (want & 8) ? d : Tensor());
 }
 
 // ---------------------------------------------------------------------------
@@ -800,6 +898,7 @@ PyMethodDef methods[] = {METHOD(setup, 3),         METHOD(entries, 0),        ME
                          METHOD(quantize_rows, 1), METHOD(quantize_weight, 2), METHOD(fp8_gemm_fwd, 7),
                          METHOD(gated_fwd, 7),     METHOD(gated_dgrad, 7),    METHOD(norm_fwd, 7),
                          METHOD(norm_bwd, 11),     METHOD(grad_norm, 1),      METHOD(clip_grads, 4),
+                         METHOD(ffn_fwd, 6),       METHOD(ffn_bwd, 9),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

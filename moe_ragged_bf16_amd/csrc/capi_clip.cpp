@@ -20,8 +20,8 @@ constexpr int64_t kMaxTensors = 65536;
 constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of a tensor: a launch's units stay below 2^31
 
 int64_t bytes_of(const mdg_gradient& g) { return g.elements * (g.dtype == MDG_FP32 ? 4 : 2); }
-int64_t launches_of(int64_t count) { return (count + kClipTensors - 1) / kClipTensors; }
-size_t workspace_of(int64_t count) { return (size_t)launches_of(count) * kClipBlocks * sizeof(double); }
+int64_t launches_of(int64_t count, bool apart) { return (count + clip_tensors(apart) - 1) / clip_tensors(apart); }
+size_t workspace_of(int64_t count) { return (size_t)launches_of(count, false) * kClipBlocks * sizeof(double); }
 
 int check_device() {
   DeviceInfo dev;
@@ -70,16 +70,20 @@ int check_outputs(const mdg_gradient* g, int64_t count, const Range (&others)[3]
   return MDG_OK;
 }
 
-// The tensors of launch `k`; `blocks` the workgroups its units fill.
-ClipTable table_of(const mdg_gradient* g, int64_t count, int64_t k, bool scaled) {
+// The tensors of launch `k`, with the outputs where they are apart; `blocks` the
+// workgroups its units fill.
+ClipTable table_of(const mdg_gradient* g, int64_t count, int64_t k, bool apart) {
   ClipTable t{};
+  const int capacity = clip_tensors(apart);
   int64_t units = 0;
-  for (int64_t i = k * kClipTensors; i < std::min(count, (k + 1) * kClipTensors); ++i) {
-    t.src[t.count] = g[i].data;
-    if (scaled) t.dst[t.count] = g[i].out;
-    t.elements[t.count++] = 2 * g[i].elements + (g[i].dtype == MDG_FP32);
+  for (int64_t i = k * capacity; i < std::min(count, (k + 1) * capacity); ++i) {
+    t.words[t.count] = reinterpret_cast<uint64_t>(g[i].data);
+    t.words[capacity + t.count] = 2 * (uint64_t)g[i].elements + (g[i].dtype == MDG_FP32);
+    if (apart) t.words[2 * capacity + t.count] = reinterpret_cast<uint64_t>(g[i].out);
+    ++t.count;
     units += (bytes_of(g[i]) + kClipUnitBytes - 1) / kClipUnitBytes;
   }
+  t.apart = apart;
   t.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(units, kClipBlocks));
   return t;
 }
@@ -87,7 +91,7 @@ ClipTable table_of(const mdg_gradient* g, int64_t count, int64_t k, bool scaled)
 // Enqueues the norm's launches; `last` gets what reads their sums.
 int enqueue_norm(const mdg_gradient* g, int64_t count, double* partial, hipStream_t s, int32_t* partials) {
   int32_t first = 0;
-  for (int64_t k = 0; k < launches_of(count); ++k) {
+  for (int64_t k = 0; k < launches_of(count, false); ++k) {
     ClipTable t = table_of(g, count, k, false);
     t.partial = partial;
     t.first = first;
@@ -158,9 +162,11 @@ MDG_API mdg_status grad_clip(const mdg_gradient* gradients, int64_t count, float
   double* partial = static_cast<double*>(workspace);
   int32_t partials = 0;
   if (!norm_in && (st = enqueue_norm(gradients, count, partial, s, &partials)) != MDG_OK) return status(st);
-  const int64_t launches = std::max<int64_t>(1, launches_of(count));  // (without tensors: the norm, 0)
+  bool apart = false;
+  for (int64_t i = 0; i < count; ++i) apart = apart || (gradients[i].elements > 0 && gradients[i].out != gradients[i].data);
+  const int64_t launches = std::max<int64_t>(1, launches_of(count, apart));  // (without tensors: the norm, 0)
   for (int64_t k = launches - 1; k >= 0; --k) {
-    ClipTable t = table_of(gradients, count, k, true);
+    ClipTable t = table_of(gradients, count, k, apart);
     if (norm_in && t.count == 0) return status(MDG_OK);
     t.partial = partial;
     t.partials = partials;

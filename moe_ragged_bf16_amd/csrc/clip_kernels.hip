@@ -2,7 +2,7 @@
 //
 //   norm = sqrt(sum over all tensors of g^2),  g' = g min(1, max_norm / (norm + eps))
 //
-// A launch takes up to 128 tensors by value in its arguments, so nothing is copied to
+// A launch takes up to 246 tensors by value in its arguments, so nothing is copied to
 // the device and a captured launch keeps its tensors.  Each tensor is cut into units
 // of 32 KiB; a workgroup walks units b, b + grid, ..., so the sums' order is a function of
 // the sizes.  Squares and sums are in 64 bits: no square of an fp32 value overflows or
@@ -24,56 +24,65 @@ constexpr int kSteps = kClipUnitBytes / (kClipThreads * 16);  // 16-byte pieces 
 // 16 bytes that start on an element (tensors may start anywhere in a flat buffer).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// Units of the table's tensors before each one, in LDS; returns their number.
-__device__ int clip_units(const ClipTable& t, int* before, int* scratch) {
+// Addresses come from a table: their memory is said here, or accesses would be flat ones.
+typedef __attribute__((address_space(1))) uint8_t gbyte;
+typedef __attribute__((address_space(1))) uint16_t ghalf;
+typedef __attribute__((address_space(1))) float gfloat;
+typedef __attribute__((address_space(1))) u32x4_any gpiece;
+
+// The table in LDS: addresses, sizes (2 elements + (1: fp32)) and the units of the
+// tensors before each one.
+struct ClipLds {
+  uint64_t src[clip_tensors(false)], dst[clip_tensors(false)], elements[clip_tensors(false)];
+  int before[clip_tensors(false) + 1];
+  int scratch[4];
+};
+static_assert(clip_tensors(false) <= kClipThreads, "a thread for every tensor");
+
+// Fills it; returns the number of units.
+__device__ __forceinline__ int clip_units(const ClipTable& t, ClipLds& s) {
+  const int i = threadIdx.x, capacity = clip_tensors(t.apart);
   int units = 0;
-  if ((int)threadIdx.x < t.count) {
-    const int64_t n = t.elements[threadIdx.x];
-    units = (int)(((n >> 1) * ((n & 1) ? 4 : 2) + kClipUnitBytes - 1) / kClipUnitBytes);
+  if (i < t.count) {
+    const uint64_t src = t.words[i], n = t.words[capacity + i];
+    s.src[i] = src;
+    s.elements[i] = n;
+    s.dst[i] = t.apart ? t.words[2 * capacity + i] : src;
+    units = (int)(((int64_t)(n >> 1) * ((n & 1) ? 4 : 2) + kClipUnitBytes - 1) / kClipUnitBytes);
   }
   int total;
-  const int b = block_excl_sum(units, scratch, &total);
-  if ((int)threadIdx.x < t.count) before[threadIdx.x] = b;
-  if (threadIdx.x == 0) before[t.count] = total;
+  const int b = block_excl_sum(units, s.scratch, &total);
+  if (i < t.count) s.before[i] = b;
+  if (i == 0) s.before[t.count] = total;
   __syncthreads();
   return total;
 }
 
-// One unit: where it starts in its tensor and how many bytes it has.
+// One unit: its tensor, where it starts and how many bytes it has.
 struct ClipUnit {
-  int tensor;
+  const gbyte* src;
+  gbyte* dst;
   bool fp32;
-  int64_t at;
   int bytes;
 };
-__device__ __forceinline__ ClipUnit clip_unit(const ClipTable& t, const int* before, int u) {
+__device__ __forceinline__ ClipUnit clip_unit(const ClipTable& t, const ClipLds& s, int u) {
   ClipUnit x;
-  x.tensor = uniform(find_group(before, t.count, u));
-  const int64_t n = t.elements[x.tensor];
-  x.fp32 = n & 1;
-  x.at = (int64_t)(u - uniform(before[x.tensor])) * kClipUnitBytes;
-  const int64_t left = (n >> 1) * (x.fp32 ? 4 : 2) - x.at;
-  x.bytes = (int)(left < kClipUnitBytes ? left : kClipUnitBytes);
+  const int i = uniform(find_group(s.before, t.count, u));
+  const uint64_t n = s.elements[i];
+  x.fp32 = uniform((int)(n & 1));
+  const int64_t at = (int64_t)(u - s.before[i]) * kClipUnitBytes;
+  const int64_t left = (int64_t)(n >> 1) * (x.fp32 ? 4 : 2) - at;
+  x.bytes = uniform((int)(left < kClipUnitBytes ? left : kClipUnitBytes));
+  x.src = reinterpret_cast<const gbyte*>(s.src[i]) + at;
+  x.dst = reinterpret_cast<gbyte*>(s.dst[i]) + at;
   return x;
 }
 
-__device__ __forceinline__ u32x4 load_any(const uint8_t* p) { return *reinterpret_cast<const u32x4_any*>(p); }
-// The first `bytes` (below 16) of a piece, zeros behind.
-__device__ __forceinline__ u32x4 load_tail(const uint8_t* p, int bytes) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (2 * i < bytes) v[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-  return v;
-}
-__device__ __forceinline__ void store_tail(uint8_t* p, const u32x4& v, int bytes) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (2 * i < bytes) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-}
+__device__ __forceinline__ u32x4 load_any(const gbyte* p) { return *reinterpret_cast<const gpiece*>(p); }
 
-// A thread's pieces of a unit: piece i at byte 16 (thread + 256 i).
-__device__ __forceinline__ void load_unit(u32x4 (&v)[kSteps], const uint8_t* src, int bytes) {
+// A thread's pieces of a unit: piece i at byte 16 (thread + 256 i), zeros where the unit
+// has no whole piece.
+__device__ __forceinline__ void load_unit(u32x4 (&v)[kSteps], const gbyte* src, int bytes) {
   if (bytes == kClipUnitBytes) {  // (all but a tensor's last unit)
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) v[i] = load_any(src + 16 * (threadIdx.x + kClipThreads * i));
@@ -82,10 +91,20 @@ __device__ __forceinline__ void load_unit(u32x4 (&v)[kSteps], const uint8_t* src
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int at = 16 * (threadIdx.x + kClipThreads * i);
+    v[i] = u32x4{0u, 0u, 0u, 0u};
     if (at + 16 <= bytes) v[i] = load_any(src + at);
-    else if (at < bytes) v[i] = load_tail(src + at, bytes - at);
-    else v[i] = u32x4{0u, 0u, 0u, 0u};
   }
+}
+
+// The elements behind a unit's whole pieces (fewer than 16 bytes), one to a thread: this
+// thread's, at byte *at; false where it has none.
+__device__ __forceinline__ bool rest_of(const ClipUnit& x, int* at) {
+  *at = (x.bytes & ~15) + (int)threadIdx.x * (x.fp32 ? 4 : 2);
+  return *at < x.bytes;
+}
+__device__ __forceinline__ float load_one(const ClipUnit& x, int at) {
+  if (x.fp32) return *reinterpret_cast<const gfloat*>(x.src + at);
+  return __uint_as_float((uint32_t)*reinterpret_cast<const ghalf*>(x.src + at) << 16);
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -104,15 +123,14 @@ __device__ __forceinline__ double block_sum(double v, double* scratch) {
 __device__ __forceinline__ double square(float f) { return (double)f * (double)f; }
 
 __global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(ClipTable t) {
-  __shared__ int s_before[kClipTensors + 1];
-  __shared__ int s_scratch[4];
+  __shared__ ClipLds s_table;
   __shared__ double s_sum[4];
-  const int total = clip_units(t, s_before, s_scratch);
+  const int total = clip_units(t, s_table);
   double sum[4] = {0.0, 0.0, 0.0, 0.0};
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
-    const ClipUnit x = clip_unit(t, s_before, u);
+    const ClipUnit x = clip_unit(t, s_table, u);
     u32x4 v[kSteps];
-    load_unit(v, static_cast<const uint8_t*>(t.src[x.tensor]) + x.at, x.bytes);
+    load_unit(v, x.src, x.bytes);
     if (x.fp32) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
@@ -125,57 +143,89 @@ __global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(ClipTable t) {
         for (int c = 0; c < 4; ++c)
           sum[c] += square(__uint_as_float(v[i][c] << 16)) + square(__uint_as_float(v[i][c] & 0xffff0000u));
     }
+    int at;
+    if (rest_of(x, &at)) sum[0] += square(load_one(x, at));
   }
   const double s = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), s_sum);
   if (threadIdx.x == 0) t.partial[t.first + blockIdx.x] = s;
 }
 
-// The norm from the launches' partial sums, in every thread of a workgroup.
-__device__ __forceinline__ double clip_norm(const ClipTable& t, double* scratch) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < t.partials; i += kClipThreads) s += t.partial[i];
-  return sqrt(block_sum(s, scratch));
-}
+// This thread's share of the launches' partial sums, its first loads apart from their use.
+struct Partials {
+  double first[4];
+  __device__ __forceinline__ void load(const ClipTable& t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = threadIdx.x + kClipThreads * i;
+      first[i] = at < t.partials ? t.partial[at] : 0.0;
+    }
+  }
+  __device__ __forceinline__ double sum(const ClipTable& t) const {
+    double s = (first[0] + first[1]) + (first[2] + first[3]);
+    for (int i = threadIdx.x + 4 * kClipThreads; i < t.partials; i += kClipThreads) s += t.partial[i];
+    return s;
+  }
+};
 
 __global__ __launch_bounds__(kClipThreads) void clip_finish_kernel(ClipTable t) {
   __shared__ double s_sum[4];
-  const double norm = clip_norm(t, s_sum);
+  Partials mine;
+  mine.load(t);
+  const double norm = sqrt(block_sum(mine.sum(t), s_sum));
   if (threadIdx.x == 0) *t.norm_out = (float)norm;
 }
 
 // Walks the units from the last one back: what the norm kernel read last is what the
-// caches still hold.  In place nothing is written where nothing changes.
-__global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable t) {
-  __shared__ int s_before[kClipTensors + 1];
-  __shared__ int s_scratch[4];
+// caches still hold.  In place nothing is written where nothing changes.  A workgroup's
+// first unit loads while the norm is added up.
+__global__ __launch_bounds__(kClipThreads, 6) void clip_scale_kernel(ClipTable t) {
+  __shared__ ClipLds s_table;
   __shared__ double s_sum[4];
-  const double norm = t.norm_in ? (double)*t.norm_in : clip_norm(t, s_sum);
+  Partials mine;
+  mine.load(t);  // (none with a norm given)
+  const int total = clip_units(t, s_table);
+  int u = total - 1 - (int)blockIdx.x;
+  ClipUnit x{};
+  u32x4 v[kSteps];
+  if (u >= 0) {
+    x = clip_unit(t, s_table, u);
+    load_unit(v, x.src, x.bytes);
+  }
+  const double norm = t.norm_in ? (double)*t.norm_in : sqrt(block_sum(mine.sum(t), s_sum));
   if (t.norm_out && blockIdx.x == 0 && threadIdx.x == 0) *t.norm_out = (float)norm;
   // a norm that is not finite leaves the gradients as they are
   const bool finite = fabsf((float)norm) < __builtin_inff();
   const double by = (double)t.max_norm / (norm + (double)t.eps);
   const float scale = finite && by < 1.0 ? (float)by : 1.0f;
-  const int total = clip_units(t, s_before, s_scratch);
-  for (int u = total - 1 - (int)blockIdx.x; u >= 0; u -= gridDim.x) {
-    const ClipUnit x = clip_unit(t, s_before, u);
-    const uint8_t* src = static_cast<const uint8_t*>(t.src[x.tensor]) + x.at;
-    uint8_t* dst = static_cast<uint8_t*>(t.dst[x.tensor]) + x.at;
-    if (scale == 1.0f && src == dst) continue;
-    u32x4 v[kSteps];
-    load_unit(v, src, x.bytes);
+  if (scale == 1.0f && !t.apart) return;
+  while (u >= 0) {
+    if (scale != 1.0f || x.src != x.dst) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (scale != 1.0f) {  // (a copy keeps every bit, NaN's too)
+      for (int i = 0; i < kSteps; ++i) {
+        if (scale != 1.0f) {  // (a copy keeps every bit, NaN's too)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (x.fp32) v[i][c] = __float_as_uint(__uint_as_float(v[i][c]) * scale);
-          else v[i][c] = pack_bf16x2(__uint_as_float(v[i][c] << 16) * scale,
-                                     __uint_as_float(v[i][c] & 0xffff0000u) * scale);
+          for (int c = 0; c < 4; ++c) {
+            if (x.fp32) v[i][c] = __float_as_uint(__uint_as_float(v[i][c]) * scale);
+            else v[i][c] = pack_bf16x2(__uint_as_float(v[i][c] << 16) * scale,
+                                       __uint_as_float(v[i][c] & 0xffff0000u) * scale);
+          }
         }
+        const int at = 16 * (threadIdx.x + kClipThreads * i);
+        if (at + 16 <= x.bytes) *reinterpret_cast<gpiece*>(x.dst + at) = v[i];
       }
-      const int at = 16 * (threadIdx.x + kClipThreads * i);
-      if (at + 16 <= x.bytes) *reinterpret_cast<u32x4_any*>(dst + at) = v[i];
-      else if (at < x.bytes) store_tail(dst + at, v[i], x.bytes - at);
+      int at;
+      if (rest_of(x, &at)) {
+        const float f = load_one(x, at);
+        const uint32_t bits = scale != 1.0f ? __float_as_uint(f * scale) : __float_as_uint(f);
+        if (x.fp32) *reinterpret_cast<gfloat*>(x.dst + at) = __uint_as_float(bits);
+        else *reinterpret_cast<ghalf*>(x.dst + at) =
+            scale != 1.0f ? (uint16_t)pack_bf16x2(__uint_as_float(bits), 0.0f) : (uint16_t)(bits >> 16);
+      }
+    }
+    u -= gridDim.x;
+    if (u >= 0) {
+      x = clip_unit(t, s_table, u);
+      load_unit(v, x.src, x.bytes);
     }
   }
 }

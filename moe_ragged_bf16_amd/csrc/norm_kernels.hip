@@ -187,7 +187,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void norm_fwd_kernel
 // so one exchange of three sums a row is enough.  The weights' gradients add up in the
 // lanes' registers over a block's rows; norm_finish_kernel adds the blocks.
 template <int WAVES, bool FP32>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void norm_bwd_kernel(NormBwdParams p) {
+__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ? 1 : 4) void norm_bwd_kernel(NormBwdParams p) {
   constexpr int kRows = WAVES == 1 ? 4 : 1, kLanes = 64 * WAVES;
   __shared__ float s_red[2 * 3 * 16];
   __shared__ float s_part[WAVES == 1 ? 4 * 1024 : 1];
@@ -296,9 +296,10 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void norm_bwd_kernel
   }
 }
 
-// Adds the blocks' sums of a weight (blockIdx.y) over 16 columns: row group g of 64 adds
-// blocks g, g + 64, ..., then the groups of a wave by shuffles and the 16 waves in order.
-constexpr int kFinishCols = 16;
+// Adds the blocks' sums of a weight (blockIdx.y) over 32 columns (whole cache lines): row
+// group g of 32 adds blocks g, g + 32, ..., then the two groups of a wave by a shuffle and
+// the 16 waves in order.
+constexpr int kFinishCols = 32, kFinishRows = 1024 / kFinishCols;
 
 __global__ __launch_bounds__(1024) void norm_finish_kernel(NormBwdParams p) {
   __shared__ float s_sum[16][kFinishCols];
@@ -307,7 +308,8 @@ __global__ __launch_bounds__(1024) void norm_finish_kernel(NormBwdParams p) {
   const int col = threadIdx.x % kFinishCols, g = threadIdx.x / kFinishCols, c = blockIdx.x * kFinishCols + col;
   float s = 0.0f;
   if (c < p.hidden)
-    for (int b = g; b < p.blocks; b += 64) s += p.part[((int64_t)b * 2 + blockIdx.y) * p.hidden + c];
+#pragma unroll 8
+    for (int b = g; b < p.blocks; b += kFinishRows) s += p.part[((int64_t)b * 2 + blockIdx.y) * p.hidden + c];
   for (int d = kFinishCols; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
   if ((threadIdx.x & 63) < kFinishCols) s_sum[threadIdx.x >> 6][col] = s;
   __syncthreads();

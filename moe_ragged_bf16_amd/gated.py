@@ -24,10 +24,9 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import _capi, ops
+from . import _capi
 from ._capi import native, refuse_tracing
 from .autograd import _fused_main_grad, _fused_wgrad, _main_grad
-from .ops import _need
 
 __all__ = ["GatedRows", "grouped_gated_gemm_fwd", "grouped_gated_gemm_dgrad", "grouped_gated_ffn",
            "gated_gemm_fwd_workspace_bytes", "gated_gemm_dgrad_workspace_bytes"]
@@ -81,14 +80,12 @@ def grouped_gated_gemm_dgrad(dy: torch.Tensor, w_down: torch.Tensor, gate_up: to
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, w_down, offs, activation, fuse):
+    def forward(ctx, x, w, w_down, offs, code, fuse):
         keep = any(ctx.needs_input_grad[:3])
-        h, gate_up = grouped_gated_gemm_fwd(x, w, offs, activation=activation, keep=keep)
-        y = ops.grouped_det_gemm_fwd(h, w_down, offs)
-        ops.zero_pad_rows(y, offs, w.shape[0])
+        y, h, gate_up = native.ffn_fwd(x, w, w_down, offs, code, keep)
         if keep:
             ctx.save_for_backward(x, w, w_down, offs, h, gate_up)
-        ctx.activation, ctx.fuse = activation, fuse
+        ctx.code, ctx.fuse = code, fuse
         # (the caller's weights themselves, whose main_grad the backward reads)
         ctx.w_objs = (w, w_down) if fuse else (None, None)
         return y
@@ -100,32 +97,24 @@ class _GatedFfn(torch.autograd.Function):
         x, w, w_down, offs, h, gate_up = ctx.saved_tensors
         dy = dy.contiguous()
         need_x, need_w, need_down = ctx.needs_input_grad[:3]
-        E = w.shape[0]
+        if not ctx.fuse:
+            dx, dw, dw_down, _ = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h,
+                                                need_x + 2 * need_w + 4 * need_down)
+            return dx, dw, dw_down, None, None, None
         read = (("the output gradient", dy), ("x", x), ("offs", offs), ("w", w), ("w_down", w_down), ("h", h),
                 ("gate_up", gate_up))
-        mg = mg_down = dx = dw = dw_down = None
-        if ctx.fuse and need_w:
-            mg = _fused_main_grad(ctx.w_objs[0], "grouped_gated_ffn", read)
-        if ctx.fuse and need_down:
-            mg_down = _fused_main_grad(ctx.w_objs[1], "grouped_gated_ffn", read)
-        if need_x or need_w:
-            d = grouped_gated_gemm_dgrad(dy, w_down, gate_up, offs, activation=ctx.activation)
-        if need_x:
-            dx = ops.grouped_det_gemm_dgrad(d, w, offs)
-            ops.zero_pad_rows(dx, offs, E)
-        if need_w:
-            dw = _fused_wgrad(ctx.w_objs[0], mg, d, x, offs) if ctx.fuse else \
-                ops.grouped_det_gemm_wgrad(d, x, offs, out_dtype=w.dtype, num_groups=E)
-        if need_down:
-            dw_down = _fused_wgrad(ctx.w_objs[1], mg_down, dy, h, offs) if ctx.fuse else \
-                ops.grouped_det_gemm_wgrad(dy, h, offs, out_dtype=w_down.dtype, num_groups=E)
+        mgs = [_fused_main_grad(o, "grouped_gated_ffn", read) if need else None
+               for o, need in zip(ctx.w_objs, (need_w, need_down))]
+        dx, _, _, d = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h, need_x + 8 * need_w)
+        dw = _fused_wgrad(ctx.w_objs[0], mgs[0], d, x, offs) if need_w else None
+        dw_down = _fused_wgrad(ctx.w_objs[1], mgs[1], dy, h, offs) if need_down else None
         return dx, dw, dw_down, None, None, None
 
 
 @torch.compiler.disable
-def _apply_eagerly(x, w, w_down, offs, activation, fuse):
+def _apply_eagerly(x, w, w_down, offs, code, fuse):
     # (the library's calls are opaque to torch.compile: out of its graphs)
-    return _GatedFfn.apply(x, w, w_down, offs, activation, fuse)
+    return _GatedFfn.apply(x, w, w_down, offs, code, fuse)
 
 
 def grouped_gated_ffn(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, offs: torch.Tensor, *,
@@ -144,15 +133,9 @@ def grouped_gated_ffn(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
         raise NotImplementedError("grouped_gated_ffn cannot be compiled by torch.compile")
     if not isinstance(fuse_wgrad_accumulation, bool):
         raise ValueError(f"fuse_wgrad_accumulation must be a bool, got {type(fuse_wgrad_accumulation).__name__}")
-    _code(activation)
-    _need(x, "x", torch.bfloat16, 2)
-    _need(w_gate_up, "w_gate_up", torch.bfloat16, 3)
-    _need(w_down, "w_down", torch.bfloat16, 3)
-    if w_gate_up.shape[0] != w_down.shape[0] or w_gate_up.shape[1] != 2 * w_down.shape[2]:
-        raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not belong together: "
-                         "[E, 2 F, K] and [E, N, F]")
+    code = _code(activation)
     if fuse_wgrad_accumulation and torch.is_grad_enabled() and torch._C._current_autograd_node() is None:
         for w in (w_gate_up, w_down):
-            if w.requires_grad:
+            if isinstance(w, torch.Tensor) and w.requires_grad:
                 _main_grad(w, "forward", "grouped_gated_ffn")
-    return _apply_eagerly(x, w_gate_up, w_down, offs, activation, fuse_wgrad_accumulation)
+    return _apply_eagerly(x, w_gate_up, w_down, offs, code, fuse_wgrad_accumulation)
