@@ -1,6 +1,6 @@
 """Ahead-of-time build of the gfx950 HIP library ``libmoe_ragged_bf16.so``.
 
-One ``hipcc`` invocation compiles the kernels and the C ABI for gfx950 only and
+``hipcc`` compiles the kernels and the C ABI for gfx950 only, one file each, and
 links them into the package directory; a C++ one compiles ``_binding.so``, the Python
 calls of the operators around the products.  Run ``python -m moe_ragged_bf16_amd.build``.
 """
@@ -12,6 +12,8 @@ import shutil
 import tempfile
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
+from functools import lru_cache
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -57,23 +59,32 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     """Compile the library (always) and return its path."""
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC]
-    for s in SOURCES:
-        cmd += ["-x", "hip", os.path.join(CSRC, s)]
-    cmd += ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building %s" % LIB_NAME)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+            raise RuntimeError("hipcc failed building %s" % LIB_NAME)
+
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s + ".o") for s in SOURCES]
+        flags = [f for f in HIP_FLAGS if f != "-shared"]
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(run, [[hipcc(), *flags, "-I", INCLUDE, "-I", CSRC, "-x", "hip", "-c", os.path.join(CSRC, s),
+                                 "-o", o] for s, o in zip(SOURCES, objects)]))
+        run([hipcc(), "--offload-arch=gfx950", "-shared", *objects, "-o", tmp])
     try:
-        check_no_packed_fp32(tmp)
-        check_mfma_sources(tmp)
-        check_mfma_results(tmp)
+        asm = device_assembly(tmp)
+        check_no_packed_fp32(tmp, asm)
+        check_mfma_sources(tmp, asm)
+        check_mfma_results(tmp, asm)
     except Exception:
         os.unlink(tmp)
         raise
+    finally:
+        _functions.cache_clear()
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
@@ -107,10 +118,11 @@ def device_assembly(lib_path: str = LIB_PATH) -> str:
         return "".join(out)
 
 
-def check_no_packed_fp32(lib_path: str = LIB_PATH) -> int:
+def check_no_packed_fp32(lib_path: str = LIB_PATH, asm: str = "") -> int:
     """Raises if the built device code holds a packed fp32 add, multiply or
-    fma; returns the number of MFMA instructions seen (a sanity count)."""
-    asm = device_assembly(lib_path)
+    fma; returns the number of MFMA instructions seen (a sanity count).  `asm`:
+    the library's disassembly, where the caller has it."""
+    asm = asm or device_assembly(lib_path)
     bad = [ln.strip() for ln in asm.splitlines() if PACKED_FP32.search(ln)]
     if bad:
         raise RuntimeError("packed fp32 arithmetic in the gfx950 code: %d instructions, e.g. %s" % (len(bad), bad[0]))
@@ -144,6 +156,7 @@ class _Instruction:
         return self.name.startswith(("v_mfma", "v_smfma"))
 
 
+@lru_cache(maxsize=1)
 def _functions(asm: str) -> list:
     """The instructions of each function of a disassembly, with the branches
     between them (a branch names its target as <function+offset>)."""
@@ -238,14 +251,14 @@ def mfma_result_hazards(asm: str) -> list:
     return bad
 
 
-def check_mfma_sources(lib_path: str = LIB_PATH) -> None:
-    bad = mfma_source_hazards(device_assembly(lib_path))
+def check_mfma_sources(lib_path: str = LIB_PATH, asm: str = "") -> None:
+    bad = mfma_source_hazards(asm or device_assembly(lib_path))
     if bad:
         raise RuntimeError("a matrix instruction too close behind a write of its source: %d, e.g. %s" % (len(bad), bad[0]))
 
 
-def check_mfma_results(lib_path: str = LIB_PATH) -> None:
-    bad = mfma_result_hazards(device_assembly(lib_path))
+def check_mfma_results(lib_path: str = LIB_PATH, asm: str = "") -> None:
+    bad = mfma_result_hazards(asm or device_assembly(lib_path))
     if bad:
         raise RuntimeError("an access of a matrix instruction's result before it is there: %d, e.g. %s" % (len(bad), bad[0]))
 

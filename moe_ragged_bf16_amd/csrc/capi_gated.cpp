@@ -22,12 +22,11 @@ int check_sizes(int64_t m_rows, int64_t n, int64_t f, int32_t num_groups) {
   return MDG_OK;
 }
 
+static_assert(MDG_SILU == kActSilu && MDG_GELU_TANH == kActGeluTanh, "activations");
+
 bool activation(int act, GatedParams* p) {
-  const float c = 1.59576912160573071f;  // 2 sqrt(2 / pi)
-  if (act == MDG_SILU) p->q0 = 1.0f, p->q1 = 0.0f;
-  else if (act == MDG_GELU_TANH) p->q0 = c, p->q1 = c * 0.044715f;
-  else return false;
-  return true;
+  p->act = act;
+  return act == MDG_SILU || act == MDG_GELU_TANH;
 }
 
 // Units of the tile kernel, at most: row tiles of every group, the last one of each
@@ -83,15 +82,16 @@ int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, vo
   if (!dev.gfx950) return MDG_EUNSUPPORTED;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t cus = dev.cus > 0 ? dev.cus : 256, active = std::min<int64_t>(num_groups, m_rows);
-  const int64_t cols = op == kFwd ? kGatedMidTile / 2 : kGatedMidTile;
-  const int64_t mid = ((m_rows + kGatedMidTile - 1) / kGatedMidTile + active) * ((f + cols - 1) / cols);
   Kernel which = kernel_of(op, m_rows, p->g.n, f, active, cus);
-  if (which == kMid && (mid + 7) / 8 * 8 * 256 > UINT32_MAX) which = kTile;  // (a launch's work-items)
+  const int64_t cols = op == kFwd ? kGatedMidTile / 2 : kGatedMidTile;
+  const int64_t row_tiles = (m_rows + kGatedMidTile - 1) / kGatedMidTile + active;
+  const int64_t mid = (row_tiles * ((f + cols - 1) / cols) + 7) / 8 * 8;
+  if (which == kMid && mid * 256 > UINT32_MAX) which = kTile;  // (a launch's work-items)
   hipError_t err = hipSuccess;
   if (which == kSmall) {
     err = launch_gated_small(*p, (int)(active + m_rows / kGatedSmallRows), s);
   } else if (which == kMid) {
-    err = launch_gated_mid(op, *p, (int)((mid + 7) / 8 * 8), s);
+    err = launch_gated_mid(op, *p, (int)mid, s);
   } else {
     const int64_t units = units_of(op, m_rows, f, num_groups), slots = slots_of(units);
     char* ws = static_cast<char*>(workspace);

@@ -15,6 +15,8 @@ constexpr int kGatedSmallCols = 16;         // hidden columns of the small kerne
 constexpr int kGatedSmallRows = 64;         // and their rows, at most
 constexpr int kGatedMidTile = 128;          // rows, and columns of operand B, of the middle kernel's tiles
 
+enum Activation : int { kActSilu = 0, kActGeluTanh = 1 };
+
 struct GatedParams {
   // The product.  fwd: a = x, b = w, out = h, n = 2 f, k; dgrad: a = dy, b = w_down,
   // out = dgate_up, n, k = f.
@@ -22,7 +24,7 @@ struct GatedParams {
   const uint16_t* gate_up;  // dgrad: [m_rows, 2 f] as fwd kept them
   uint16_t* keep;           // fwd: [m_rows, 2 f] the projections, or nullptr
   int32_t f;
-  float q0, q1;             // q(a) = a (q0 + q1 a^2) of the activation a s(q(a))
+  int32_t act;              // kActSilu or kActGeluTanh
 };
 
 // Where a split tail unit's tile goes (written by the tile kernel, read by the

@@ -101,7 +101,7 @@ __device__ __forceinline__ void settle(f32x4 (&acc)[I][J]) {
 // product (16 of 16 bytes a lane, 12 waves to a CU).
 constexpr int kSmallPiece = 256;
 
-template <int MB>
+template <int MB, int ACT>
 __device__ __forceinline__ void small_gated(const GatedParams& gp, int e, int row0, int rows, int f0, f32x4* s_acc) {
   const GemmParams& p = gp.g;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
@@ -163,9 +163,8 @@ __device__ __forceinline__ void small_gated(const GatedParams& gp, int e, int ro
     a += s_acc[(w * 2 * 4 + q) * 64 + lane];
     b += s_acc[((w * 2 + 1) * 4 + q) * 64 + lane];
   }
-  const Act act{gp.q0, gp.q1};
 #pragma unroll
-  for (int x = 0; x < 4; ++x) h[x] = act.hidden(a[x], b[x]);
+  for (int x = 0; x < 4; ++x) h[x] = Act<ACT>::hidden(a[x], b[x]);
   const int64_t t = row0 + row;
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + t * f + col) = pack4(h);
   if (gp.keep != nullptr) {
@@ -174,15 +173,16 @@ __device__ __forceinline__ void small_gated(const GatedParams& gp, int e, int ro
   }
 }
 
+template <int ACT>
 __global__ __launch_bounds__(256, 3) void gated_small_kernel(GatedParams gp) {
   __shared__ f32x4 s_acc[kGatedSmallRows / 16 * 2 * 4 * 64];
   Rows u;
   if (!find_rows<kGatedSmallRows>(gp.g, blockIdx.y, 1, false, &u)) return;
   const int row0 = u.start + u.unit * kGatedSmallRows, rows = min(kGatedSmallRows, u.rows - u.unit * kGatedSmallRows);
   const int f0 = blockIdx.x * kGatedSmallCols;
-  if (rows <= 16) small_gated<1>(gp, u.e, row0, rows, f0, s_acc);
-  else if (rows <= 32) small_gated<2>(gp, u.e, row0, rows, f0, s_acc);
-  else small_gated<4>(gp, u.e, row0, rows, f0, s_acc);
+  if (rows <= 16) small_gated<1, ACT>(gp, u.e, row0, rows, f0, s_acc);
+  else if (rows <= 32) small_gated<2, ACT>(gp, u.e, row0, rows, f0, s_acc);
+  else small_gated<4, ACT>(gp, u.e, row0, rows, f0, s_acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -191,20 +191,25 @@ __global__ __launch_bounds__(256, 3) void gated_small_kernel(GatedParams gp) {
 // Tiles of 128 rows x 128 columns (fwd: 64 hidden columns, gate and up in turns of 16;
 // dgrad: 128 hidden columns), four waves of 64 x 64, stages of 64 reductions (16 KiB an
 // operand), two buffers, two workgroups to a CU, one of which computes while the other
-// waits.
+// waits.  What a CU takes in bounds it, 34 to 45 GB/s with all of them at it: 64 groups of
+// 128 rows on average of 2 x 1536 x 2048 take 200 us, 12 TB/s into LDS; rows that do not
+// start on cache lines (k no multiple of 64) ask for two lines where one would do, 16
+// groups of 188 rows on average of 2 x 1000 x 2000 62 us, of 2 x 1024 x 2048 47.
+// (Tried and not kept: weights straight to registers and four buffers of rows, 192 KiB on
+// their way to a CU, 0 to 12 % longer; 256 rows and eight waves, a quarter fewer bytes but
+// one workgroup to a CU, 20 to 40 % longer.)
 constexpr int kMidTile = kGatedMidTile;
-constexpr int kMidBytes = kMidTile * 128;
 
 // Buffer B of operand A (0) or B (1); each a static array of its own, so that the compiler
 // can tell reads of one from loads still landing in another.
 template <int OPERAND, int B>
 __device__ __forceinline__ uint8_t* mid_buffer() {
-  __shared__ __attribute__((aligned(1024))) uint8_t s_buf[kMidBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_buf[kMidTile * 128];
   return s_buf;
 }
 
-// An operand read along its rows: 128 rows x 64 reductions, LDS rows of 128 bytes, 16-byte
-// chunk c of row r at c ^ (r % 8).  A fragment is 16 rows x 32 reductions (half h).
+// An operand read along its rows: LDS rows of 64 reductions (128 bytes), 16-byte chunk c of
+// row r at c ^ (r % 8).  A fragment is 16 rows x 32 reductions (half h).
 __device__ __forceinline__ bf16x8 mid_frag(const uint8_t* st, int row0, int h, int lane) {
   const int r = row0 + (lane & 15);
   return *reinterpret_cast<const bf16x8*>(st + r * 128 + (((h * 4 + (lane >> 4)) ^ (r & 7)) << 4));
@@ -223,7 +228,20 @@ __device__ __forceinline__ bf16x8 mid_frag_t(const uint8_t* st, int col0, int h,
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <int OP>
+// bf16 rows of 128 bytes in LDS (chunk c of row r at c ^ (r / 2 % 8)) to columns
+// f0 .. f0 + valid of rows row0 .. of a tensor with rows of `ld`: 8 rows an instruction.
+__device__ __forceinline__ void mid_store_rows(const uint8_t* st, uint16_t* to, int64_t ld, int row0, int f0, int i_valid,
+                                               int f_valid, int w, int lane) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = (w * 4 + q) * 8 + (lane >> 3), c = lane & 7;
+    if (r < i_valid && c * 8 < f_valid)
+      *reinterpret_cast<u32x4*>(to + (int64_t)(row0 + r) * ld + f0 + c * 8) =
+          *reinterpret_cast<const u32x4*>(st + r * 128 + ((c ^ ((r >> 1) & 7)) << 4));
+  }
+}
+
+template <int OP, int ACT>
 __global__ __launch_bounds__(256, 2) void gated_mid_kernel(GatedParams gp) {
   const GemmParams& p = gp.g;
   constexpr int kCols = OP == kFwd ? kMidTile / 2 : kMidTile;  // hidden columns of a tile
@@ -237,7 +255,7 @@ __global__ __launch_bounds__(256, 2) void gated_mid_kernel(GatedParams gp) {
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), wi = w >> 1, wj = w & 1;
   const int R = OP == kFwd ? p.k : p.n;  // the reduction, and A's row length
   const int nk = (R + 63) / 64;
-  // A: segment 4 q + w of 8 rows; lane l loads chunk (l % 8) ^ (l / 8) of row l / 8 of it
+  // A: segments 4 q + w of 8 rows; lane l loads chunk (l % 8) ^ (l / 8) of row l / 8 of it
   const uint16_t* xa = p.a + (int64_t)row0 * R;
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
   const uint32_t off_a = (uint32_t)(w * 8 + (lane >> 3)) * (uint32_t)(R * 2) + chunk;
@@ -271,11 +289,13 @@ __global__ __launch_bounds__(256, 2) void gated_mid_kernel(GatedParams gp) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint32_t at = (int)chunk < left ? off_a + (uint32_t)(q * 32) * (uint32_t)(R * 2) : kOutOfRange;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(mid_buffer<0, B>() + (q * 4 + w) * 1024), 16, at, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(mid_buffer<0, B>() + (q * 4 + w) * 1024), 16, at,
+                                               0, 0, 0);
       uint32_t bt;
       if constexpr (OP == kFwd) bt = (int)chunk < left ? off_b + (uint32_t)(q * 16) * (uint32_t)(R * 2) : kOutOfRange;
       else bt = in_b ? off_b + (uint32_t)(q * 16) * (uint32_t)(f * 2) : kOutOfRange;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rbs, (lds_void*)(mid_buffer<1, B>() + (q * 4 + w) * 1024), 16, bt, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rbs, (lds_void*)(mid_buffer<1, B>() + (q * 4 + w) * 1024), 16, bt,
+                                               0, 0, 0);
     }
   };
   f32x4 acc[4][4];
@@ -320,48 +340,44 @@ __global__ __launch_bounds__(256, 2) void gated_mid_kernel(GatedParams gp) {
   wait_vm_lgkm<0>();
   __syncthreads();  // no load in flight, every wave past its reads: the buffers are free
 
-  const Act act{gp.q0, gp.q1};
+  uint8_t *const s0 = mid_buffer<0, 0>(), *const s1 = mid_buffer<0, 1>();
   const int r16 = lane & 15, q4 = lane >> 4;
   if constexpr (OP == kFwd) {
-    // The tile as bf16 rows of 128 bytes, chunk c of row r at c ^ (r / 2 % 8): h, and gate and
-    // up where they are kept, in a buffer each.  acc[i][2 j], [2 j + 1]: gate and up of hidden
-    // columns 32 wj + 16 j ..; lane l holds row l % 16, columns 4 (l / 16) .. + 3 of a block.
+    // acc[i][2 j], [2 j + 1]: gate and up of hidden columns 32 wj + 16 j ..; lane l holds row l % 16,
+    // columns 4 (l / 16) .. + 3 of a block.
+    const auto place = [&](int i, int j) {
+      const int r = wi * 64 + i * 16 + r16;
+      return r * 128 + (((wj * 4 + j * 2 + (q4 >> 1)) ^ ((r >> 1) & 7)) << 4) + (q4 & 1) * 8;
+    };
+    uint16_t* const h = static_cast<uint16_t*>(p.out);
+    if (gp.keep != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          *reinterpret_cast<u32x2*>(s0 + place(i, j)) = pack4(acc[i][2 * j]);
+          *reinterpret_cast<u32x2*>(s1 + place(i, j)) = pack4(acc[i][2 * j + 1]);
+        }
+      __syncthreads();
+      mid_store_rows(s0, gp.keep, 2 * f, row0, f0, i_valid, f_valid, w, lane);
+      mid_store_rows(s1, gp.keep + f, 2 * f, row0, f0, i_valid, f_valid, w, lane);
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const f32x4 a = acc[i][2 * j], b = acc[i][2 * j + 1];
-        f32x4 h;
+        f32x4 v;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) h[x] = act.hidden(a[x], b[x]);
-        const int r = wi * 64 + i * 16 + r16;
-        const int at = r * 128 + (((wj * 4 + j * 2 + (q4 >> 1)) ^ ((r >> 1) & 7)) << 4) + (q4 & 1) * 8;
-        *reinterpret_cast<u32x2*>(mid_buffer<0, 0>() + at) = pack4(h);
-        if (gp.keep != nullptr) {
-          *reinterpret_cast<u32x2*>(mid_buffer<0, 1>() + at) = pack4(a);
-          *reinterpret_cast<u32x2*>(mid_buffer<1, 1>() + at) = pack4(b);
-        }
+        for (int x = 0; x < 4; ++x) v[x] = Act<ACT>::hidden(acc[i][2 * j][x], acc[i][2 * j + 1][x]);
+        *reinterpret_cast<u32x2*>(s0 + place(i, j)) = pack4(v);
       }
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {  // 8 rows an instruction
-      const int r = (w * 4 + q) * 8 + (lane >> 3), c = lane & 7;
-      const int at = r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
-      if (r >= i_valid || c * 8 >= f_valid) continue;
-      const int64_t t = row0 + r;
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + t * f + f0 + c * 8) =
-          *reinterpret_cast<const u32x4*>(mid_buffer<0, 0>() + at);
-      if (gp.keep != nullptr) {
-        *reinterpret_cast<u32x4*>(gp.keep + t * 2 * f + f0 + c * 8) =
-            *reinterpret_cast<const u32x4*>(mid_buffer<0, 1>() + at);
-        *reinterpret_cast<u32x4*>(gp.keep + t * 2 * f + f + f0 + c * 8) =
-            *reinterpret_cast<const u32x4*>(mid_buffer<1, 1>() + at);
-      }
-    }
+    mid_store_rows(s0, h, f, row0, f0, i_valid, f_valid, w, lane);
   } else {
-    // A wave's 64 x 64 of dh in fp32 in a buffer of its own, rows of 256 bytes, chunk c of
-    // row r at c ^ (r % 16); a lane then has 8 columns of rows 8 q + l / 8.
-    uint8_t* xo = w == 0 ? mid_buffer<0, 0>() : w == 1 ? mid_buffer<0, 1>() : w == 2 ? mid_buffer<1, 0>() : mid_buffer<1, 1>();
+    // 32 of a wave's 64 rows of dh at a time in fp32 in 8 KiB of its own, rows of 256 bytes,
+    // chunk c of row r at c ^ (r % 16); a lane then has 8 columns of rows 8 q + l / 8.
+    uint8_t* xo = (w < 2 ? s0 : s1) + (w & 1) * 8192;
     const int col = wj * 64 + (lane & 7) * 8;
     u32x4 av[8], bv[8];
 #pragma unroll
@@ -373,29 +389,33 @@ __global__ __launch_bounds__(256, 2) void gated_mid_kernel(GatedParams gp) {
       bv[q] = *reinterpret_cast<const u32x4*>(g + f);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4*>(xo + (i * 16 + r16) * 256 + (((j * 4 + q4) ^ r16) << 4)) = acc[i][j];
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int rr = q * 8 + (lane >> 3), c = (lane & 7) * 2;
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(xo + rr * 256 + ((c ^ (rr & 15)) << 4));
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(xo + rr * 256 + (((c + 1) ^ (rr & 15)) << 4));
-      u32x4 da, db;
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<f32x4*>(xo + (i * 16 + r16) * 256 + (((j * 4 + q4) ^ r16) << 4)) = acc[2 * half + i][j];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        float p0, p1, g0, g1;
-        act.grads(lo_f(av[q][x]), lo_f(bv[q][x]), x < 2 ? lo[2 * x] : hi[2 * x - 4], &p0, &g0);
-        act.grads(hi_f(av[q][x]), hi_f(bv[q][x]), x < 2 ? lo[2 * x + 1] : hi[2 * x - 3], &p1, &g1);
-        da[x] = pack_bf16x2(p0, p1);
-        db[x] = pack_bf16x2(g0, g1);
-      }
-      const int r = wi * 64 + rr;
-      if (r < i_valid && col < f_valid) {
-        uint16_t* d = static_cast<uint16_t*>(p.out) + (int64_t)(row0 + r) * 2 * f + f0 + col;
-        *reinterpret_cast<u32x4*>(d) = da;
-        *reinterpret_cast<u32x4*>(d + f) = db;
+      for (int q = 0; q < 4; ++q) {
+        const int rr = q * 8 + (lane >> 3), c = (lane & 7) * 2;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(xo + rr * 256 + ((c ^ (rr & 15)) << 4));
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(xo + rr * 256 + (((c + 1) ^ (rr & 15)) << 4));
+        u32x4 da, db;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t a = av[4 * half + q][x], b = bv[4 * half + q][x];
+          float p0, p1, g0, g1;
+          Act<ACT>::grads(lo_f(a), lo_f(b), x < 2 ? lo[2 * x] : hi[2 * x - 4], &p0, &g0);
+          Act<ACT>::grads(hi_f(a), hi_f(b), x < 2 ? lo[2 * x + 1] : hi[2 * x - 3], &p1, &g1);
+          da[x] = pack_bf16x2(p0, p1);
+          db[x] = pack_bf16x2(g0, g1);
+        }
+        const int r = wi * 64 + half * 32 + rr;
+        if (r < i_valid && col < f_valid) {
+          uint16_t* d = static_cast<uint16_t*>(p.out) + (int64_t)(row0 + r) * 2 * f + f0 + col;
+          *reinterpret_cast<u32x4*>(d) = da;
+          *reinterpret_cast<u32x4*>(d + f) = db;
+        }
       }
     }
   }
@@ -405,13 +425,18 @@ __global__ __launch_bounds__(256, 2) void gated_mid_kernel(GatedParams gp) {
 
 hipError_t launch_gated_small(const GatedParams& p, int pieces, hipStream_t s) {
   const dim3 g((p.f + kGatedSmallCols - 1) / kGatedSmallCols, pieces), b(256);
-  hipLaunchKernelGGL(gated_small_kernel, g, b, 0, s, p);
+  if (p.act == kActSilu) hipLaunchKernelGGL((gated_small_kernel<kActSilu>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((gated_small_kernel<kActGeluTanh>), g, b, 0, s, p);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_mid(Op op, const GatedParams& p, int grid, hipStream_t s) {
-  if (op == kFwd) hipLaunchKernelGGL((gated_mid_kernel<kFwd>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((gated_mid_kernel<kDgrad>), dim3(grid), dim3(256), 0, s, p);
+  const dim3 g(grid), b(256);
+  const bool silu = p.act == kActSilu;
+  if (op == kFwd && silu) hipLaunchKernelGGL((gated_mid_kernel<kFwd, kActSilu>), g, b, 0, s, p);
+  else if (op == kFwd) hipLaunchKernelGGL((gated_mid_kernel<kFwd, kActGeluTanh>), g, b, 0, s, p);
+  else if (silu) hipLaunchKernelGGL((gated_mid_kernel<kDgrad, kActSilu>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((gated_mid_kernel<kDgrad, kActGeluTanh>), g, b, 0, s, p);
   return hipGetLastError();
 }
 

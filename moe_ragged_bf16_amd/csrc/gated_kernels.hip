@@ -118,11 +118,10 @@ __device__ __forceinline__ GatedUnit decode_gated(const GatedParams& gp, const G
 // row r at chunk c ^ (r / 2 % 8) (conflict-free both ways).  Returns the memory
 // operations issued.  (KEEP is a template argument: a branch around the projections'
 // slabs made the compiler spill 194 registers.)
-template <bool KEEP>
+template <bool KEEP, int ACT>
 __device__ __forceinline__ int store_hidden(const Acc& acc, const GatedParams& gp, const GatedUnit& y, uint8_t* xb,
                                             int wi, int wj, int lane) {
   const int f = gp.f;
-  const Act act{gp.q0, gp.q1};
   if constexpr (KEEP) {
     const Staging x = staging(xb, lane, true);
     const int extent = (y.u.i_valid - 1) * f * 4 + f * 2 + y.f_valid * 2;
@@ -178,8 +177,8 @@ __device__ __forceinline__ int store_hidden(const Acc& acc, const GatedParams& g
       for (int q = 0; q < 4; ++q) {
         const f32x4 &a = acc[4 * half + ib][2 * q], &b = acc[4 * half + ib][2 * q + 1];
         u32x2 pk;
-        pk[0] = pack_bf16x2(act.hidden(acc_read(a[0]), acc_read(b[0])), act.hidden(acc_read(a[1]), acc_read(b[1])));
-        pk[1] = pack_bf16x2(act.hidden(acc_read(a[2]), acc_read(b[2])), act.hidden(acc_read(a[3]), acc_read(b[3])));
+        pk[0] = pack_bf16x2(Act<ACT>::hidden(acc_read(a[0]), acc_read(b[0])), Act<ACT>::hidden(acc_read(a[1]), acc_read(b[1])));
+        pk[1] = pack_bf16x2(Act<ACT>::hidden(acc_read(a[2]), acc_read(b[2])), Act<ACT>::hidden(acc_read(a[3]), acc_read(b[3])));
         *reinterpret_cast<u32x2*>(xb + wo + ib * 2048 + (((2 * q) ^ kw) << 4)) = pk;
       }
     }
@@ -200,10 +199,10 @@ __device__ __forceinline__ int store_hidden(const Acc& acc, const GatedParams& g
 // fp32 staging, from which a lane takes 8 consecutive columns (two 16-byte chunks) of
 // rows 8 q + l / 8; a and b of those are read, and their gradients written, 16 bytes
 // each.  The next half slab's a and b load while one is worked on.
+template <int ACT>
 __device__ __forceinline__ int store_grads(const Acc& acc, const GatedParams& gp, const GatedUnit& y, uint8_t* xb,
                                            int wi, int wj, int lane) {
   const int f = gp.f;
-  const Act act{gp.q0, gp.q1};
   const Staging x = staging(xb, lane, false);
   const int extent = uniform((y.u.i_valid - 1) * f * 4 + f * 2 + y.f_valid * 2);
   const int64_t at = (int64_t)y.row0 * 2 * f + y.f0;
@@ -250,8 +249,8 @@ __device__ __forceinline__ int store_grads(const Acc& acc, const GatedParams& gp
       for (int c = 0; c < 4; ++c) {
         const uint32_t av = a[hs & 1][q][c], bv = b[hs & 1][q][c];
         float p0, p1, g0, g1;
-        act.grads(lo_f(av), lo_f(bv), c < 2 ? lo[2 * c] : hi[2 * c - 4], &p0, &g0);
-        act.grads(hi_f(av), hi_f(bv), c < 2 ? lo[2 * c + 1] : hi[2 * c - 3], &p1, &g1);
+        Act<ACT>::grads(lo_f(av), lo_f(bv), c < 2 ? lo[2 * c] : hi[2 * c - 4], &p0, &g0);
+        Act<ACT>::grads(hi_f(av), hi_f(bv), c < 2 ? lo[2 * c + 1] : hi[2 * c - 3], &p1, &g1);
         da[c] = pack_bf16x2(p0, p1);
         db[c] = pack_bf16x2(g0, g1);
       }
@@ -263,7 +262,7 @@ __device__ __forceinline__ int store_grads(const Acc& acc, const GatedParams& gp
   return 128;
 }
 
-template <int OP, bool KEEP>
+template <int OP, bool KEEP, int ACT>
 __device__ __forceinline__ int gated_epilogue(const Acc& acc, const GatedParams& p, const GatedUnit& y, uint8_t* xb,
                                               int wi, int wj, int lane) {
   if (y.u.mode == kStoreF32) {  // a piece of a split tail unit: fp32 partial tile
@@ -271,8 +270,8 @@ __device__ __forceinline__ int gated_epilogue(const Acc& acc, const GatedParams&
     epilogue_store<kStoreF32>(acc, ot, xb, lane);
     return epilogue_ops<kStoreF32>();
   }
-  if constexpr (OP == kFwd) return store_hidden<KEEP>(acc, p, y, xb, wi, wj, lane);
-  else return store_grads(acc, p, y, xb, wi, wj, lane);
+  if constexpr (OP == kFwd) return store_hidden<KEEP, ACT>(acc, p, y, xb, wi, wj, lane);
+  else return store_grads<ACT>(acc, p, y, xb, wi, wj, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -283,7 +282,7 @@ __device__ __forceinline__ int gated_epilogue(const Acc& acc, const GatedParams&
 // stages stands in both: as a function of tile_pipe.h it made the compiler schedule
 // the other kernels anew.)
 // KEEP: fwd keeps the projections.
-template <int OP, bool KEEP, bool MASK, bool PAIRS>
+template <int OP, bool KEEP, int ACT, bool MASK, bool PAIRS>
 __global__ __launch_bounds__(kThreads, 1) void gated_kernel(GatedParams gp) {
   using Pp = Pipe<OP, MASK, PAIRS>;
   __shared__ int s_end[kMaxGroups];
@@ -367,8 +366,8 @@ __global__ __launch_bounds__(kThreads, 1) void gated_kernel(GatedParams gp) {
     const int ln = lane_here();
     // (each branch names its staging array, so that the compiler can tell its
     // accesses from the loads landing in the others)
-    if (pipe.w < 2) tail = gated_epilogue<OP, KEEP>(acc, gp, cur, s_a3 + (pipe.w & 1) * 8192, pipe.wi, pipe.wj, ln);
-    else tail = gated_epilogue<OP, KEEP>(acc, gp, cur, s_b3 + (pipe.w & 1) * 8192, pipe.wi, pipe.wj, ln);
+    if (pipe.w < 2) tail = gated_epilogue<OP, KEEP, ACT>(acc, gp, cur, s_a3 + (pipe.w & 1) * 8192, pipe.wi, pipe.wj, ln);
+    else tail = gated_epilogue<OP, KEEP, ACT>(acc, gp, cur, s_b3 + (pipe.w & 1) * 8192, pipe.wi, pipe.wj, ln);
     wait_vm_lgkm<63>();  // the staging reads have returned ...
     lds_barrier();       // ... in every wave
     cur = nxt;
@@ -400,14 +399,13 @@ __device__ __forceinline__ u32x4 pack8(const f32x4 (&s)[2]) {
 // blockIdx.y picks the tail unit, blockIdx.x a set of rows of its tile; a thread adds 8
 // consecutive hidden columns (fwd: of gate and up) of a row over the pieces in range
 // order and runs what the tile kernel's epilogue runs.
-template <int OP>
+template <int OP, int ACT>
 __global__ __launch_bounds__(kThreads) void gated_reduce_kernel(GatedParams gp) {
   const GemmParams& p = gp.g;
   const int T = uniform(p.tail_head[0]), S = uniform(p.tail_head[1]), t = blockIdx.y;
   if (t >= T || S < 2) return;
   constexpr int kLanes = (OP == kFwd ? kGatedCols : kTileJ) / 8;  // threads of a row
   const GatedTail tu = gated_tail(p)[t];
-  const Act act{gp.q0, gp.q1};
   const int f = gp.f, j = (threadIdx.x % kLanes) * 8;
   // fwd: hidden column j of the tile is gate column 128 (j / 64) + 32 (j / 16 % 4) + j % 16, and up 16 further
   const int col = OP == kFwd ? (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15) : j;
@@ -431,7 +429,7 @@ __global__ __launch_bounds__(kThreads) void gated_reduce_kernel(GatedParams gp) 
         *reinterpret_cast<u32x4*>(gp.keep + r * 2 * f + f + tu.f0 + j) = pack8(b);
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) a[c >> 2][c & 3] = act.hidden(a[c >> 2][c & 3], b[c >> 2][c & 3]);
+      for (int c = 0; c < 8; ++c) a[c >> 2][c & 3] = Act<ACT>::hidden(a[c >> 2][c & 3], b[c >> 2][c & 3]);
       *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + r * f + tu.f0 + j) = pack8(a);
     } else {
       const int64_t at = r * 2 * f + tu.f0 + j;
@@ -441,7 +439,7 @@ __global__ __launch_bounds__(kThreads) void gated_reduce_kernel(GatedParams gp) 
       for (int c = 0; c < 8; ++c) {
         const float x = (c & 1) ? hi_f(av[c >> 1]) : lo_f(av[c >> 1]), y = (c & 1) ? hi_f(bv[c >> 1]) : lo_f(bv[c >> 1]);
         float da, db;
-        act.grads(x, y, a[c >> 2][c & 3], &da, &db);
+        Act<ACT>::grads(x, y, a[c >> 2][c & 3], &da, &db);
         a[c >> 2][c & 3] = da;
         b[c >> 2][c & 3] = db;
       }
@@ -453,33 +451,42 @@ __global__ __launch_bounds__(kThreads) void gated_reduce_kernel(GatedParams gp) 
 
 }  // namespace
 
-template <bool KEEP, bool MASK>
+template <int ACT, bool KEEP, bool MASK>
 static void launch_gated_fwd(const GatedParams& p, int grid, hipStream_t s) {
   // stages in pairs where the experts' rows average kPairRows, as for the plain product
   const dim3 g(grid), b(kThreads);
   if (p.g.m_rows >= (int64_t)kPairRows * p.g.num_groups)
-    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, MASK, true>), g, b, 0, s, p);
+    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, ACT, MASK, true>), g, b, 0, s, p);
   else
-    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, MASK, false>), g, b, 0, s, p);
+    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, ACT, MASK, false>), g, b, 0, s, p);
 }
 
-hipError_t launch_gated(Op op, const GatedParams& p, int grid, hipStream_t s) {
+template <int ACT>
+static void launch_gated_act(Op op, const GatedParams& p, int grid, hipStream_t s) {
   const dim3 g(grid), b(kThreads);
   if (op == kFwd) {
     const bool mask = p.g.k % kTileR != 0;
-    if (p.keep) mask ? launch_gated_fwd<true, true>(p, grid, s) : launch_gated_fwd<true, false>(p, grid, s);
-    else mask ? launch_gated_fwd<false, true>(p, grid, s) : launch_gated_fwd<false, false>(p, grid, s);
+    if (p.keep) mask ? launch_gated_fwd<ACT, true, true>(p, grid, s) : launch_gated_fwd<ACT, true, false>(p, grid, s);
+    else mask ? launch_gated_fwd<ACT, false, true>(p, grid, s) : launch_gated_fwd<ACT, false, false>(p, grid, s);
   } else {
-    if (p.g.n % kTileR == 0) hipLaunchKernelGGL((gated_kernel<kDgrad, false, false, true>), g, b, 0, s, p);
-    else hipLaunchKernelGGL((gated_kernel<kDgrad, false, true, true>), g, b, 0, s, p);
+    if (p.g.n % kTileR == 0) hipLaunchKernelGGL((gated_kernel<kDgrad, false, ACT, false, true>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((gated_kernel<kDgrad, false, ACT, true, true>), g, b, 0, s, p);
   }
+}
+
+hipError_t launch_gated(Op op, const GatedParams& p, int grid, hipStream_t s) {
+  if (p.act == kActSilu) launch_gated_act<kActSilu>(op, p, grid, s);
+  else launch_gated_act<kActGeluTanh>(op, p, grid, s);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_reduce(Op op, const GatedParams& p, int grid_x, int grid_y, hipStream_t s) {
   const dim3 g(grid_x, grid_y), b(kThreads);
-  if (op == kFwd) hipLaunchKernelGGL((gated_reduce_kernel<kFwd>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((gated_reduce_kernel<kDgrad>), g, b, 0, s, p);
+  const bool silu = p.act == kActSilu;
+  if (op == kFwd && silu) hipLaunchKernelGGL((gated_reduce_kernel<kFwd, kActSilu>), g, b, 0, s, p);
+  else if (op == kFwd) hipLaunchKernelGGL((gated_reduce_kernel<kFwd, kActGeluTanh>), g, b, 0, s, p);
+  else if (silu) hipLaunchKernelGGL((gated_reduce_kernel<kDgrad, kActSilu>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((gated_reduce_kernel<kDgrad, kActGeluTanh>), g, b, 0, s, p);
   return hipGetLastError();
 }
 
