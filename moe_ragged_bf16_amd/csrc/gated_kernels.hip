@@ -451,27 +451,31 @@ __global__ __launch_bounds__(kThreads) void gated_reduce_kernel(GatedParams gp) 
 
 }  // namespace
 
-template <int ACT, bool KEEP, bool MASK>
+// Stages in pairs (tile_pipe.h), in us without / with: where experts average 1024 rows or
+// more (8 of 2 x 4096 x 4096, 8192 rows 497 / 481; 16 of 2 x 2048 x 6144, 16384 rows 752 /
+// 740; 32 of them 867 / 897; 64 of 2 x 1536 x 2048, 16384 rows 316 / 323), and where rows of k
+// end inside a stage, which start inside cache lines that the two halves of a pair share (8 of 2 x
+// 4096 x 4104, 8192 rows 654 / 618; 64 of 2 x 1536 x 2056, 20000 rows 473 / 440; 4 of 2 x 2048 x
+// 2056, 4096 rows 110 / 99).
+constexpr int kGatedPairRows = 1024;
+
+template <int ACT, bool KEEP>
 static void launch_gated_fwd(const GatedParams& p, int grid, hipStream_t s) {
-  // stages in pairs where the experts' rows average kPairRows, as for the plain product
   const dim3 g(grid), b(kThreads);
-  if (p.g.m_rows >= (int64_t)kPairRows * p.g.num_groups)
-    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, ACT, MASK, true>), g, b, 0, s, p);
+  if (p.g.k % kTileR != 0)
+    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, ACT, true, true>), g, b, 0, s, p);
+  else if (p.g.m_rows >= (int64_t)kGatedPairRows * p.g.num_groups)
+    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, ACT, false, true>), g, b, 0, s, p);
   else
-    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, ACT, MASK, false>), g, b, 0, s, p);
+    hipLaunchKernelGGL((gated_kernel<kFwd, KEEP, ACT, false, false>), g, b, 0, s, p);
 }
 
 template <int ACT>
 static void launch_gated_act(Op op, const GatedParams& p, int grid, hipStream_t s) {
   const dim3 g(grid), b(kThreads);
-  if (op == kFwd) {
-    const bool mask = p.g.k % kTileR != 0;
-    if (p.keep) mask ? launch_gated_fwd<ACT, true, true>(p, grid, s) : launch_gated_fwd<ACT, true, false>(p, grid, s);
-    else mask ? launch_gated_fwd<ACT, false, true>(p, grid, s) : launch_gated_fwd<ACT, false, false>(p, grid, s);
-  } else {
-    if (p.g.n % kTileR == 0) hipLaunchKernelGGL((gated_kernel<kDgrad, false, ACT, false, true>), g, b, 0, s, p);
-    else hipLaunchKernelGGL((gated_kernel<kDgrad, false, ACT, true, true>), g, b, 0, s, p);
-  }
+  if (op == kFwd) p.keep ? launch_gated_fwd<ACT, true>(p, grid, s) : launch_gated_fwd<ACT, false>(p, grid, s);
+  else if (p.g.n % kTileR == 0) hipLaunchKernelGGL((gated_kernel<kDgrad, false, ACT, false, true>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((gated_kernel<kDgrad, false, ACT, true, true>), g, b, 0, s, p);
 }
 
 hipError_t launch_gated(Op op, const GatedParams& p, int grid, hipStream_t s) {
