@@ -59,10 +59,14 @@ Kernel kernel_of(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, in
     // of 2 x 1536 x 2048 152 / 140.
     const int64_t units = (active + m_rows / kGatedSmallRows) * ((f + kGatedSmallCols - 1) / kGatedSmallCols);
     if ((m_rows <= 32 * active && units <= 2 * cus) || (m_rows <= 16 * active && units <= 8 * cus)) return kSmall;
-    // Groups that fill a 256-row tile on average: the tile kernel.  Middle against tile: 64
-    // groups of 2 x 1536 x 2048, 128 rows on average 200 / 226, 256 rows 295 / 289; 4 and 8 of
-    // 2 x 4096 x 4096, 500 rows 175 / 163 and 329 / 287; 16 of 2 x 1000 x 2000, 188 rows 63 / 80.
-    return m_rows < 256 * active ? kMid : kTile;
+    // The tile kernel where groups fill a 256-row tile on average and its tiles (half of
+    // each group's last one is counted) 5/8 of the CUs.  Middle against tile: 64 groups of 2 x 1536
+    // x 2048, 128 rows on average 200 / 226, 256 rows 295 / 289; 4 and 8 of 2 x 4096 x 4096, 500
+    // rows 175 / 163 and 329 / 287; 16 of 2 x 1000 x 2000, 188 rows 63 / 78; one of 2 x 2048 x 2048,
+    // 1500 rows (102 tiles) 34 / 53; 2 of 2 x 2048 x 4096, 1000 rows (141) 70 / 77; one of 2 x 8192
+    // x 2048, 600 rows (181) 57 / 57; 4 of 2 x 2000 x 2000, 750 rows (219) 87 / 69.
+    const int64_t half_tiles = (m_rows / (kTileI / 2) + active) * ((f + kGatedCols - 1) / kGatedCols);
+    return m_rows < 256 * active || half_tiles * 4 < 5 * cus ? kMid : kTile;
   }
   // dgrad, whose tiles have twice the hidden columns.  Middle against tile: 64 groups of
   // 2048 x 1536, 64 rows on average 113 / 131, 128 rows 147 / 144, 256 rows 198 / 187; 16 of 2000 x

@@ -75,3 +75,25 @@ def check_dgrad(dy, w_down, gate_up, offs, name, d, rows):
     ta = np.abs(b) * (slope * t + (np.abs(dh) + t) * err) + 3 * U * np.abs(dh * b) * slope
     tb = act * t + (np.abs(dh) + t) * (act * (es + 4 * U) + np.abs(a) * TINY)
     inside(d[:rows], want, np.concatenate([ta, tb], 1) + 1e-38, "dgate_up")
+
+
+def kernel_of(op, m, e, n, f, cus=256):
+    """The kernel that takes a call ("small", "mid", "tile"), restated from the library's rule; n: k in
+    the forward."""
+    active, up = min(e, m), lambda a, b: -(-a // b)
+    if op == "fwd":
+        units = (active + m // 64) * up(f, 16)
+        if (m <= 32 * active and units <= 2 * cus) or (m <= 16 * active and units <= 8 * cus):
+            return "small"
+        return "mid" if m < 256 * active or (m // 128 + active) * up(f, 128) * 4 < 5 * cus else "tile"
+    if (m // 128 + active) * up(f, 128) < cus:
+        return "mid" if n <= 2048 else "tile"
+    return "mid" if m < 96 * active else "tile"
+
+
+def variant_of(op, m, e, n, f):
+    """The kernel and, of the tile kernel, its form: partial stages, stages in pairs."""
+    k = kernel_of(op, m, e, n, f)
+    if k != "tile":
+        return (op, k)
+    return (op, k, n % 32 != 0, op == "dgrad" or n % 32 != 0 or m >= 1024 * e)

@@ -8,7 +8,7 @@ import torch
 
 import moe_ragged_bf16_amd as mdg
 from oracle import gated as ref
-from _gated import DEV, U, bf16, check_dgrad, check_fwd, f64, inside, offsets
+from _gated import DEV, U, bf16, check_dgrad, check_fwd, f64, inside, offsets, variant_of
 
 pytestmark = pytest.mark.gpu
 
@@ -31,6 +31,21 @@ SIZES = [
     ([255, 0, 0, 513], 264, 1000, 520), ([1] * 40 + [0] * 20 + [3] * 4, 40, 64, 72), ([600], 1000, 136, 1000),
     ([2, 100, 1, 0, 48], 520, 2000, 2000), ([3000], 128, 64, 64), ([2100, 2050], 384, 512, 128),
 ]
+
+# sizes whose tiles fill the GPU: the 256-row tile kernels in all of their forms
+RAGGED = [513, 0, 1100, 1, 700, 257]
+SIZES += [(RAGGED, 1608, 40, 24), (RAGGED, 1608, 64, 96), (RAGGED, 1672, 200, 64), ([2100, 300], 2048, 96, 40),
+          ([2100, 0, 1900], 2056, 32, 8), ([255, 260, 256, 770], 2568, 328, 264), ([2600], 2176, 1000, 64), ([90, 20], 72, 40, 2056)]
+FORMS = {(op, k) for op, k in (("fwd", "small"), ("fwd", "mid"), ("dgrad", "mid"))} | {
+    ("fwd", "tile", False, False), ("fwd", "tile", False, True), ("fwd", "tile", True, True),
+    ("dgrad", "tile", False, True), ("dgrad", "tile", True, True)}
+
+
+def test_the_sizes_reach_every_form():
+    got = set()
+    for sizes, f, k, n in SIZES:
+        got |= {variant_of("fwd", sum(sizes), len(sizes), k, f), variant_of("dgrad", sum(sizes), len(sizes), n, f)}
+    assert FORMS <= got, FORMS - got
 
 
 @pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
@@ -61,7 +76,7 @@ def test_random_sizes():
         check_dgrad(dy, w2, r.gate_up, offs, "silu", d, sum(sizes))
 
 
-@pytest.mark.parametrize("sizes", [[3, 0, 2], [40, 0, 300]])
+@pytest.mark.parametrize("sizes", [[3, 0, 2], [40, 0, 300], [30_000, 0, 20_300]])
 def test_rows_of_no_group_are_left_and_any_form_of_offsets(sizes):
     f, k, n, m = 72, 64, 40, sum(sizes)
     x, w, dy, w2, offs = operands(sizes, f, k, n, 3, pad=21)
@@ -100,7 +115,7 @@ def test_no_rows_and_no_groups_with_rows(m):
 
 
 @pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
-@pytest.mark.parametrize("rows", [4, 300])
+@pytest.mark.parametrize("rows", [4, 300, 50_000])
 def test_special_values_stay_where_they_belong(rows, name):
     """Projections of any size, zeros of both signs and values that are not finite: each
     reaches its own h, da and db only, and far tails are exact zeros or the value itself."""
@@ -138,8 +153,9 @@ def test_special_values_stay_where_they_belong(rows, name):
     assert torch.isfinite(d[:, clean]).all()
 
 
-def test_nan_in_one_row_or_weight_stays_there():
-    sizes, f, k, n = [20, 300, 5], 136, 96, 72
+@pytest.mark.parametrize("sizes,f", [([20, 300, 5], 136), ([900, 1100, 700], 1608), ([20, 300, 5], 40_008)])
+def test_nan_in_one_row_or_weight_stays_there(sizes, f):
+    k, n, m, last = 96, 72, sum(sizes), sum(sizes[:2])
     x, w, dy, w2, offs = operands(sizes, f, k, n, 9)
     base = mdg.grouped_gated_gemm_fwd(x, w, offs, keep=True)
     x2, w_ = x.clone(), w.clone()
@@ -148,14 +164,14 @@ def test_nan_in_one_row_or_weight_stays_there():
     r = mdg.grouped_gated_gemm_fwd(x2, w_, offs, keep=True)
     hit = torch.zeros_like(base.h, dtype=torch.bool)
     hit[30] = True
-    hit[320:, 3] = True
+    hit[last:, 3] = True
     assert torch.equal(r.h[~hit], base.h[~hit]) and not torch.isfinite(r.h[hit]).any()
     dy2 = dy.clone()
-    dy2[319, 2] = float("inf")
+    dy2[last - 1, 2] = float("inf")
     d0 = mdg.grouped_gated_gemm_dgrad(dy, w2, base.gate_up, offs)
     d = mdg.grouped_gated_gemm_dgrad(dy2, w2, base.gate_up, offs)
-    rows = torch.arange(325, device=DEV) != 319
-    assert torch.equal(d[rows], d0[rows]) and not torch.isfinite(d[319]).any()
+    rows = torch.arange(m, device=DEV) != last - 1
+    assert torch.equal(d[rows], d0[rows]) and not torch.isfinite(d[last - 1]).any()
 
 
 @pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
@@ -246,7 +262,7 @@ def test_no_double_backward_and_needed_gradients_only():
     assert not mdg.grouped_gated_ffn(x, w, w2, offs).requires_grad
 
 
-@pytest.mark.parametrize("sizes", [[2, 0, 3], [300, 0, 40]])
+@pytest.mark.parametrize("sizes", [[2, 0, 3], [300, 0, 40], [12_000, 0, 9000]])
 def test_other_stream_and_graph_replay(sizes):
     f, k, n = 136, 200, 72
     x, w, dy, w2, offs = operands(sizes, f, k, n, 12)
