@@ -80,8 +80,8 @@ def grouped_gated_gemm_dgrad(dy: torch.Tensor, w_down: torch.Tensor, gate_up: to
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, w_down, offs, code, fuse):
-        keep = any(ctx.needs_input_grad[:3])
+    def forward(ctx, x, w, w_down, offs, code, fuse, record):
+        keep = record and any(ctx.needs_input_grad[:3])
         y, h, gate_up = native.ffn_fwd(x, w, w_down, offs, code, keep)
         if keep:
             ctx.save_for_backward(x, w, w_down, offs, h, gate_up)
@@ -100,7 +100,7 @@ class _GatedFfn(torch.autograd.Function):
         if not ctx.fuse:
             dx, dw, dw_down, _ = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h,
                                                 need_x + 2 * need_w + 4 * need_down)
-            return dx, dw, dw_down, None, None, None
+            return dx, dw, dw_down, None, None, None, None
         read = (("the output gradient", dy), ("x", x), ("offs", offs), ("w", w), ("w_down", w_down), ("h", h),
                 ("gate_up", gate_up))
         mgs = [_fused_main_grad(o, "grouped_gated_ffn", read) if need else None
@@ -108,13 +108,14 @@ class _GatedFfn(torch.autograd.Function):
         dx, _, _, d = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h, need_x + 8 * need_w)
         dw = _fused_wgrad(ctx.w_objs[0], mgs[0], d, x, offs) if need_w else None
         dw_down = _fused_wgrad(ctx.w_objs[1], mgs[1], dy, h, offs) if need_down else None
-        return dx, dw, dw_down, None, None, None
+        return dx, dw, dw_down, None, None, None, None
 
 
 @torch.compiler.disable
 def _apply_eagerly(x, w, w_down, offs, code, fuse):
     # (the library's calls are opaque to torch.compile: out of its graphs)
-    return _GatedFfn.apply(x, w, w_down, offs, code, fuse)
+    # (grad mode is off inside forward, and needs_input_grad does not follow it)
+    return _GatedFfn.apply(x, w, w_down, offs, code, fuse, torch.is_grad_enabled())
 
 
 def grouped_gated_ffn(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, offs: torch.Tensor, *,

@@ -127,6 +127,25 @@ def test_inference_mode_and_no_grad():
         assert not mdg.grouped_gated_ffn(v["x"].requires_grad_(), v["w"], v["w2"], OFFS).requires_grad
 
 
+def test_without_grad_mode_nothing_is_kept():
+    """Trained weights in a serving call: no projections, so the memory of weights that are not."""
+    x = torch.randn((4096, H), device=DEV).bfloat16()
+    offs = torch.tensor([1000, 1500, 1500, 4096], dtype=torch.int32, device=DEV)
+    w, w2 = (torch.randn(s, device=DEV).bfloat16() for s in ((E, 1024, H), (E, H, 512)))
+    peaks, ys = [], []
+    for trained in (False, False, True):  # (the first call fills the allocator)
+        ws = [t.requires_grad_(trained) for t in (w, w2)]
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        with torch.no_grad():
+            y = mdg.grouped_gated_ffn(x, *ws, offs)
+        peaks.append(torch.cuda.max_memory_allocated() - before)
+        ys.append(y)
+    assert peaks[2] == peaks[1]
+    assert torch.equal(ys[2], ys[1]) and not ys[2].requires_grad
+
+
 def test_retained_graph_gives_the_same_gradients_twice():
     v = {k: t.clone().requires_grad_() for k, t in inputs(7).items()}
     y = run(v)
