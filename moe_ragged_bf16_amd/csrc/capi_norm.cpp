@@ -46,13 +46,19 @@ bool apart(const Range (&outs)[O], const Range (&ins)[I]) {
 
 Range optional(const void* p, int64_t bytes) { return range_of(p, p ? bytes : 0); }
 
-int64_t bwd_blocks(int64_t tokens, int64_t hidden) {
+// Blocks of a gradient call.  More of them keep more rows on their way and leave more
+// sums to write and add: 512, and 1024 for long calls of bf16 rows of two waves, which
+// leave a SIMD one wave and half of fp32's bytes (512 / 1024 blocks in us, 16384 rows: bf16 of
+// 2048 104 / 89, of 1024 39 / 42, fp32 of 2048 151 / 163; 8192 bf16 rows of 4096 84 / 91; bf16 rows
+// of 2048: 4096 of them 30.5 / 27.4, 1024 15.4 / 19.0).
+int64_t bwd_blocks(int64_t tokens, int64_t hidden, int dtype) {
   const int rows = norm_rows_per_block((int)hidden);
-  return std::min<int64_t>((tokens + rows - 1) / rows, kNormMaxBlocks);
+  const bool more = dtype == MDG_BF16 && norm_waves((int)hidden) == 2 && tokens >= 8 * kNormMaxBlocks;
+  return std::min<int64_t>((tokens + rows - 1) / rows, more ? 2 * kNormMaxBlocks : kNormMaxBlocks);
 }
 
-size_t part_bytes(int64_t tokens, int64_t hidden) {
-  return align256((size_t)bwd_blocks(tokens, hidden) * 2 * (size_t)hidden * sizeof(float));
+size_t part_bytes(int64_t tokens, int64_t hidden) {  // (bf16 has the most)
+  return align256((size_t)bwd_blocks(tokens, hidden, MDG_BF16) * 2 * (size_t)hidden * sizeof(float));
 }
 
 }  // namespace
@@ -166,7 +172,7 @@ MDG_API mdg_status block_norm_bwd(const void* dout, const void* dnormed, const v
   p.hidden = (int32_t)hidden;
   p.fp32 = dtype == MDG_FP32;
   p.weight_fp32 = weight_dtype == MDG_FP32;
-  p.blocks = (int32_t)bwd_blocks(tokens, hidden);
+  p.blocks = (int32_t)bwd_blocks(tokens, hidden, dtype);
   p.scale = scale;
   return status(launch_norm_bwd(p, static_cast<hipStream_t>(stream)) == hipSuccess ? MDG_OK : MDG_EHIP);
 }

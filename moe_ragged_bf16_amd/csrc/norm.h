@@ -8,7 +8,7 @@
 namespace mdg {
 
 constexpr int kNormMaxHidden = 16384;
-constexpr int kNormMaxBlocks = 512;  // blocks of a gradient call that leave partial sums
+constexpr int kNormMaxBlocks = 512;  // blocks of a gradient call that leave partial sums (bwd_blocks of capi_norm.cpp)
 
 struct NormParams {
   const void* residual;     // [tokens, hidden]

@@ -8,10 +8,14 @@
 // One pass over the rows: a row lies in the registers of 1 to 16 waves, 16 values a
 // lane, and each sum over a row is DPP moves in a wave and one LDS exchange of the waves.
 // Sums run in fp32 in one fixed order without atomics: results are bitwise
-// reproducible.
+// reproducible.  The rows' bytes bound it: 16383 bf16 rows of 7168 with both norms 198 us, 4.75
+// TB/s read and written; 16384 of 2048 44 us, 6.1, where the caches hold some; one token 3.5 us, a
+// launch's own time.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "kernel_common.h"
 #include "norm.h"
@@ -186,6 +190,13 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void norm_fwd_kernel
 //   dweight = sum_t dnormed x,  dpost_weight = sum_t dz y rstd_y
 // so one exchange of three sums a row is enough.  The weights' gradients add up in the
 // lanes' registers over a block's rows; norm_finish_kernel adds the blocks.
+// Memory bounds it: 16383 bf16 rows of 7168 with everything (six rows read or written for
+// each) 287 us, 4.9 TB/s; 16384 fp32 rows of 2048 151 us, 5.3; one row of 16 waves at a time and
+// their barrier hold 4096 fp32 rows of 16384 at 4.1.  bf16 rows: at most 128 registers, so that 16
+// waves fit a CU (327 us with one block of 8).
+// kLean: fp32 rows of 16 waves, which have 128 registers a lane: rows of dout and y and
+// the weights are read again, from the caches, where they are used (held as for narrower
+// rows 72 registers spilled: 4096 rows of 16384 835 us, here 393).
 template <int WAVES, bool FP32>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ? 1 : 4) void norm_bwd_kernel(NormBwdParams p) {
   constexpr int kRows = WAVES == 1 ? 4 : 1, kLanes = 64 * WAVES;
@@ -195,17 +206,30 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ?
   const int lane = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
   const bool pre = p.weight != nullptr && p.dnormed != nullptr, post = p.post_weight != nullptr;
   const bool with_z = post || p.gate != nullptr;
+  constexpr bool kLean = FP32 && WAVES == 16;
   bool in[kPieces];
   Eight w[kPieces], wp[kPieces], aw[kPieces], ap[kPieces];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c0 = (lane + i * kLanes) * 8;
     in[i] = c0 < H;
-    if (in[i] && pre) w[i] = weights8(p.weight, p.weight_fp32, c0);
-    if (in[i] && post) wp[i] = weights8(p.post_weight, p.weight_fp32, c0);
+    if (!kLean && in[i] && pre) w[i] = weights8(p.weight, p.weight_fp32, c0);
+    if (!kLean && in[i] && post) wp[i] = weights8(p.post_weight, p.weight_fp32, c0);
 #pragma unroll
     for (int c = 0; c < 8; ++c) aw[i].v[c] = ap[i].v[c] = 0.0f;
   }
+  // A piece's weights: held, or read again (through an address that the compiler cannot
+  // know, or the loads would move out of the loop over rows).
+  const auto weights = [&](const Eight& held, const void* base, bool some,
+                           int i) -> std::conditional_t<kLean, Eight, const Eight&> {
+    if constexpr (kLean) {
+      int at = (lane + i * kLanes) * 8;
+      opaque(at);
+      return some ? weights8(base, p.weight_fp32, at) : Eight{};
+    } else {
+      return held;
+    }
+  };
   const float inv_h = 1.0f / (float)H;
   int turn = 0;
   for (int64_t t = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? threadIdx.x >> 6 : 0); t < p.tokens;
@@ -216,30 +240,43 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ?
     for (int i = 0; i < kPieces; ++i)
       if (in[i]) {
         const int64_t at = row + i * kLanes * 8;
-        if (p.dout) d[i] = load8<FP32>(p.dout, at);
+        if (!kLean && p.dout) d[i] = load8<FP32>(p.dout, at);
         if (pre) n[i] = load8<FP32>(p.dnormed, at), o[i] = load8<FP32>(p.out, at);
-        if (with_z) y[i] = load8<FP32>(p.y, at);
+        if (!kLean && with_z) y[i] = load8<FP32>(p.y, at);
       }
+    const auto again = [&](int i) {  // kLean: dout and y of a piece
+      if constexpr (kLean) {
+        __builtin_amdgcn_sched_barrier(0);
+        int at = i * kLanes * 8;
+        opaque(at);
+        if (p.dout) d[i] = load8<FP32>(p.dout, row + at);
+        if (with_z) y[i] = load8<FP32>(p.y, row + at);
+      }
+    };
     const float ro = pre ? p.rstd[t] : 0.0f, ry = post ? p.post_rstd[t] : 1.0f;
     const float gate = p.gate ? p.scale * p.gate[t] : p.scale;
     float s[3] = {0.0f, 0.0f, 0.0f};
     if (pre || with_z) {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
-        if (in[i])
+        if (in[i]) {
+          if (with_z) again(i);
+          const Eight& wi = weights(w[i], p.weight, pre, i);
+          const Eight& wpi = weights(wp[i], p.post_weight, post, i);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float x = pre ? value<FP32>(o[i], c) * ro : 0.0f;
-            const float g = pre ? value<FP32>(n[i], c) * w[i].v[c] : 0.0f;
+            const float g = pre ? value<FP32>(n[i], c) * wi.v[c] : 0.0f;
             s[0] = __builtin_fmaf(g, x, s[0]);
             if (with_z) {
               float z = value<FP32>(y[i], c) * ry;
-              if (post) z *= wp[i].v[c];
+              if (post) z *= wpi.v[c];
               const float dv = p.dout ? value<FP32>(d[i], c) : 0.0f;
               s[1] = __builtin_fmaf(__builtin_fmaf(ro, g, dv), z, s[1]);
               s[2] = __builtin_fmaf(x, z, s[2]);
             }
           }
+        }
       row_sums<WAVES>(s, s_red, turn);
     }
     const float m = s[0] * inv_h;
@@ -250,13 +287,16 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ?
     for (int i = 0; i < kPieces; ++i)
       if (in[i]) {
         const int64_t at = row + i * kLanes * 8;
+        again(i);
+        const Eight& wi = weights(w[i], p.weight, pre, i);
+        const Eight& wpi = weights(wp[i], p.post_weight, post, i);
         Eight dr, dv;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           float e = p.dout ? value<FP32>(d[i], c) : 0.0f;
           if (pre) {
             const float x = value<FP32>(o[i], c) * ro, nv = value<FP32>(n[i], c);
-            e = __builtin_fmaf(ro, __builtin_fmaf(-x, m, nv * w[i].v[c]), e);
+            e = __builtin_fmaf(ro, __builtin_fmaf(-x, m, nv * wi.v[c]), e);
             aw[i].v[c] = __builtin_fmaf(nv, x, aw[i].v[c]);
           }
           dr.v[c] = e;
@@ -264,7 +304,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ?
           dv.v[c] = dz;
           if (post) {
             const float yh = value<FP32>(y[i], c) * ry;
-            dv.v[c] = ry * __builtin_fmaf(-yh, back, dz * wp[i].v[c]);
+            dv.v[c] = ry * __builtin_fmaf(-yh, back, dz * wpi.v[c]);
             ap[i].v[c] = __builtin_fmaf(dz, yh, ap[i].v[c]);
           }
         }

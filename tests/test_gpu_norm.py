@@ -124,7 +124,7 @@ def test_sizes(T, H, dtype, wdtype):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T,H", [(6, 72), (2100, 264), (40, 2304)])
+@pytest.mark.parametrize("T,H", [(6, 72), (2100, 264), (40, 2304), (5, 16376)])
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_every_combination(T, H, dtype):
     for with_y, weight, post, gate in itertools.product((True, False), repeat=4):
@@ -140,6 +140,16 @@ def test_every_combination(T, H, dtype):
             _, grads = run(c, -0.5, 1e-5, dnormed=False)
             check({**c, "dnormed": None}, -0.5, 1e-5, got, grads)
             assert torch.all(grads.dweight == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T,H", [(4095, 1032), (4096, 1032), (5001, 2048)])
+def test_long_calls_around_the_rule_for_blocks(T, H, dtype):
+    c = make(T, H, dtype, FP, T)
+    got, grads = run(c, 0.25, 1e-6)
+    check(c, 0.25, 1e-6, got, grads)
+    _, grads2 = run(c, 0.25, 1e-6)
+    assert all(torch.equal(a, b) for a, b in zip(grads, grads2))
 
 
 def test_many_rows_of_a_narrow_width():
