@@ -5,7 +5,9 @@
 // which the launch is 3.4; here it takes 3.9 to 4.9 (plan 7.4 and 4.6 to 5.4, the 8-bit
 // product 13.5 and 7.1 to 8.5).  One token's route, whose five outputs are allocated
 // one by one, takes 7.4 to 8.1 (1.6 less when they shared a storage, which their
-// owner could then not save or free one by one).
+// owner could then not save or free one by one).  A call of the gated product takes 5 to 7,
+// a block norm 5.3, clipping of 4 tensors 8.2 and of 300 26; the gated feed-forward's forward and
+// backward pass, eight entries, 117 (238 with a Python call for each).
 //
 // The C entries are those of the library that the package has loaded; setup()
 // takes their addresses.

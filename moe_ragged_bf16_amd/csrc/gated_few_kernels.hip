@@ -98,7 +98,8 @@ __device__ __forceinline__ void settle(f32x4 (&acc)[I][J]) {
 // W_up, straight from memory into matrix operands, and the rows of x through the
 // caches.  Its four waves take pieces of 256 of K in turn and their sums are added in wave
 // order.  The weights' bytes bound it: all of a piece's loads go out before the first
-// product (16 of 16 bytes a lane, 12 waves to a CU).
+// product (16 of 16 bytes a lane, 12 waves to a CU).  2 rows in two groups of 2 x 14336 x 4096
+// take 83 us, 5.6 TB/s; 100 rows over 8 groups of 2 x 512 x 1024 8 us, most of it latency.
 constexpr int kSmallPiece = 256;
 
 template <int MB, int ACT>
@@ -194,10 +195,12 @@ __global__ __launch_bounds__(256, 3) void gated_small_kernel(GatedParams gp) {
 // waits.  What a CU takes in bounds it, 34 to 45 GB/s with all of them at it: 64 groups of
 // 128 rows on average of 2 x 1536 x 2048 take 200 us, 12 TB/s into LDS; rows that do not
 // start on cache lines (k no multiple of 64) ask for two lines where one would do, 16
-// groups of 188 rows on average of 2 x 1000 x 2000 62 us, of 2 x 1024 x 2048 47.
+// groups of 188 rows on average of 2 x 1000 x 2000 62 us, of 2 x 1024 x 2048 47.  With few rows
+// the weights' bytes do: 488 rows over 64 groups of 2 x 1536 x 2048 139 us, 5.7 TB/s.
 // (Tried and not kept: weights straight to registers and four buffers of rows, 192 KiB on
 // their way to a CU, 0 to 12 % longer; 256 rows and eight waves, a quarter fewer bytes but
-// one workgroup to a CU, 20 to 40 % longer.)
+// one workgroup to a CU, 20 to 40 % longer; two stages' loads and fragments at a time, so that
+// a line that both need is asked for at once: no faster for either k.)
 constexpr int kMidTile = kGatedMidTile;
 
 // Buffer B of operand A (0) or B (1); each a static array of its own, so that the compiler

@@ -327,7 +327,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ?
             s_part[(threadIdx.x >> 6) * 1024 + (lane + i * 64) * 8 + c] = which ? ap[i].v[c] : aw[i].v[c];
       __syncthreads();
       for (int c = threadIdx.x; c < H; c += 256)
-        part[c] = ((s_part[c] + s_part[1024 + c]) + s_part[2048 + c]) + s_part[3072 + c];
+        part[c] = ((s_part[c] + s_part[1024 + c]) + s_part[2 * 1024 + c]) + s_part[3 * 1024 + c];
     } else {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
