@@ -46,36 +46,57 @@ size_t workspace_of(Op op, int64_t m_rows, int64_t n, int64_t f, int32_t num_gro
 
 enum Kernel { kSmall, kMid, kTile };
 
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The middle kernel's tiles: 64 x 64 where there are few of them, at most two to a CU (dgrad
+// 3.5), as a tile of 128 x 128 alone on a CU takes 0.75 us for a stage of 64 (dgrad 1.1) and one of 64 x 64
+// 0.45 (0.65).  64 against 128, fwd: one group of 2 x 2048 x 2048, 100 rows 12.6 / 20; 4 of 2 x 520 x 1624,
+// 1111 rows (357 tiles) 18.4 / 19.7; one of 2 x 4096 x 4096, 300 rows (640) 50 / 44.  dgrad: one of 2048
+// x 2048, 1500 rows (768) 28 / 33; 2 of 456 x 280, 11127 rows (875) 16.6 / 19.7; 2 of 1000 x 1000, 4000
+// rows (1024) 25.5 / 24.2; 4 of 2048 x 2048, 2048 rows (1152) 54 / 44.
+int mid_tile(Op op, int64_t m_rows, int64_t f, int64_t active, int64_t cus) {
+  constexpr int kHalf = kGatedMidTile / 2;
+  const int64_t tiles = (m_rows / kHalf + active) * up(f, op == kFwd ? kHalf / 2 : kHalf);
+  return tiles * 2 <= (op == kFwd ? 4 : 7) * cus ? kHalf : kGatedMidTile;
+}
+
 // Which kernel takes a launch (one takes all of its groups).  The rules go by the most
-// groups that can have rows, as offs is not read here.  Times in us, weights from memory.
+// groups that can have rows, as offs is not read here.  n: what is summed over (k in the forward).
+// Times in us, weights from memory.
 Kernel kernel_of(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, int64_t cus) {
+  // tiles of the tile kernel, twice over (half of each group's last one is counted)
+  const int64_t half_tiles = (m_rows / (kTileI / 2) + active) * up(f, op == kFwd ? kGatedCols : kTileJ);
   if (op == kFwd) {
     // Few rows: the small kernel starts and ends faster and fills the GPU where the middle
     // one has too few tiles; with more rows it reads weights again for each 64 of them and
     // x through the caches, and with many units the middle kernel streams as well.  Small
-    // against middle: 16 rows of one group of 2 x 4096 x 4096 20 / 42, 30 of 2 x 8192 x 4096
-    // 41 / 46, 64 of them 62 / 48; 100 over 8 of 2 x 512 x 1024 8 / 13; 40 over 8 of 2 x 2048 x
-    // 2048 30 / 35, 200 42 / 35; 2 over 8 of 2 x 14336 x 4096 84 / 92, 16 310 / 303; 512 over 64
-    // of 2 x 1536 x 2048 152 / 140.
-    const int64_t units = (active + m_rows / kGatedSmallRows) * ((f + kGatedSmallCols - 1) / kGatedSmallCols);
-    if ((m_rows <= 32 * active && units <= 2 * cus) || (m_rows <= 16 * active && units <= 8 * cus)) return kSmall;
-    // The tile kernel where groups fill a 256-row tile on average and its tiles (half of
-    // each group's last one is counted) 5/8 of the CUs.  Middle against tile: 64 groups of 2 x 1536
-    // x 2048, 128 rows on average 200 / 226, 256 rows 295 / 289; 4 and 8 of 2 x 4096 x 4096, 500
-    // rows 175 / 163 and 329 / 287; 16 of 2 x 1000 x 2000, 188 rows 63 / 78; one of 2 x 2048 x 2048,
-    // 1500 rows (102 tiles) 34 / 53; 2 of 2 x 2048 x 4096, 1000 rows (141) 70 / 77; one of 2 x 8192
-    // x 2048, 600 rows (181) 57 / 57; 4 of 2 x 2000 x 2000, 750 rows (219) 87 / 69.
-    const int64_t half_tiles = (m_rows / (kTileI / 2) + active) * ((f + kGatedCols - 1) / kGatedCols);
-    return m_rows < 256 * active || half_tiles * 4 < 5 * cus ? kMid : kTile;
+    // against middle: one group of 2 x 4096 x 4096, 12 rows 20 / 30, 32 27 / 30, 64 51 / 31; 24 of 2 x
+    // 8192 x 4096 41 / 35; 80 over 4 of 2 x 1024 x 4096 25 / 30; 200 over 8 of 2 x 512 x 1024 12.3 / 8.7;
+    // 15 over 8 of 2 x 416 x 2176 10 / 13; 200 over 8 of 2 x 2048 x 2048 47 / 36; 2 over 8 of 2 x 14336
+    // x 4096 84 / 92, 16 310 / 303; 512 over 64 of 2 x 1536 x 2048 152 / 140.
+    const int64_t units = (active + m_rows / kGatedSmallRows) * up(f, kGatedSmallCols);
+    if ((m_rows <= 32 * active && units * 4 <= 5 * cus) || (m_rows <= 16 * active && units <= 8 * cus)) return kSmall;
+    // The tile kernel where groups fill a 256-row tile on average and its tiles 5/8 of the CUs, 9/8
+    // where k has up to 32 of its stages, over which it fills its pipeline and ends.  Middle
+    // against tile: 64 groups of 2 x 1536 x 2048, 128 rows on average 200 / 226, 256 rows 295 /
+    // 289; 4 and 8 of 2 x 4096 x 4096, 500 rows 175 / 163 and 329 / 287; 16 of 2 x 1000 x 2000, 188 rows 58 / 83;
+    // one of 2 x 2048 x 2048, 1500 rows 33 / 51; 2 of 2 x 2048 x 4096, 1000 rows 47 / 56; one of
+    // 2 x 8192 x 2048, 600 rows 59 / 57; 4 of 2 x 2048 x 2048, 3000 rows 69 / 62.  k up to 1024: 3 of 2 x
+    // 5904 x 600, 902 rows 35 / 48; 8 of 2 x 1024 x 1024, 8192 rows 54 / 64; one of 2 x 4096 x 1024, 2000 rows
+    // 39 / 35; 4 of 2 x 2048 x 1024, 4096 rows 49 / 57, 8192 86 / 88; 2 of 2 x 1024 x 512, 16000 rows 47 / 42.
+    return m_rows < 256 * active || half_tiles * 4 <= (n <= 1024 ? 9 : 5) * cus ? kMid : kTile;
   }
-  // dgrad, whose tiles have twice the hidden columns.  Middle against tile: 64 groups of
-  // 2048 x 1536, 64 rows on average 113 / 131, 128 rows 147 / 144, 256 rows 198 / 187; 16 of 2000 x
-  // 1000, 188 rows 49 / 44; 8 of 1024 x 512, 125 rows 20 / 30.  Where the middle kernel's tiles leave
-  // CUs idle, it takes 0.9 us for each 64 of n; the tile kernel cuts n: one group of
-  // 4096 x 4096, 300 rows 58 / 43.
-  const int64_t tiles = (m_rows / kGatedMidTile + active) * ((f + kGatedMidTile - 1) / kGatedMidTile);
-  if (tiles < cus) return n <= 2048 ? kMid : kTile;
-  return m_rows < 96 * active ? kMid : kTile;
+  // dgrad, whose tiles have twice the hidden columns, cut along n by the tile kernel where there
+  // are few.  Middle against tile, tiles of 64: one group of 4096 x 4096, 300 rows 50 / 43; 4 of 4096 x
+  // 512, 600 rows 39 / 33; 2 of 3000 x 1024, 200 rows 29 / 28; 8 of 2560 x 1024, 1200 rows 37 / 39; one of
+  // 2048 x 2048, 1500 rows 28 / 41; 8 of 1024 x 512, 125 rows 13 / 21.
+  if (mid_tile(op, m_rows, f, active, cus) != kGatedMidTile) return n <= 2560 ? kMid : kTile;
+  // Tiles of 128: 64 groups of 2048 x 1536, 64 rows on average 113 / 131, 128 rows 147 / 144, 256 rows 198 /
+  // 187; 16 of 2000 x 1000, 188 rows 48 / 49; 4 of 2048 x 2048, 3000 rows 46 / 55, 4096 73 / 68; one of
+  // 2048 x 8192, 600 rows 43 / 51; 8 of 2048 x 1024, 8192 rows 74 / 65, of 1024 x 1024 45 / 45; 2 of 1000 x 1000,
+  // 4000 rows 24 / 39; 4 of 512 x 2048, 8192 rows 49 / 57; one of 512 x 4096, 16384 rows 204 / 151.
+  if (m_rows < 96 * active || (half_tiles <= cus && n <= 2048)) return kMid;
+  return half_tiles * 4 <= 9 * cus && n <= 1024 ? kMid : kTile;
 }
 
 int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, void* workspace, void* stream) {
@@ -86,16 +107,16 @@ int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, vo
   if (!dev.gfx950) return MDG_EUNSUPPORTED;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t cus = dev.cus > 0 ? dev.cus : 256, active = std::min<int64_t>(num_groups, m_rows);
-  Kernel which = kernel_of(op, m_rows, p->g.n, f, active, cus);
-  const int64_t cols = op == kFwd ? kGatedMidTile / 2 : kGatedMidTile;
-  const int64_t row_tiles = (m_rows + kGatedMidTile - 1) / kGatedMidTile + active;
+  Kernel which = kernel_of(op, m_rows, op == kFwd ? p->g.k : p->g.n, f, active, cus);
+  const int tile = mid_tile(op, m_rows, f, active, cus);
+  const int64_t cols = op == kFwd ? tile / 2 : tile, row_tiles = (m_rows + tile - 1) / tile + active;
   const int64_t mid = (row_tiles * ((f + cols - 1) / cols) + 7) / 8 * 8;
   if (which == kMid && mid * 256 > UINT32_MAX) which = kTile;  // (a launch's work-items)
   hipError_t err = hipSuccess;
   if (which == kSmall) {
     err = launch_gated_small(*p, (int)(active + m_rows / kGatedSmallRows), s);
   } else if (which == kMid) {
-    err = launch_gated_mid(op, *p, (int)mid, s);
+    err = launch_gated_mid(op, *p, tile, (int)mid, s);
   } else {
     const int64_t units = units_of(op, m_rows, f, num_groups), slots = slots_of(units);
     char* ws = static_cast<char*>(workspace);

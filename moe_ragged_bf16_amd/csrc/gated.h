@@ -35,7 +35,7 @@ struct GatedTail {
 
 hipError_t launch_gated(Op op, const GatedParams& p, int grid, hipStream_t s);
 hipError_t launch_gated_small(const GatedParams& p, int pieces, hipStream_t s);  // fwd
-hipError_t launch_gated_mid(Op op, const GatedParams& p, int grid, hipStream_t s);
+hipError_t launch_gated_mid(Op op, const GatedParams& p, int tile, int grid, hipStream_t s);  // tile: kGatedMidTile or half
 hipError_t launch_gated_reduce(Op op, const GatedParams& p, int grid_x, int grid_y, hipStream_t s);
 
 }  // namespace mdg

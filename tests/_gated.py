@@ -77,23 +77,38 @@ def check_dgrad(dy, w_down, gate_up, offs, name, d, rows):
     inside(d[:rows], want, np.concatenate([ta, tb], 1) + 1e-38, "dgate_up")
 
 
+def up(a, b):
+    return -(-a // b)
+
+
+def mid_tile(op, m, e, f, cus=256):
+    """The middle kernel's tiles, restated from the library's rule."""
+    tiles = (m // 64 + min(e, m)) * up(f, 32 if op == "fwd" else 64)
+    return 64 if tiles * 2 <= (4 if op == "fwd" else 7) * cus else 128
+
+
 def kernel_of(op, m, e, n, f, cus=256):
     """The kernel that takes a call ("small", "mid", "tile"), restated from the library's rule; n: k in
     the forward."""
-    active, up = min(e, m), lambda a, b: -(-a // b)
+    active = min(e, m)
+    half_tiles = (m // 128 + active) * up(f, 128 if op == "fwd" else 256)
     if op == "fwd":
         units = (active + m // 64) * up(f, 16)
-        if (m <= 32 * active and units <= 2 * cus) or (m <= 16 * active and units <= 8 * cus):
+        if (m <= 32 * active and units * 4 <= 5 * cus) or (m <= 16 * active and units <= 8 * cus):
             return "small"
-        return "mid" if m < 256 * active or (m // 128 + active) * up(f, 128) * 4 < 5 * cus else "tile"
-    if (m // 128 + active) * up(f, 128) < cus:
-        return "mid" if n <= 2048 else "tile"
-    return "mid" if m < 96 * active else "tile"
+        return "mid" if m < 256 * active or half_tiles * 4 <= (9 if n <= 1024 else 5) * cus else "tile"
+    if mid_tile(op, m, e, f, cus) == 64:
+        return "mid" if n <= 2560 else "tile"
+    if m < 96 * active or (half_tiles <= cus and n <= 2048):
+        return "mid"
+    return "mid" if half_tiles * 4 <= 9 * cus and n <= 1024 else "tile"
 
 
 def variant_of(op, m, e, n, f):
-    """The kernel and, of the tile kernel, its form: partial stages, stages in pairs."""
+    """The kernel and its form: the middle kernel's tiles; the tile kernel's partial stages and stages in pairs."""
     k = kernel_of(op, m, e, n, f)
-    if k != "tile":
+    if k == "mid":
+        return (op, k, mid_tile(op, m, e, f))
+    if k == "small":
         return (op, k)
     return (op, k, n % 32 != 0, op == "dgrad" or n % 32 != 0 or m >= 1024 * e)

@@ -35,8 +35,12 @@ SIZES = [
 # sizes whose tiles fill the GPU: the 256-row tile kernels in all of their forms
 RAGGED = [513, 0, 1100, 1, 700, 257]
 SIZES += [(RAGGED, 1608, 40, 24), (RAGGED, 1608, 64, 96), (RAGGED, 1672, 200, 64), ([2100, 300], 2048, 96, 40),
-          ([2100, 0, 1900], 2056, 32, 8), ([255, 260, 256, 770], 2568, 328, 264), ([2600], 2176, 1000, 64), ([90, 20], 72, 40, 2056)]
-FORMS = {(op, k) for op, k in (("fwd", "small"), ("fwd", "mid"), ("dgrad", "mid"))} | {
+          ([2100, 0, 1900], 2056, 32, 8), ([255, 260, 256, 770], 2568, 328, 264), ([2600], 2176, 1000, 64), ([90, 20], 72, 40, 2056),
+          (RAGGED, 1608, 1056, 2080), (RAGGED, 1608, 1064, 2056), ([8200], 2312, 40, 24), ([130, 65], 328, 72, 2600)]
+# the middle kernel's two tiles, whole and partial, in one group and several
+SIZES += [([64], 32, 64, 64), ([65, 0, 63, 128], 96, 136, 128), ([129], 40, 328, 72), ([64, 64, 1], 264, 2048, 192),
+          ([1500, 700, 3], 1096, 136, 264), ([1281], 1928, 200, 128)]
+FORMS = {("fwd", "small"), ("fwd", "mid", 64), ("fwd", "mid", 128), ("dgrad", "mid", 64), ("dgrad", "mid", 128)} | {
     ("fwd", "tile", False, False), ("fwd", "tile", False, True), ("fwd", "tile", True, True),
     ("dgrad", "tile", False, True), ("dgrad", "tile", True, True)}
 
@@ -76,7 +80,7 @@ def test_random_sizes():
         check_dgrad(dy, w2, r.gate_up, offs, "silu", d, sum(sizes))
 
 
-@pytest.mark.parametrize("sizes", [[3, 0, 2], [40, 0, 300], [30_000, 0, 20_300]])
+@pytest.mark.parametrize("sizes", [[3, 0, 2], [40, 0, 300], [30_000, 0, 20_300], [60_000, 0, 40_000]])
 def test_rows_of_no_group_are_left_and_any_form_of_offsets(sizes):
     f, k, n, m = 72, 64, 40, sum(sizes)
     x, w, dy, w2, offs = operands(sizes, f, k, n, 3, pad=21)
@@ -153,7 +157,8 @@ def test_special_values_stay_where_they_belong(rows, name):
     assert torch.isfinite(d[:, clean]).all()
 
 
-@pytest.mark.parametrize("sizes,f", [([20, 300, 5], 136), ([900, 1100, 700], 1608), ([20, 300, 5], 40_008)])
+@pytest.mark.parametrize("sizes,f", [([20, 300, 5], 136), ([900, 1100, 700], 1608), ([20, 300, 5], 40_008),
+                                     ([3000, 2600, 2700], 2056)])
 def test_nan_in_one_row_or_weight_stays_there(sizes, f):
     k, n, m, last = 96, 72, sum(sizes), sum(sizes[:2])
     x, w, dy, w2, offs = operands(sizes, f, k, n, 9)
@@ -262,7 +267,7 @@ def test_no_double_backward_and_needed_gradients_only():
     assert not mdg.grouped_gated_ffn(x, w, w2, offs).requires_grad
 
 
-@pytest.mark.parametrize("sizes", [[2, 0, 3], [300, 0, 40], [12_000, 0, 9000]])
+@pytest.mark.parametrize("sizes", [[2, 0, 3], [300, 0, 40], [12_000, 0, 9000], [45_000, 0, 30_001]])
 def test_other_stream_and_graph_replay(sizes):
     f, k, n = 136, 200, 72
     x, w, dy, w2, offs = operands(sizes, f, k, n, 12)
