@@ -17,7 +17,7 @@ namespace mdg {
 namespace {
 
 constexpr int64_t kMaxTensors = 65536;
-constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of a tensor: a launch's units stay below 2^31
+constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of a tensor: a launch's units stay below 2^31, a size in 38 bits
 
 int64_t bytes_of(const mdg_gradient& g) { return g.elements * (g.dtype == MDG_FP32 ? 4 : 2); }
 int64_t launches_of(int64_t count, bool apart) { return (count + clip_tensors(apart) - 1) / clip_tensors(apart); }
@@ -31,7 +31,10 @@ int check_device() {
   return dev.gfx950 ? MDG_OK : MDG_EUNSUPPORTED;
 }
 
-bool on_element(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == MDG_FP32 ? 4 : 2) == 0; }
+// (an address of more than 48 bits is none of the device's)
+bool on_element(const void* p, int dtype) {
+  return reinterpret_cast<uintptr_t>(p) % (dtype == MDG_FP32 ? 4 : 2) == 0 && reinterpret_cast<uintptr_t>(p) >> 48 == 0;
+}
 
 int check_gradients(const mdg_gradient* g, int64_t count, bool scaled) {
   if (count < 0 || (count > 0 && !g)) return MDG_EINVAL;
@@ -77,9 +80,17 @@ ClipTable table_of(const mdg_gradient* g, int64_t count, int64_t k, bool apart) 
   const int capacity = clip_tensors(apart);
   int64_t units = 0;
   for (int64_t i = k * capacity; i < std::min(count, (k + 1) * capacity); ++i) {
-    t.words[t.count] = reinterpret_cast<uint64_t>(g[i].data);
-    t.words[capacity + t.count] = 2 * (uint64_t)g[i].elements + (g[i].dtype == MDG_FP32);
-    if (apart) t.words[2 * capacity + t.count] = reinterpret_cast<uint64_t>(g[i].out);
+    const bool some = g[i].elements > 0;  // (pointers of empty tensors may be anything)
+    const uint64_t src = some ? reinterpret_cast<uint64_t>(g[i].data) : 0, dst = some ? reinterpret_cast<uint64_t>(g[i].out) : 0;
+    const uint64_t size = 2 * (uint64_t)g[i].elements + (g[i].dtype == MDG_FP32);
+    uint32_t* w = t.words + t.count;
+    w[0] = (uint32_t)src;
+    w[capacity] = (uint32_t)(src >> 32) | (uint32_t)(size >> 32) << 16;
+    w[2 * capacity] = (uint32_t)size;
+    if (apart) {
+      w[3 * capacity] = (uint32_t)dst;
+      w[4 * capacity] = (uint32_t)(dst >> 32);
+    }
     ++t.count;
     units += (bytes_of(g[i]) + kClipUnitBytes - 1) / kClipUnitBytes;
   }

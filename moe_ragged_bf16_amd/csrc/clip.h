@@ -7,17 +7,19 @@
 
 namespace mdg {
 
-constexpr int kClipWords = 492;         // of the table in a launch's arguments (below 4 KiB)
+constexpr int kClipWords = 1008;        // 32-bit ones of the table in a launch's arguments (4 KiB in all)
 constexpr int kClipUnitBytes = 32768;   // bytes of a tensor that a workgroup takes at a time
 constexpr int kClipBlocks = 1024;       // workgroups of a launch, at most
 
-// Tensors of one launch: two words each where an output is its own gradient (or there are
-// none), else three.
-constexpr int clip_tensors(bool apart) { return kClipWords / (apart ? 3 : 2); }
+// Words of a tensor: its address's low half, 22 bits above them (16 of the address, 6 of the
+// size), the size's low half, and where outputs are apart the output's address in two.  (An address
+// has 48 bits.)  The size is 2 elements + (1: fp32), of 38 bits.
+constexpr int clip_words(bool apart) { return apart ? 5 : 3; }
+constexpr int clip_tensors(bool apart) { return kClipWords / clip_words(apart); }  // of one launch
 
 // The tensors of one launch, by value.
 struct ClipTable {
-  uint64_t words[kClipWords];           // addresses [capacity], elements [capacity], outputs' addresses
+  uint32_t words[kClipWords];           // [words of a tensor][capacity]
   int32_t count;
   int32_t apart;                        // outputs have addresses of their own
   int32_t blocks;                       // of the norm kernel (and partial sums of this launch)

@@ -2,7 +2,7 @@
 //
 //   norm = sqrt(sum over all tensors of g^2),  g' = g min(1, max_norm / (norm + eps))
 //
-// A launch takes up to 246 tensors by value in its arguments, so nothing is copied to
+// A launch takes up to 336 tensors by value in its arguments, so nothing is copied to
 // the device and a captured launch keeps its tensors.  Each tensor is cut into units
 // of 32 KiB; a workgroup walks units b, b + grid, ..., so the sums' order is a function of
 // the sizes.  Squares and sums are in 64 bits: no square of an fp32 value overflows or
@@ -11,7 +11,7 @@
 //
 // Memory bounds both kernels: two fp32 tensors of 302 million values each (2.4 GB read twice,
 // written once) take 422 us for the norm (5.7 TB/s) and 907 to scale (5.3 TB/s read and
-// written); 301 tensors of 60 million values in all, two launches of each, 139.  Nine tensors of
+// written); 301 tensors of 60 million values in all 133 (139 in two launches of each).  Nine tensors of
 // 0.3 million take 10.8: two launches, one waiting for the other's sums, 4.8 and 7.0.
 
 #include <hip/hip_runtime.h>
@@ -42,22 +42,28 @@ struct ClipLds {
   int before[clip_tensors(false) + 1];
   int scratch[4];
 };
-static_assert(clip_tensors(false) <= kClipThreads, "a thread for every tensor");
+static_assert(clip_tensors(false) <= 2 * kClipThreads, "two tensors to a thread");
 
 // Fills it; returns the number of units.
 __device__ __forceinline__ int clip_units(const ClipTable& t, ClipLds& s) {
-  const int i = threadIdx.x, capacity = clip_tensors(t.apart);
-  int units = 0;
-  if (i < t.count) {
-    const uint64_t src = t.words[i], n = t.words[capacity + i];
+  const int capacity = clip_tensors(t.apart);
+  int units[2] = {0, 0};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = 2 * threadIdx.x + q;
+    if (i >= t.count) continue;
+    const uint32_t mid = t.words[capacity + i];
+    const uint64_t src = (uint64_t)(mid & 0xffffu) << 32 | t.words[i];
+    const uint64_t n = (uint64_t)(mid >> 16) << 32 | t.words[2 * capacity + i];
     s.src[i] = src;
     s.elements[i] = n;
-    s.dst[i] = t.apart ? t.words[2 * capacity + i] : src;
-    units = (int)(((int64_t)(n >> 1) * ((n & 1) ? 4 : 2) + kClipUnitBytes - 1) / kClipUnitBytes);
+    s.dst[i] = t.apart ? (uint64_t)t.words[4 * capacity + i] << 32 | t.words[3 * capacity + i] : src;
+    units[q] = (int)(((int64_t)(n >> 1) * ((n & 1) ? 4 : 2) + kClipUnitBytes - 1) / kClipUnitBytes);
   }
   int total;
-  const int b = block_excl_sum(units, s.scratch, &total);
+  const int b = block_excl_sum(units[0] + units[1], s.scratch, &total), i = 2 * threadIdx.x;
   if (i < t.count) s.before[i] = b;
+  if (i + 1 < t.count) s.before[i + 1] = b + units[0];
   if (i == 0) s.before[t.count] = total;
   __syncthreads();
   return total;

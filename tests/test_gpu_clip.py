@@ -56,7 +56,7 @@ def check(before, after, got, max_norm, norm=None):
 
 @pytest.mark.parametrize("lengths", [
     [1], [0], [0, 0, 5], [7, 8], [1, 2, 3, 4, 5, 6, 7, 8, 9], [16384], [8192, 8192], [16383, 8191], [16385, 8193, 0, 40],
-    [100_003, 1, 77], [3] * 163, [5] * 164, [3, 40] * 82 + [9], [7] * 246, [1] * 247, [1] * 300, [4] * 493, [2_000_003, 999], [40_000_001]])
+    [100_003, 1, 77], [3] * 163, [5] * 164, [3, 40] * 82 + [9], [7] * 246, [1] * 247, [1] * 300, [2] * 201, [6] * 202, [3, 1] * 168, [5] * 337, [1] * 673, [4] * 493, [2_000_003, 999], [40_000_001]])
 @pytest.mark.parametrize("max_norm", [0.25, 1e9])
 def test_clipped_in_place_and_into_others(lengths, max_norm):
     grads = make(lengths, len(lengths))

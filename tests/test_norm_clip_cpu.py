@@ -80,8 +80,8 @@ def table(*rows):
 
 def test_clip_refusals(lib):
     need = lib.grad_norm_workspace_bytes(2)
-    assert need == 1024 * 8 and lib.grad_norm_workspace_bytes(246) == need
-    assert lib.grad_norm_workspace_bytes(247) == 2 * need
+    assert need == 1024 * 8 and lib.grad_norm_workspace_bytes(336) == need
+    assert lib.grad_norm_workspace_bytes(337) == 2 * need
     assert lib.grad_norm_workspace_bytes(-1) == 0 and lib.grad_norm_workspace_bytes(65537) == 0
     assert lib.grad_norm_workspace_bytes(0) == 0
     ok = ((P[0], P[1], 100, FP32), (P[2], P[2], 100, BF16))
