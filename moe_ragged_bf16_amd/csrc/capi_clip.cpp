@@ -17,9 +17,10 @@ namespace mdg {
 namespace {
 
 constexpr int64_t kMaxTensors = 65536;
-constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of a tensor: a launch's units stay below 2^31, a size in 38 bits
+constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of a tensor: its size has 38 bits in a launch's arguments
 
 int64_t bytes_of(const mdg_gradient& g) { return g.elements * (g.dtype == MDG_FP32 ? 4 : 2); }
+int64_t units_of(const mdg_gradient& g) { return (bytes_of(g) + kClipUnitBytes - 1) / kClipUnitBytes; }
 int64_t launches_of(int64_t count, bool apart) { return (count + clip_tensors(apart) - 1) / clip_tensors(apart); }
 size_t workspace_of(int64_t count) { return (size_t)launches_of(count, false) * kClipBlocks * sizeof(double); }
 
@@ -39,12 +40,15 @@ bool on_element(const void* p, int dtype) {
 int check_gradients(const mdg_gradient* g, int64_t count, bool scaled) {
   if (count < 0 || (count > 0 && !g)) return MDG_EINVAL;
   if (count > kMaxTensors) return MDG_EUNSUPPORTED;
+  int64_t units = 0;  // of all tensors: the kernels count a launch's in 32 bits
   for (int64_t i = 0; i < count; ++i) {
     const mdg_gradient& x = g[i];
     if ((x.dtype != MDG_BF16 && x.dtype != MDG_FP32) || x.elements < 0) return MDG_EINVAL;
     if (x.elements > kMaxElements) return MDG_EUNSUPPORTED;
     if (x.elements > 0 && (!x.data || !on_element(x.data, x.dtype))) return MDG_EINVAL;
     if (scaled && x.elements > 0 && (!x.out || !on_element(x.out, x.dtype))) return MDG_EINVAL;
+    units += units_of(x);
+    if (units > INT32_MAX) return MDG_EUNSUPPORTED;
   }
   return MDG_OK;
 }
@@ -92,7 +96,7 @@ ClipTable table_of(const mdg_gradient* g, int64_t count, int64_t k, bool apart) 
       w[4 * capacity] = (uint32_t)(dst >> 32);
     }
     ++t.count;
-    units += (bytes_of(g[i]) + kClipUnitBytes - 1) / kClipUnitBytes;
+    units += units_of(g[i]);
   }
   t.apart = apart;
   t.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(units, kClipBlocks));

@@ -99,6 +99,8 @@ def test_clip_refusals(lib):
                     (P[0] + 1, P[1], 1, BF16)):
             assert call(rows=(ok[1], row)) == EINVAL, row
         assert call(rows=((P[0], P[1], 2 ** 36 + 1, BF16),), wsn=need) == EUNSUP
+        assert call(rows=((P[0], P[1], 2 ** 36, FP32),) * 300, wsn=need) == EUNSUP      # 2.5e9 pieces
+        assert call(rows=(ok[1], (P[0] + 2 ** 48, P[1], 1, FP32))) == EINVAL
         assert call(norm=P[0] + 396) == EOVERLAP and call(ws=P[0]) == EOVERLAP and call(norm=P[6]) == EOVERLAP
     assert lib.grad_norm(None, 1, P[5], P[6], need, None) == EINVAL
     assert clip(limit=-1.0) == EINVAL and clip(limit=float("nan")) == EINVAL
