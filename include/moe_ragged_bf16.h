@@ -526,7 +526,7 @@ MDG_API mdg_status block_norm_bwd(const void* dout, const void* dnormed, const v
  *   gradients   `count` (up to 65536) tensors, in HOST memory, read before the call returns: data (read) and
  *               out (written by grad_clip; out == data: in place) of `elements` values of dtype MDG_BF16 or
  *               MDG_FP32 on the device, aligned to their type.  Pointers of empty tensors may be NULL.
- *               Up to 2^36 values each, and 2^31 pieces of 32 KiB in all.
+ *               Up to 2^36 values each, and fewer than 2^31 - 1024 pieces of 32 KiB in all.
  *   norm        one fp32 value on the device, written: the norm, squares and sums in 64 bits.
  *   norm_in     grad_clip: one fp32 value on the device to clip by; NULL: the gradients' norm, which
  *               norm receives (norm is NULL otherwise).

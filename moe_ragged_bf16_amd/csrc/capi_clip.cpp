@@ -40,7 +40,9 @@ bool on_element(const void* p, int dtype) {
 int check_gradients(const mdg_gradient* g, int64_t count, bool scaled) {
   if (count < 0 || (count > 0 && !g)) return MDG_EINVAL;
   if (count > kMaxTensors) return MDG_EUNSUPPORTED;
-  int64_t units = 0;  // of all tensors: the kernels count a launch's in 32 bits
+  // Of all tensors.  The kernels count a launch's in 32 bits, and a workgroup's count passes
+  // the last one by up to a launch's workgroups.
+  int64_t units = 0;
   for (int64_t i = 0; i < count; ++i) {
     const mdg_gradient& x = g[i];
     if ((x.dtype != MDG_BF16 && x.dtype != MDG_FP32) || x.elements < 0) return MDG_EINVAL;
@@ -48,7 +50,7 @@ int check_gradients(const mdg_gradient* g, int64_t count, bool scaled) {
     if (x.elements > 0 && (!x.data || !on_element(x.data, x.dtype))) return MDG_EINVAL;
     if (scaled && x.elements > 0 && (!x.out || !on_element(x.out, x.dtype))) return MDG_EINVAL;
     units += units_of(x);
-    if (units > INT32_MAX) return MDG_EUNSUPPORTED;
+    if (units > INT32_MAX - kClipBlocks) return MDG_EUNSUPPORTED;
   }
   return MDG_OK;
 }
