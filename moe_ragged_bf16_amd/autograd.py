@@ -176,7 +176,7 @@ class CakeGroupedDetMm(torch.autograd.Function):
         if torch.is_grad_enabled():
             raise NotImplementedError("cake_grouped_det_mm has no double backward (create_graph=True)")
         x, w, offs = ctx.saved_tensors
-        dy = dy.contiguous()
+        dy = ops.incoming_gradient(dy)
         need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         E = w.shape[0]
         dx = dw = None

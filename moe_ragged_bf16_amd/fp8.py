@@ -113,7 +113,7 @@ class _Fp8Mm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, offs, qt, scale_t = ctx.saved_tensors
-        dy = dy.contiguous()
+        dy = ops.incoming_gradient(dy)
         dx = dw = None
         if ctx.needs_input_grad[0]:
             dx = grouped_fp8_gemm_dgrad(dy, qt, scale_t, offs)

@@ -27,6 +27,7 @@ import torch
 from . import _capi
 from ._capi import native, refuse_tracing
 from .autograd import _fused_main_grad, _fused_wgrad, _main_grad
+from .ops import incoming_gradient
 
 __all__ = ["GatedRows", "grouped_gated_gemm_fwd", "grouped_gated_gemm_dgrad", "grouped_gated_ffn",
            "gated_gemm_fwd_workspace_bytes", "gated_gemm_dgrad_workspace_bytes"]
@@ -95,7 +96,7 @@ class _GatedFfn(torch.autograd.Function):
         if torch.is_grad_enabled():
             raise NotImplementedError("grouped_gated_ffn has no double backward (create_graph=True)")
         x, w, w_down, offs, h, gate_up = ctx.saved_tensors
-        dy = dy.contiguous()
+        dy = incoming_gradient(dy)
         need_x, need_w, need_down = ctx.needs_input_grad[:3]
         if not ctx.fuse:
             dx, dw, dw_down, _ = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h,

@@ -22,6 +22,7 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from ._capi import native, refuse_tracing
+from .ops import incoming_gradient
 
 __all__ = ["MoeRoute", "MoePlan", "moe_route", "moe_route_fwd", "moe_route_bwd", "moe_plan", "moe_dispatch",
            "moe_dispatch_fwd", "moe_dispatch_bwd", "moe_combine", "moe_combine_fwd", "moe_combine_bwd"]
@@ -144,7 +145,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, drows):
-        return moe_dispatch_bwd(drows.contiguous(), MoePlan(*ctx.saved_tensors)), None, None
+        return moe_dispatch_bwd(incoming_gradient(drows), MoePlan(*ctx.saved_tensors)), None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -157,7 +158,7 @@ class _Combine(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         y, weight, offs, dest = ctx.saved_tensors
-        dy, dweight = moe_combine_bwd(dout.contiguous(), y, weight, MoePlan(offs, dest))
+        dy, dweight = moe_combine_bwd(incoming_gradient(dout), y, weight, MoePlan(offs, dest))
         return dy, dweight, None, None
 
 

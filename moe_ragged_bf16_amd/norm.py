@@ -21,6 +21,7 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from ._capi import native, refuse_tracing
+from .ops import incoming_gradient
 
 __all__ = ["BlockNorm", "BlockNormGrads", "block_norm", "block_norm_fwd", "block_norm_bwd"]
 
@@ -88,7 +89,7 @@ class _BlockNorm(torch.autograd.Function):
         dout, dnormed = grads if ctx.with_y else (None, grads[0])
         if dout is None and dnormed is None:
             return (None,) * 7
-        dout, dnormed = (None if g is None else g.contiguous() for g in (dout, dnormed))
+        dout, dnormed = (None if g is None else incoming_gradient(g) for g in (dout, dnormed))
         need = sum(1 << i for i in range(5) if ctx.needs_input_grad[i])
         g = _bwd(dout, dnormed, BlockNorm(out, None, rstd, post_rstd), y, weight, post_weight, gate, ctx.scale, need)
         return (*g, None, None)

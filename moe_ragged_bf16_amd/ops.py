@@ -64,6 +64,14 @@ def _written(t: torch.Tensor) -> None:
         torch.autograd.graph.increment_version(t)
 
 
+def incoming_gradient(g: torch.Tensor) -> torch.Tensor:
+    """An output's gradient as the entries read it, contiguous and starting on 16
+    bytes: autograd hands over views that start anywhere in their buffer (the
+    gradient of a flattened ``torch.cat``, say)."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 def _same_device(*ts):
     d = ts[0].device
     for t in ts[1:]:
