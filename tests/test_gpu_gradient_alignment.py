@@ -16,7 +16,7 @@ def inputs():
     g.manual_seed(1)
     r = lambda *s: torch.randn(s, generator=g, device=DEV)
     return {"x": r(T, H).bfloat16(), "w": (r(E, 2 * F, H) / 8).bfloat16(), "w2": (r(E, H, F) / 7).bfloat16(),
-            "res": r(T, H).bfloat16(), "n": r(H), "p": r(H), "gate": r(T), "weight": torch.rand((T, 2), device=DEV)}
+            "res": r(T, H).bfloat16(), "n": r(H), "p": r(H), "gate": r(T), "weight": torch.rand((T, 2), generator=g, device=DEV)}
 
 
 OFFS = torch.tensor([7, 7, T], dtype=torch.int32, device=DEV) if torch.cuda.is_available() else None
