@@ -40,8 +40,8 @@ not differentiable), and so does ``torch.jit.trace``.  ``torch.compile`` with
 ``fullgraph=True`` fails at the same refusal; otherwise torch.compile runs the
 call eagerly outside its graphs.
 
-Memory: a non-contiguous (but valid) main_grad is accumulated through a
-contiguous copy; the workspaces (fp32 partial tiles of experts split into row
+Memory: a main_grad that is not contiguous or does not start on 16 bytes is
+accumulated through a copy; the workspaces (fp32 partial tiles of experts split into row
 chunks and of split tail units) are allocated per call from torch's caching
 allocator.  Under ``torch.use_deterministic_algorithms(True)``
 with ``fill_uninitialized_memory`` torch fills the fresh outputs and the
@@ -107,10 +107,10 @@ def _main_grad(w: torch.Tensor, where: str, call: str = "cake_grouped_det_mm") -
 
 def _accumulate_into(main_grad: torch.Tensor, dy, x, offs) -> None:
     E = main_grad.shape[0]
-    if main_grad.is_contiguous():
+    if main_grad.is_contiguous() and main_grad.data_ptr() % 16 == 0:
         ops.grouped_det_gemm_wgrad(dy, x, offs, out=main_grad, accumulate=True)
         return
-    tmp = main_grad.contiguous()
+    tmp = main_grad.clone(memory_format=torch.contiguous_format)
     ops.grouped_det_gemm_wgrad(dy, x, offs, out=tmp, num_groups=E, accumulate=True)
     main_grad.copy_(tmp)
 
