@@ -737,33 +737,36 @@ PyObject* norm_fwd(PyObject* const* a) {
   return got;
 }
 
-// dout, dnormed, out, rstd, post_rstd, y, weight, post_weight, gate, scale, what is wanted (bits)
+// dout, dnormed, out (may be None without a weight), rstd, post_rstd, y, weight, post_weight, gate, scale, what is wanted (bits)
 // -> dresidual, dy, dweight, dpost_weight, dgate
 PyObject* norm_bwd(PyObject* const* a) {
   int code;
-  const Tensor& out = float_tensor(a[2], "norm.out", 2, &code);
-  const Tensor dout = optional_rows(a[0], "dout", out), dnormed = optional_rows(a[1], "dnormed", out);
+  const bool with_out = a[2] != Py_None;
+  const Tensor& like = with_out ? float_tensor(a[2], "norm.out", 2, &code) : float_tensor(a[0], "dout", 2, &code);
+  const Tensor out = with_out ? like : Tensor();
+  const Tensor dout = optional_rows(a[0], "dout", like), dnormed = optional_rows(a[1], "dnormed", like);
   if (!dout.defined() && !dnormed.defined()) refuse(PyExc_ValueError, "dout or dnormed is needed");
-  const Tensor rstd = optional_of_tokens(a[3], "norm.rstd", out), post_rstd = optional_of_tokens(a[4], "norm.post_rstd", out);
-  const Tensor y = optional_rows(a[5], "y", out);
-  const NormWeights w = need_norm_weights(a[6], a[7], out);
-  const Tensor gate = optional_of_tokens(a[8], "gate", out);
+  const Tensor rstd = optional_of_tokens(a[3], "norm.rstd", like), post_rstd = optional_of_tokens(a[4], "norm.post_rstd", like);
+  const Tensor y = optional_rows(a[5], "y", like);
+  const NormWeights w = need_norm_weights(a[6], a[7], like);
+  const Tensor gate = optional_of_tokens(a[8], "gate", like);
   const float scale = real(a[9], "scale");
-  const int64_t need = integer(a[10], "need"), T = out.size(0), H = out.size(1);
+  const int64_t need = integer(a[10], "need"), T = like.size(0), H = like.size(1);
+  if (!with_out && w.weight.defined()) refuse(PyExc_ValueError, "norm.out goes with a weight");
   if (dnormed.defined() && !w.weight.defined()) refuse(PyExc_ValueError, "dnormed goes with a weight");
   if (w.weight.defined() != rstd.defined() || w.post_weight.defined() != post_rstd.defined())
     refuse(PyExc_ValueError, "norm does not belong to these weights");
   if ((w.post_weight.defined() || gate.defined()) && !y.defined()) refuse(PyExc_ValueError, "post_weight and gate go with y");
   const ScalarType wt = w.code == MDG_FP32 ? ScalarType::Float : ScalarType::BFloat16;
   Tensor dr, dy, dw, dp, dg;
-  if (need & 1) dr = fresh(out, {T, H}, out.scalar_type());
-  if (need & 2) dy = fresh(out, {T, H}, out.scalar_type());
-  if (need & 4) dw = fresh(out, {H}, wt);
-  if (need & 8) dp = fresh(out, {H}, wt);
-  if (need & 16) dg = fresh(out, {T}, ScalarType::Float);
+  if (need & 1) dr = fresh(like, {T, H}, like.scalar_type());
+  if (need & 2) dy = fresh(like, {T, H}, like.scalar_type());
+  if (need & 4) dw = fresh(like, {H}, wt);
+  if (need & 8) dp = fresh(like, {H}, wt);
+  if (need & 16) dg = fresh(like, {T}, ScalarType::Float);
   const size_t bytes = (need & 12) ? g.block_norm_bwd_workspace_bytes(T, H) : 0;
-  const Tensor ws = scratch(out, bytes);
-  call("block_norm_bwd", g.block_norm_bwd, out, ptr(dout), ptr(dnormed), ptr(out), ptr(y), ptr(w.weight),
+  const Tensor ws = scratch(like, bytes);
+  call("block_norm_bwd", g.block_norm_bwd, like, ptr(dout), ptr(dnormed), ptr(out), ptr(y), ptr(w.weight),
        ptr(w.post_weight), ptr(gate), ptr(rstd), ptr(post_rstd), ptr(dr), ptr(dy), ptr(dw), ptr(dp), ptr(dg), T, H, code,
        w.code, scale, ptr(ws), bytes);
   return tuple(dr, dy, dw, dp, dg);

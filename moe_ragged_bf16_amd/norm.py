@@ -78,8 +78,8 @@ class _BlockNorm(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         with_z = post_weight is not None or gate is not None
         ctx.with_y, ctx.scale = y is not None, scale
-        # (without a norm or a gate on it, y's gradient does not need y)
-        ctx.save_for_backward(r.out, y if with_z else None, weight, post_weight, gate, r.rstd, r.post_rstd)
+        # (without a norm or a gate on it, y's gradient does not need y, nor any out without a norm of it)
+        ctx.save_for_backward(r.out if weight is not None else None, y if with_z else None, weight, post_weight, gate, r.rstd, r.post_rstd)
         return (r.normed,) if y is None else (r.out, r.normed)
 
     @staticmethod
