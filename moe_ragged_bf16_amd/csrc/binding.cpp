@@ -610,7 +610,8 @@ void zero_rows(const Tensor& t, int64_t E, const int32_t* offs) {
        size32(E));
 }
 
-// x, w, w_down, offs, activation's code, keep -> y (zeros in rows of no group), h, gate_up (None unless kept)
+// x, w, w_down, offs, activation's code, what is kept (1: gate_up, 2: h)
+// -> y (zeros in rows of no group), h, gate_up (None unless kept)
 PyObject* ffn_fwd(PyObject* const* a) {
   const Tensor& x = tensor(a[0], "x", ScalarType::BFloat16, 2);
   const Tensor& w = tensor(a[1], "w_gate_up", ScalarType::BFloat16, 3, &x);
@@ -623,38 +624,47 @@ PyObject* ffn_fwd(PyObject* const* a) {
            shape_name(w.sizes()).c_str(), shape_name(w2.sizes()).c_str());
   const int32_t* offs = need_offs(a[3], E, x);
   const int act = (int)integer(a[4], "activation");
-  const bool keep = boolean(a[5], "keep");
+  const int64_t keep = integer(a[5], "keep");
   Tensor kept;
-  const Tensor h = gated_h(x, w, offs, act, keep, &kept);
+  const Tensor h = gated_h(x, w, offs, act, keep & 1, &kept);
   const Tensor y = det_fwd(h, w2, offs);
   zero_rows(y, E, offs);
-  return keep ? tuple(y, h, kept) : tuple(y, Tensor(), Tensor());
+  return tuple(y, (keep & 2) ? h : Tensor(), kept);
 }
 
-// dy, w_down, gate_up, offs, activation's code, x, w, h, what is wanted (1: dx, 2: dw, 4: dw_down; 8: dgate_up)
-// -> dx (zeros in rows of no group), dw, dw_down, dgate_up
+// dy, w_down, gate_up, offs, activation's code, x, w, h, experts, what is wanted (1: dx, 2: dw, 4: dw_down; 8:
+// dgate_up) -> dx (zeros in rows of no group), dw, dw_down, dgate_up.  What nothing wanted reads may be None: w_down and
+// gate_up but for 1, 2 and 8, w but for 1, x but for 2, h but for 4.
 PyObject* ffn_bwd(PyObject* const* a) {
   const Tensor& dy = tensor(a[0], "the output gradient", ScalarType::BFloat16, 2);
-  const Tensor& w2 = tensor(a[1], "w_down", ScalarType::BFloat16, 3, &dy);
-  const Tensor& gate_up = tensor(a[2], "gate_up", ScalarType::BFloat16, 2, &dy);
-  const Tensor& x = tensor(a[5], "x", ScalarType::BFloat16, 2, &dy);
-  const Tensor& w = tensor(a[6], "w_gate_up", ScalarType::BFloat16, 3, &dy);
-  const Tensor& h = tensor(a[7], "h", ScalarType::BFloat16, 2, &dy);
-  const int64_t M = dy.size(0), E = w2.size(0), F = w2.size(2), want = integer(a[8], "need");
-  need_shape(dy, "the output gradient", {x.size(0), w2.size(1)});
-  need_shape(gate_up, "gate_up", {M, 2 * F});
-  need_shape(h, "h", {M, F});
-  need_shape(w, "w_gate_up", {E, 2 * F, x.size(1)});
+  const int64_t M = dy.size(0), E = integer(a[8], "experts"), want = integer(a[9], "need");
   const int32_t* offs = need_offs(a[3], E, dy);
   const int act = (int)integer(a[4], "activation");
   Tensor d, dx, dw, dw2;
-  if (want & 11) d = gated_d(dy, w2, gate_up, offs, act, Tensor());
+  if (want & 11) {
+    const Tensor& w2 = tensor(a[1], "w_down", ScalarType::BFloat16, 3, &dy);
+    const int64_t F = w2.size(2);
+    need_shape(w2, "w_down", {E, dy.size(1), F});
+    const Tensor& gate_up = tensor(a[2], "gate_up", ScalarType::BFloat16, 2, &dy);
+    need_shape(gate_up, "gate_up", {M, 2 * F});
+    d = gated_d(dy, w2, gate_up, offs, act, Tensor());
+  }
   if (want & 1) {
+    const Tensor& w = tensor(a[6], "w_gate_up", ScalarType::BFloat16, 3, &dy);
+    need_shape(w, "w_gate_up", {E, d.size(1), w.size(2)});
     dx = det_dgrad(d, w, offs);
     zero_rows(dx, E, offs);
   }
-  if (want & 2) dw = det_wgrad(d, x, E, offs);
-  if (want & 4) dw2 = det_wgrad(dy, h, E, offs);
+  if (want & 2) {
+    const Tensor& x = tensor(a[5], "x", ScalarType::BFloat16, 2, &dy);
+    need_rows(x, "x", M);
+    dw = det_wgrad(d, x, E, offs);
+  }
+  if (want & 4) {
+    const Tensor& h = tensor(a[7], "h", ScalarType::BFloat16, 2, &dy);
+    need_rows(h, "h", M);
+    dw2 = det_wgrad(dy, h, E, offs);
+  }
   return tuple(dx, dw, dw2, (want & 8) ? d : Tensor());
 }
 
@@ -903,7 +913,7 @@ PyMethodDef methods[] = {METHOD(setup, 3),         METHOD(entries, 0),        ME
                          METHOD(quantize_rows, 1), METHOD(quantize_weight, 2), METHOD(fp8_gemm_fwd, 7),
                          METHOD(gated_fwd, 7),     METHOD(gated_dgrad, 7),    METHOD(norm_fwd, 7),
                          METHOD(norm_bwd, 11),     METHOD(grad_norm, 1),      METHOD(clip_grads, 4),
-                         METHOD(ffn_fwd, 6),       METHOD(ffn_bwd, 9),
+                         METHOD(ffn_fwd, 6),       METHOD(ffn_bwd, 10),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

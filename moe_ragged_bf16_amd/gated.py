@@ -82,11 +82,13 @@ def grouped_gated_gemm_dgrad(dy: torch.Tensor, w_down: torch.Tensor, gate_up: to
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, w_down, offs, code, fuse, record):
-        keep = record and any(ctx.needs_input_grad[:3])
-        y, h, gate_up = native.ffn_fwd(x, w, w_down, offs, code, keep)
-        if keep:
-            ctx.save_for_backward(x, w, w_down, offs, h, gate_up)
-        ctx.code, ctx.fuse = code, fuse
+        need_x, need_w, need_down = (record and n for n in ctx.needs_input_grad[:3])
+        through = need_x or need_w                     # (the gradients through the down product)
+        y, h, gate_up = native.ffn_fwd(x, w, w_down, offs, code, through + 2 * need_down)
+        if through or need_down:                       # what the wanted gradients read
+            ctx.save_for_backward(x if need_w else None, w if need_x else None, w_down if through else None, offs, h,
+                                  gate_up)
+        ctx.code, ctx.fuse, ctx.experts = code, fuse, w.shape[0]
         # (the caller's weights themselves, whose main_grad the backward reads)
         ctx.w_objs = (w, w_down) if fuse else (None, None)
         return y
@@ -99,14 +101,15 @@ class _GatedFfn(torch.autograd.Function):
         dy = incoming_gradient(dy)
         need_x, need_w, need_down = ctx.needs_input_grad[:3]
         if not ctx.fuse:
-            dx, dw, dw_down, _ = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h,
+            dx, dw, dw_down, _ = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h, ctx.experts,
                                                 need_x + 2 * need_w + 4 * need_down)
             return dx, dw, dw_down, None, None, None, None
         read = (("the output gradient", dy), ("x", x), ("offs", offs), ("w", w), ("w_down", w_down), ("h", h),
                 ("gate_up", gate_up))
+        read = tuple((name, t) for name, t in read if t is not None)
         mgs = [_fused_main_grad(o, "grouped_gated_ffn", read) if need else None
                for o, need in zip(ctx.w_objs, (need_w, need_down))]
-        dx, _, _, d = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h, need_x + 8 * need_w)
+        dx, _, _, d = native.ffn_bwd(dy, w_down, gate_up, offs, ctx.code, x, w, h, ctx.experts, need_x + 8 * need_w)
         dw = _fused_wgrad(ctx.w_objs[0], mgs[0], d, x, offs) if need_w else None
         dw_down = _fused_wgrad(ctx.w_objs[1], mgs[1], dy, h, offs) if need_down else None
         return dx, dw, dw_down, None, None, None, None
