@@ -466,7 +466,8 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
  * rounding hides, and 0 below 2^-126.  A value of a or b that is not finite reaches its own h, da and db only;
  * act(-inf), and act' at either infinity, are NaN.
  * workspace: at least grouped_gated_gemm_{fwd,dgrad}_workspace_bytes() bytes (a function of
- * the sizes; 0 for invalid ones), 256-byte aligned, used until the stream has passed the
+ * the sizes and, as the kernels are chosen by it, the current device's number of compute
+ * units; 0 for invalid sizes), 256-byte aligned, used until the stream has passed the
  * call.  The sums' order is fixed by the sizes and offs: a call repeats bit for bit, and
  * the same row can get different bits in calls of other sizes.  m_rows == 0 enqueues nothing.
  */

@@ -156,6 +156,13 @@ Tensor fresh(const Tensor& like, at::IntArrayRef shape, ScalarType type) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
 
+// A workspace query on t's device (what a call needs can depend on it).
+template <class F, class... A>
+size_t query(const Tensor& t, F entry, A... a) {
+  const c10::DeviceGuard guard(t.device());
+  return entry(a...);
+}
+
 Tensor scratch(const Tensor& like, size_t bytes) {
   return bytes ? fresh(like, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
 }
@@ -523,7 +530,7 @@ Tensor gated_h(const Tensor& x, const Tensor& w, const int32_t* offs, int act, b
   const int64_t M = x.size(0), K = x.size(1), E = w.size(0), F = w.size(1) / 2;
   const Tensor h = need_out(out, x, {M, F});
   if (keep) *kept = fresh(x, {M, 2 * F}, ScalarType::BFloat16);
-  size_t need = g.grouped_gated_gemm_fwd_workspace_bytes(M, F, K, size32(E));
+  size_t need = query(x, g.grouped_gated_gemm_fwd_workspace_bytes, M, F, K, size32(E));
   const Tensor ws = need_workspace(ws_given, &need, x);
   call("grouped_gated_gemm_fwd", g.grouped_gated_gemm_fwd, x, ptr(x), ptr(w), offs, ptr(h), ptr(*kept), act, M, F, K,
        size32(E), ptr(ws), need);
@@ -533,7 +540,7 @@ Tensor gated_d(const Tensor& dy, const Tensor& w, const Tensor& gate_up, const i
                PyObject* ws_given = Py_None) {
   const int64_t M = dy.size(0), N = dy.size(1), E = w.size(0), F = w.size(2);
   if (!out.defined()) out = fresh(dy, {M, 2 * F}, ScalarType::BFloat16);
-  size_t need = g.grouped_gated_gemm_dgrad_workspace_bytes(M, N, F, size32(E));
+  size_t need = query(dy, g.grouped_gated_gemm_dgrad_workspace_bytes, M, N, F, size32(E));
   const Tensor ws = need_workspace(ws_given, &need, dy);
   call("grouped_gated_gemm_dgrad", g.grouped_gated_gemm_dgrad, dy, ptr(dy), ptr(w), ptr(gate_up), offs, ptr(out), act,
        M, N, F, size32(E), ptr(ws), need);

@@ -39,11 +39,6 @@ int64_t units_of(Op op, int64_t m_rows, int64_t f, int32_t num_groups) {
 // fp32 partial tiles of the tail split (as for the plain products).
 int64_t slots_of(int64_t units) { return std::min<int64_t>(units * kMaxSplit, kBalanceSlots); }
 
-size_t workspace_of(Op op, int64_t m_rows, int64_t n, int64_t f, int32_t num_groups) {
-  if (check_sizes(m_rows, n, f, num_groups) != MDG_OK) return 0;
-  return (size_t)kTailHeadBytes + (size_t)slots_of(units_of(op, m_rows, f, num_groups)) * kTileI * kTileJ * sizeof(float);
-}
-
 enum Kernel { kSmall, kMid, kTile };
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -99,6 +94,34 @@ Kernel kernel_of(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, in
   return half_tiles * 4 <= 9 * cus && n <= 1024 ? kMid : kTile;
 }
 
+// A call's kernel and the middle one's launch.
+struct Choice {
+  Kernel which;
+  int tile;       // rows and columns of the middle kernel's tiles
+  int64_t grid;   // its workgroups
+};
+Choice choose(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, int64_t cus) {
+  Choice c{kernel_of(op, m_rows, n, f, active, cus), mid_tile(op, m_rows, f, active, cus), 0};
+  const int64_t cols = op == kFwd ? c.tile / 2 : c.tile, row_tiles = (m_rows + c.tile - 1) / c.tile + active;
+  c.grid = (row_tiles * ((f + cols - 1) / cols) + 7) / 8 * 8;
+  if (c.which == kMid && c.grid * 256 > UINT32_MAX) c.which = kTile;  // (a launch's work-items)
+  return c;
+}
+
+int64_t cus_of(const DeviceInfo& dev) { return dev.cus > 0 ? dev.cus : 256; }
+
+// The plan's head (never 0 for valid sizes), and where the tile kernel takes the call its
+// partial tiles; without a device it could.
+size_t workspace_of(Op op, int64_t m_rows, int64_t n, int64_t f, int32_t num_groups) {
+  if (check_sizes(m_rows, n, f, num_groups) != MDG_OK) return 0;
+  DeviceInfo dev;
+  int device = -1;
+  const int64_t active = std::min<int64_t>(num_groups, m_rows);
+  if (query_device(&dev, &device) == MDG_OK && choose(op, m_rows, n, f, active, cus_of(dev)).which != kTile)
+    return kTailHeadBytes;
+  return (size_t)kTailHeadBytes + (size_t)slots_of(units_of(op, m_rows, f, num_groups)) * kTileI * kTileJ * sizeof(float);
+}
+
 int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, void* workspace, void* stream) {
   DeviceInfo dev;
   int device = -1;
@@ -106,17 +129,13 @@ int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, vo
   if (st != MDG_OK) return st;
   if (!dev.gfx950) return MDG_EUNSUPPORTED;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t cus = dev.cus > 0 ? dev.cus : 256, active = std::min<int64_t>(num_groups, m_rows);
-  Kernel which = kernel_of(op, m_rows, op == kFwd ? p->g.k : p->g.n, f, active, cus);
-  const int tile = mid_tile(op, m_rows, f, active, cus);
-  const int64_t cols = op == kFwd ? tile / 2 : tile, row_tiles = (m_rows + tile - 1) / tile + active;
-  const int64_t mid = (row_tiles * ((f + cols - 1) / cols) + 7) / 8 * 8;
-  if (which == kMid && mid * 256 > UINT32_MAX) which = kTile;  // (a launch's work-items)
+  const int64_t cus = cus_of(dev), active = std::min<int64_t>(num_groups, m_rows);
+  const Choice c = choose(op, m_rows, op == kFwd ? p->g.k : p->g.n, f, active, cus);
   hipError_t err = hipSuccess;
-  if (which == kSmall) {
+  if (c.which == kSmall) {
     err = launch_gated_small(*p, (int)(active + m_rows / kGatedSmallRows), s);
-  } else if (which == kMid) {
-    err = launch_gated_mid(op, *p, tile, (int)mid, s);
+  } else if (c.which == kMid) {
+    err = launch_gated_mid(op, *p, c.tile, (int)c.grid, s);
   } else {
     const int64_t units = units_of(op, m_rows, f, num_groups), slots = slots_of(units);
     char* ws = static_cast<char*>(workspace);

@@ -48,10 +48,12 @@ def _code(activation: str) -> int:
 
 
 def gated_gemm_fwd_workspace_bytes(m_rows: int, f: int, k: int, num_groups: int) -> int:
+    """Bytes of workspace of ``grouped_gated_gemm_fwd`` on the current device."""
     return int(_capi.load_library().grouped_gated_gemm_fwd_workspace_bytes(m_rows, f, k, num_groups))
 
 
 def gated_gemm_dgrad_workspace_bytes(m_rows: int, n: int, f: int, num_groups: int) -> int:
+    """Bytes of workspace of ``grouped_gated_gemm_dgrad`` on the current device."""
     return int(_capi.load_library().grouped_gated_gemm_dgrad_workspace_bytes(m_rows, n, f, num_groups))
 
 
