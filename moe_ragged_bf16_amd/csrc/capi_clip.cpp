@@ -179,6 +179,18 @@ MDG_API mdg_status grad_clip(const mdg_gradient* gradients, int64_t count, float
   double* partial = static_cast<double*>(workspace);
   int32_t partials = 0;
   if (!norm_in && (st = enqueue_norm(gradients, count, partial, s, &partials)) != MDG_OK) return status(st);
+  // More sums than a scaling workgroup's threads load at once are added up once, by a launch
+  // of its own: added up by every workgroup of every launch their cost grows with the list's square
+  // (each workgroup / once, in us, captured: 400 tensors of 60000 fp32 values, 1536 sums, 78 / 78, 1000 of them 159 / 150, 5000
+  // 1092 / 896; 65536 of 20000 41500 / 4940).
+  const bool finished = partials > kClipPartials;
+  if (finished) {
+    ClipTable t{};
+    t.partial = partial;
+    t.partials = partials;
+    if (launch_clip_finish(t, s) != hipSuccess) return status(MDG_EHIP);
+    partials = 0;
+  }
   bool apart = false;
   for (int64_t i = 0; i < count; ++i) apart = apart || (gradients[i].elements > 0 && gradients[i].out != gradients[i].data);
   const int64_t launches = std::max<int64_t>(1, launches_of(count, apart));  // (without tensors: the norm, 0)
@@ -187,6 +199,7 @@ MDG_API mdg_status grad_clip(const mdg_gradient* gradients, int64_t count, float
     if (norm_in && t.count == 0) return status(MDG_OK);
     t.partial = partial;
     t.partials = partials;
+    t.finished = finished;
     t.norm_in = norm_in;
     t.norm_out = k == 0 ? norm : nullptr;
     t.max_norm = max_norm;

@@ -10,6 +10,7 @@ namespace mdg {
 constexpr int kClipWords = 1008;        // 32-bit ones of the table in a launch's arguments (4 KiB in all)
 constexpr int kClipUnitBytes = 32768;   // bytes of a tensor that a workgroup takes at a time
 constexpr int kClipBlocks = 1024;       // workgroups of a launch, at most
+constexpr int kClipPartials = 1024;     // partial sums that every scaling workgroup adds up itself, at most
 
 // Words of a tensor: its address's low half, 22 bits above them (16 of the address, 6 of the
 // size), the size's low half, and where outputs are apart the output's address in two.  (An address
@@ -26,9 +27,10 @@ struct ClipTable {
   int32_t first;                        // partial sums of the launches before it
   int32_t partials;                     // of all launches
   float max_norm, eps;
+  int32_t finished;                     // scaling: partial[0] is the norm itself
   double* partial;                      // [partials]
   const float* norm_in;                 // scaling: the norm, or nullptr: from the partial sums
-  float* norm_out;                      // scaling and finishing: where the norm goes, or nullptr
+  float* norm_out;                      // scaling and finishing: where the norm goes, or nullptr (finishing: to partial[0])
 };
 static_assert(sizeof(ClipTable) <= 4096, "kernel arguments");
 

@@ -43,6 +43,7 @@ struct ClipLds {
   int scratch[4];
 };
 static_assert(clip_tensors(false) <= 2 * kClipThreads, "two tensors to a thread");
+static_assert(kClipPartials == 4 * kClipThreads, "four partial sums to a thread");
 
 // Fills it; returns the number of units.
 __device__ __forceinline__ int clip_units(const ClipTable& t, ClipLds& s) {
@@ -161,7 +162,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(ClipTable t) {
   if (threadIdx.x == 0) t.partial[t.first + blockIdx.x] = s;
 }
 
-// This thread's share of the launches' partial sums, its first loads apart from their use.
+// This thread's share of the launches' partial sums, its first loads apart from their use;
+// ALL: any number of them, otherwise up to kClipPartials.
 struct Partials {
   double first[4];
   __device__ __forceinline__ void load(const ClipTable& t) {
@@ -171,9 +173,11 @@ struct Partials {
       first[i] = at < t.partials ? t.partial[at] : 0.0;
     }
   }
+  template <bool ALL>
   __device__ __forceinline__ double sum(const ClipTable& t) const {
     double s = (first[0] + first[1]) + (first[2] + first[3]);
-    for (int i = threadIdx.x + 4 * kClipThreads; i < t.partials; i += kClipThreads) s += t.partial[i];
+    if constexpr (ALL)
+      for (int i = threadIdx.x + kClipPartials; i < t.partials; i += kClipThreads) s += t.partial[i];
     return s;
   }
 };
@@ -182,8 +186,10 @@ __global__ __launch_bounds__(kClipThreads) void clip_finish_kernel(ClipTable t) 
   __shared__ double s_sum[4];
   Partials mine;
   mine.load(t);
-  const double norm = sqrt(block_sum(mine.sum(t), s_sum));
-  if (threadIdx.x == 0) *t.norm_out = (float)norm;
+  const double norm = sqrt(block_sum(mine.sum<true>(t), s_sum));
+  if (threadIdx.x != 0) return;
+  if (t.norm_out) *t.norm_out = (float)norm;
+  else t.partial[0] = norm;  // (every thread has its sums: a barrier lies between)
 }
 
 // Walks the units from the last one back: what the norm kernel read last is what the
@@ -193,7 +199,7 @@ __global__ __launch_bounds__(kClipThreads, 6) void clip_scale_kernel(ClipTable t
   __shared__ ClipLds s_table;
   __shared__ double s_sum[4];
   Partials mine;
-  mine.load(t);  // (none with a norm given)
+  mine.load(t);  // (none with a norm given or finished)
   const int total = clip_units(t, s_table);
   int u = total - 1 - (int)blockIdx.x;
   ClipUnit x{};
@@ -202,7 +208,9 @@ __global__ __launch_bounds__(kClipThreads, 6) void clip_scale_kernel(ClipTable t
     x = clip_unit(t, s_table, u);
     load_unit(v, x.src, x.bytes);
   }
-  const double norm = t.norm_in ? (double)*t.norm_in : sqrt(block_sum(mine.sum(t), s_sum));
+  const double norm = t.norm_in    ? (double)*t.norm_in
+                      : t.finished ? t.partial[0]
+                                   : sqrt(block_sum(mine.sum<false>(t), s_sum));
   if (t.norm_out && blockIdx.x == 0 && threadIdx.x == 0) *t.norm_out = (float)norm;
   // a norm that is not finite leaves the gradients as they are
   const bool finite = fabsf((float)norm) < __builtin_inff();
