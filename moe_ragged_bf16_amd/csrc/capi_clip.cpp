@@ -24,14 +24,6 @@ int64_t units_of(const mdg_gradient& g) { return (bytes_of(g) + kClipUnitBytes -
 int64_t launches_of(int64_t count, bool apart) { return (count + clip_tensors(apart) - 1) / clip_tensors(apart); }
 size_t workspace_of(int64_t count) { return (size_t)launches_of(count, false) * kClipBlocks * sizeof(double); }
 
-int check_device() {
-  DeviceInfo dev;
-  int device = -1;
-  const int st = query_device(&dev, &device);
-  if (st != MDG_OK) return st;
-  return dev.gfx950 ? MDG_OK : MDG_EUNSUPPORTED;
-}
-
 // (an address of more than 48 bits is none of the device's)
 bool on_element(const void* p, int dtype) {
   return reinterpret_cast<uintptr_t>(p) % (dtype == MDG_FP32 ? 4 : 2) == 0 && reinterpret_cast<uintptr_t>(p) >> 48 == 0;
@@ -117,12 +109,6 @@ int enqueue_norm(const mdg_gradient* g, int64_t count, double* partial, hipStrea
   }
   *partials = first;
   return MDG_OK;
-}
-
-int check_workspace(const void* workspace, size_t bytes, size_t need) {
-  if (need == 0) return MDG_OK;
-  if (!workspace || bytes < need) return MDG_EWORKSPACE;
-  return (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 ? MDG_OK : MDG_EINVAL;
 }
 
 }  // namespace

@@ -21,13 +21,6 @@ int64_t rows_scale_bytes(int64_t m_rows, int64_t k) { return (blocks_of(k) + 3) 
 bool real_dtype(int dtype) { return dtype == MDG_BF16 || dtype == MDG_FP32; }
 int64_t dtype_bytes(int dtype) { return dtype == MDG_E4M3 ? 1 : dtype == MDG_FP32 ? 4 : 2; }
 
-int check_device(DeviceInfo* dev) {
-  int device = -1;
-  const int st = query_device(dev, &device);
-  if (st != MDG_OK) return st;
-  return dev->gfx950 ? MDG_OK : MDG_EUNSUPPORTED;
-}
-
 int check_rows(int64_t m_rows, int64_t k) {
   if (m_rows < 0 || k <= 0) return MDG_EINVAL;
   if (k % kKAlign != 0 || k > (1 << 20) || m_rows > kMaxRows) return MDG_EUNSUPPORTED;
@@ -145,10 +138,7 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
   if (!aligned16(x) || !aligned4(x_scale) || !aligned16(w) || !aligned4(offs) || !aligned16(y))
     return status(MDG_EINVAL);
   const XSpace xs = x_space(m_rows, k, x_dtype);
-  if (xs.total > 0) {
-    if (!workspace || workspace_bytes < xs.total) return status(MDG_EWORKSPACE);
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return status(MDG_EINVAL);
-  }
+  if ((st = check_workspace(workspace, workspace_bytes, xs.total)) != MDG_OK) return status(st);
   const Range in[5] = {range_of(x, m_rows * (quantized ? fp8_pitch(k) : k) * dtype_bytes(x_dtype)),
                        range_of(x_scale, quantized ? rows_scale_bytes(m_rows, k) : 0),
                        range_of(w, num_groups * n * fp8_pitch(k)),

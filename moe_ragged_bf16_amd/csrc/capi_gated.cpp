@@ -115,19 +115,16 @@ int64_t cus_of(const DeviceInfo& dev) { return dev.cus > 0 ? dev.cus : 256; }
 size_t workspace_of(Op op, int64_t m_rows, int64_t n, int64_t f, int32_t num_groups) {
   if (check_sizes(m_rows, n, f, num_groups) != MDG_OK) return 0;
   DeviceInfo dev;
-  int device = -1;
   const int64_t active = std::min<int64_t>(num_groups, m_rows);
-  if (query_device(&dev, &device) == MDG_OK && choose(op, m_rows, n, f, active, cus_of(dev)).which != kTile)
+  if (check_device(&dev) == MDG_OK && choose(op, m_rows, n, f, active, cus_of(dev)).which != kTile)
     return kTailHeadBytes;
   return (size_t)kTailHeadBytes + (size_t)slots_of(units_of(op, m_rows, f, num_groups)) * kTileI * kTileJ * sizeof(float);
 }
 
 int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, void* workspace, void* stream) {
   DeviceInfo dev;
-  int device = -1;
-  const int st = query_device(&dev, &device);
+  const int st = check_device(&dev);
   if (st != MDG_OK) return st;
-  if (!dev.gfx950) return MDG_EUNSUPPORTED;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t cus = cus_of(dev), active = std::min<int64_t>(num_groups, m_rows);
   const Choice c = choose(op, m_rows, op == kFwd ? p->g.k : p->g.n, f, active, cus);
@@ -149,11 +146,6 @@ int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, vo
       err = launch_gated_reduce(op, *p, 8, (int)std::min<int64_t>(kBalanceSlots / 2, slots / 2), s);
   }
   return err == hipSuccess ? MDG_OK : MDG_EHIP;
-}
-
-int check_workspace(const void* workspace, size_t bytes, size_t need) {
-  if (!workspace || bytes < need) return MDG_EWORKSPACE;
-  return (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 ? MDG_OK : MDG_EINVAL;
 }
 
 }  // namespace

@@ -30,14 +30,6 @@ bool outputs_apart(std::initializer_list<Range> outs, std::initializer_list<Rang
 
 bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-int check_device() {
-  DeviceInfo dev;
-  int device = -1;
-  const int st = query_device(&dev, &device);
-  if (st != MDG_OK) return st;
-  return dev.gfx950 ? MDG_OK : MDG_EUNSUPPORTED;
-}
-
 int check_dtype(int dtype) { return dtype == MDG_BF16 || dtype == MDG_FP32 ? MDG_OK : MDG_EINVAL; }
 int64_t dtype_bytes(int dtype) { return dtype == MDG_FP32 ? 4 : 2; }
 
@@ -100,12 +92,6 @@ int plan_blocks(int64_t slots) {
 size_t plan_workspace(int64_t slots, int32_t experts) {
   const int b = plan_blocks(slots);
   return b == 1 ? 0 : align256((size_t)b * experts * 4);
-}
-
-int check_workspace(const void* ws, size_t bytes, size_t need) {
-  if (need == 0) return MDG_OK;
-  if (!ws || bytes < need) return MDG_EWORKSPACE;
-  return aligned_to(ws, 256) ? MDG_OK : MDG_EINVAL;
 }
 
 // Sizes and types shared by the calls that move rows.

@@ -25,13 +25,6 @@ int check_sizes(int64_t tokens, int64_t hidden) {
   return MDG_OK;
 }
 
-int check_device(DeviceInfo* dev) {
-  int device = -1;
-  const int st = query_device(dev, &device);
-  if (st != MDG_OK) return st;
-  return dev->gfx950 ? MDG_OK : MDG_EUNSUPPORTED;
-}
-
 // Every output apart from every input and from every other output.
 template <size_t O, size_t I>
 bool apart(const Range (&outs)[O], const Range (&ins)[I]) {
@@ -138,10 +131,7 @@ MDG_API mdg_status block_norm_bwd(const void* dout, const void* dnormed, const v
     return status(MDG_EINVAL);
   const bool sums = dweight || dpost_weight;
   const size_t need = sums ? part_bytes(tokens, hidden) : 0;
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return status(MDG_EWORKSPACE);
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return status(MDG_EINVAL);
-  }
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != MDG_OK) return status(st);
   const int64_t rows = tokens * hidden * dtype_bytes(dtype), row = hidden * dtype_bytes(weight_dtype);
   const Range ins[9] = {optional(dout, rows),       optional(dnormed, rows),    optional(out, rows),
                         optional(y, rows),          optional(weight, row),      optional(post_weight, row),

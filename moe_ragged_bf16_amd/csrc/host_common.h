@@ -37,6 +37,16 @@ inline int query_device(DeviceInfo* out, int* device) {
   return MDG_OK;
 }
 
+// The current device is one the kernels run on; *dev (where given) its properties.
+inline int check_device(DeviceInfo* dev = nullptr) {
+  DeviceInfo own;
+  int device = -1;
+  if (!dev) dev = &own;
+  const int st = query_device(dev, &device);
+  if (st != MDG_OK) return st;
+  return dev->gfx950 ? MDG_OK : MDG_EUNSUPPORTED;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -52,6 +62,13 @@ inline Range range_of(const void* p, int64_t bytes) {
 inline bool overlaps(Range a, Range b) {
   if (a.hi == a.lo || b.hi == b.lo) return false;
   return a.lo < b.hi && b.lo < a.hi;
+}
+
+// A workspace of at least `need` bytes on 256 (any where none is needed).
+inline int check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return MDG_OK;
+  if (!workspace || bytes < need) return MDG_EWORKSPACE;
+  return (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 ? MDG_OK : MDG_EINVAL;
 }
 
 inline mdg_status status(int st) { return static_cast<mdg_status>(st); }
