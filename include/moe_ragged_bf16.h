@@ -460,7 +460,8 @@ MDG_API mdg_status grouped_fp8_gemm_fwd(const void* x, int x_dtype, const void* 
  *            rest of the block's backward pass is the products': dx = dgrad(dgate_up, w),
  *            dw = wgrad(dgate_up, x), dw_down = wgrad(dy, h).
  *
- * k, f and n are multiples of 8, 2 f <= 2^20, 2 f k and 2 f n < 2^31; 1 <= num_groups <= 1024.
+ * k, f and n are multiples of 8, 2 f <= 2^20, 2 f k and 2 f n < 2^31; 1 <= num_groups <= 1024; m_rows
+ * up to 4,000,000.
  * Rows at or past the last group's end are left as they are, and malformed offs are read
  * as for the products.  s is off by at most 2^-23 (|q| + 3) of its value, which bf16's
  * rounding hides, and 0 below 2^-126.  A value of a or b that is not finite reaches its own h, da and db only;
@@ -506,7 +507,7 @@ MDG_API mdg_status grouped_gated_gemm_dgrad(const void* dy, const void* w_down, 
  * workspace: block_norm_bwd_workspace_bytes() bytes, 256-byte aligned, where dweight or
  * dpost_weight is wanted.  tokens == 0: both are zeros, nothing else is enqueued.
  *
- * hidden is a multiple of 8 up to 16384.  Rows, weights and their gradients are 16-byte
+ * hidden is a multiple of 8 up to 16384; tokens up to 4,000,000.  Rows, weights and their gradients are 16-byte
  * aligned.  Sums are in fp32 in an order fixed by the sizes; a row whose squares overflow
  * fp32 is divided by infinity.
  */

@@ -46,8 +46,8 @@ Range optional(const void* p, int64_t bytes) { return range_of(p, p ? bytes : 0)
 // of 2048: 4096 of them 30.5 / 27.4, 1024 15.4 / 19.0).
 int64_t bwd_blocks(int64_t tokens, int64_t hidden, int dtype) {
   const int rows = norm_rows_per_block((int)hidden);
-  const bool more = dtype == MDG_BF16 && norm_waves((int)hidden) == 2 && tokens >= 8 * kNormMaxBlocks;
-  return std::min<int64_t>((tokens + rows - 1) / rows, more ? 2 * kNormMaxBlocks : kNormMaxBlocks);
+  const bool more = dtype == MDG_BF16 && norm_waves((int)hidden) == 2 && tokens >= 8 * kNormBlocks;
+  return std::min<int64_t>((tokens + rows - 1) / rows, more ? kNormManyBlocks : kNormBlocks);
 }
 
 size_t part_bytes(int64_t tokens, int64_t hidden) {  // (bf16 has the most)

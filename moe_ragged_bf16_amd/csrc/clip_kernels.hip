@@ -9,8 +9,8 @@
 // vanishes there, and the fp64 units keep up with memory many times over.  Without
 // atomics: results are bitwise reproducible.
 //
-// Memory bounds both kernels: two fp32 tensors of 302 million values each (2.4 GB read twice,
-// written once) take 422 us for the norm (5.7 TB/s) and 907 to scale (5.3 TB/s read and
+// Memory bounds both kernels: 604 million fp32 values in two tensors (403 and 201 million; 2.4 GB
+// read twice, written once) take 422 us for the norm (5.7 TB/s) and 907 to scale (5.3 TB/s read and
 // written); 301 tensors of 60 million values in all 133 (139 in two launches of each).  Nine tensors of
 // 0.3 million take 10.8: two launches, one waiting for the other's sums, 4.8 and 7.0.
 

@@ -8,7 +8,9 @@
 namespace mdg {
 
 constexpr int kNormMaxHidden = 16384;
-constexpr int kNormMaxBlocks = 512;  // blocks of a gradient call that leave partial sums (bwd_blocks of capi_norm.cpp)
+// Blocks of a gradient call, each of which leaves a row of partial sums: up to the first
+// number, or for long calls of some widths up to the second (bwd_blocks of capi_norm.cpp).
+constexpr int kNormBlocks = 512, kNormManyBlocks = 1024;
 
 struct NormParams {
   const void* residual;     // [tokens, hidden]

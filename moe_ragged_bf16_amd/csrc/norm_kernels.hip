@@ -196,7 +196,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void norm_fwd_kernel
 // waves fit a CU (327 us with one block of 8).
 // kLean: fp32 rows of 16 waves, which have 128 registers a lane: rows of dout and y and
 // the weights are read again, from the caches, where they are used (held as for narrower
-// rows 72 registers spilled: 4096 rows of 16384 835 us, here 393).
+// rows 72 registers spilled: 4096 rows of 16384 835 us, here 385).
 template <int WAVES, bool FP32>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES, FP32 || WAVES == 1 ? 1 : 4) void norm_bwd_kernel(NormBwdParams p) {
   constexpr int kRows = WAVES == 1 ? 4 : 1, kLanes = 64 * WAVES;

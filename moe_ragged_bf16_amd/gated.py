@@ -61,7 +61,8 @@ def grouped_gated_gemm_fwd(x: torch.Tensor, w: torch.Tensor, offs: torch.Tensor,
                            keep: bool = False, out: Optional[torch.Tensor] = None,
                            workspace: Optional[torch.Tensor] = None) -> GatedRows:
     """h [M, F] = act(X W_gate[e]^T) * (X W_up[e]^T) of each group's rows, bf16 x
-    [M, K] and w [E, 2 F, K] (gate rows, then up rows; F and K multiples of 8).
+    [M, K] and w [E, 2 F, K] (gate rows, then up rows; F and K multiples of 8; up to
+    4,000,000 rows and 1024 experts).
     ``keep``: also gate_up [M, 2 F], both projections in bf16, for
     ``grouped_gated_gemm_dgrad``; h has the same bits either way.  offs as in
     ``grouped_det_gemm_fwd``; rows past offs[E-1] are not written.  ``out``: h's
@@ -133,8 +134,10 @@ def grouped_gated_ffn(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
 
     The weights' gradients are in the weights' type, or, with
     ``fuse_wgrad_accumulation``, added into both weights' ``main_grad`` by the
-    wgrad kernel's epilogue, by the rules of ``cake_grouped_det_mm``.  There is
-    no double backward."""
+    wgrad kernel's epilogue, by the rules of ``cake_grouped_det_mm``.  A call
+    keeps what the gradients of the tensors that require one will read (w_down's h;
+    x's and w_gate_up's gate_up and w_down; x's w_gate_up, w_gate_up's x), nothing
+    without grad mode.  There is no double backward."""
     refuse_tracing("grouped_gated_ffn")
     if torch.compiler.is_compiling():
         raise NotImplementedError("grouped_gated_ffn cannot be compiled by torch.compile")

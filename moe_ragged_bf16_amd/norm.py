@@ -45,7 +45,7 @@ def block_norm_fwd(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
                    weight: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
                    gate: Optional[torch.Tensor] = None, scale: float = 1.0, eps: float = 1e-6) -> BlockNorm:
     """out and normed (above) of residual and y [tokens, hidden], both bf16 or
-    both fp32; hidden a multiple of 8, up to 16384.  weight and post_weight
+    both fp32; hidden a multiple of 8, up to 16384, and up to 4,000,000 tokens.  weight and post_weight
     [hidden] are both bf16 or both fp32, in either type; gate [tokens] is fp32.
     Without y there is only the norm of the residual, which needs a weight."""
     refuse_tracing("block_norm_fwd")
@@ -100,6 +100,7 @@ def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *, weig
                eps: float = 1e-6) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(out, normed) of ``block_norm_fwd``, differentiable in residual, y, weight,
     post_weight and gate; normed is None without a weight, and out is the
-    residual itself without y."""
+    residual itself without y.  Kept for the gradient: out with a weight, y with a
+    post_weight or a gate, and those."""
     got = _BlockNorm.apply(residual, y, weight, post_weight, gate, scale, eps)
     return (residual, got[0]) if y is None else got
