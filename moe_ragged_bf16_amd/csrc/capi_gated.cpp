@@ -98,43 +98,43 @@ Kernel kernel_of(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, in
   return half_tiles * 4 <= 9 * cus && n <= 1024 ? kMid : kTile;
 }
 
-// A call's kernel and the middle one's launch.
-struct Choice {
+// What a call of valid sizes comes to on the current device.
+struct Call {
+  int device;           // a status: whether it can run there
+  int64_t cus, active;  // active: groups that can have rows
   Kernel which;
-  int tile;       // rows and columns of the middle kernel's tiles
-  int64_t grid;   // its workgroups
+  int tile;             // rows and columns of the middle kernel's tiles
+  int64_t grid;         // and its workgroups
+  size_t workspace;     // the plan's head (never 0), and the tile kernel's partial tiles where it takes the call
 };
-Choice choose(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, int64_t cus) {
-  Choice c{kernel_of(op, m_rows, n, f, active, cus), mid_tile(op, m_rows, f, active, cus), 0};
-  const int64_t cols = op == kFwd ? c.tile / 2 : c.tile, row_tiles = (m_rows + c.tile - 1) / c.tile + active;
-  c.grid = (row_tiles * ((f + cols - 1) / cols) + 7) / 8 * 8;
+Call call_of(Op op, int64_t m_rows, int64_t n, int64_t f, int32_t num_groups) {
+  DeviceInfo dev;
+  Call c{};
+  c.device = check_device(&dev);
+  c.cus = dev.cus > 0 ? dev.cus : 256;
+  c.active = std::min<int64_t>(num_groups, m_rows);
+  c.which = kernel_of(op, m_rows, n, f, c.active, c.cus);
+  c.tile = mid_tile(op, m_rows, f, c.active, c.cus);
+  const int64_t row_tiles = (m_rows + c.tile - 1) / c.tile + c.active;
+  c.grid = up(row_tiles * up(f, op == kFwd ? c.tile / 2 : c.tile), 8) * 8;
   if (c.which == kMid && c.grid * 256 > UINT32_MAX) c.which = kTile;  // (a launch's work-items)
+  c.workspace = kTailHeadBytes;
+  if (c.which == kTile || c.device != MDG_OK)  // (without a device any kernel could take it)
+    c.workspace += (size_t)slots_of(units_of(op, m_rows, f, num_groups)) * kTileI * kTileJ * sizeof(float);
   return c;
 }
 
-int64_t cus_of(const DeviceInfo& dev) { return dev.cus > 0 ? dev.cus : 256; }
-
-// The plan's head (never 0 for valid sizes), and where the tile kernel takes the call its
-// partial tiles; without a device it could.
 size_t workspace_of(Op op, int64_t m_rows, int64_t n, int64_t f, int32_t num_groups) {
-  if (check_sizes(m_rows, n, f, num_groups) != MDG_OK) return 0;
-  DeviceInfo dev;
-  const int64_t active = std::min<int64_t>(num_groups, m_rows);
-  if (check_device(&dev) == MDG_OK && choose(op, m_rows, n, f, active, cus_of(dev)).which != kTile)
-    return kTailHeadBytes;
-  return (size_t)kTailHeadBytes + (size_t)slots_of(units_of(op, m_rows, f, num_groups)) * kTileI * kTileJ * sizeof(float);
+  return check_sizes(m_rows, n, f, num_groups) == MDG_OK ? call_of(op, m_rows, n, f, num_groups).workspace : 0;
 }
 
-int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, void* workspace, void* stream) {
-  DeviceInfo dev;
-  const int st = check_device(&dev);
-  if (st != MDG_OK) return st;
+int run(Op op, const Call& c, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, void* workspace,
+        void* stream) {
+  if (c.device != MDG_OK) return c.device;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t cus = cus_of(dev), active = std::min<int64_t>(num_groups, m_rows);
-  const Choice c = choose(op, m_rows, op == kFwd ? p->g.k : p->g.n, f, active, cus);
   hipError_t err = hipSuccess;
   if (c.which == kSmall) {
-    err = launch_gated_small(*p, (int)(active + m_rows / kGatedSmallRows), s);
+    err = launch_gated_small(*p, (int)(c.active + m_rows / kGatedSmallRows), s);
   } else if (c.which == kMid) {
     err = launch_gated_mid(op, *p, c.tile, (int)c.grid, s);
   } else {
@@ -143,7 +143,7 @@ int run(Op op, GatedParams* p, int64_t m_rows, int64_t f, int32_t num_groups, vo
     p->g.tail_head = reinterpret_cast<int32_t*>(ws);
     p->g.partial = reinterpret_cast<float*>(ws + kTailHeadBytes);
     p->g.tail_slots = (int32_t)slots;
-    int64_t grid = std::min<int64_t>(units + slots, cus);
+    int64_t grid = std::min<int64_t>(units + slots, c.cus);
     if (grid >= 8) grid -= grid % 8;
     err = launch_gated(op, *p, (int)grid, s);
     if (err == hipSuccess && slots >= 2)
@@ -176,7 +176,8 @@ MDG_API mdg_status grouped_gated_gemm_fwd(const void* x, const void* w, const in
   if (!activation(activation_code, &p)) return status(MDG_EINVAL);
   if (!w || !offs || (m_rows > 0 && (!x || !h))) return status(MDG_EINVAL);
   if (!aligned16(x) || !aligned16(w) || !aligned4(offs) || !aligned16(h) || !aligned16(gate_up)) return status(MDG_EINVAL);
-  const size_t need = workspace_of(kFwd, m_rows, k, f, num_groups);
+  const Call c = call_of(kFwd, m_rows, k, f, num_groups);
+  const size_t need = c.workspace;
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MDG_OK) return status(st);
   const Range in[3] = {range_of(x, m_rows * k * 2), range_of(w, (int64_t)num_groups * 2 * f * k * 2),
                        range_of(offs, (int64_t)num_groups * 4)};
@@ -199,7 +200,7 @@ MDG_API mdg_status grouped_gated_gemm_fwd(const void* x, const void* w, const in
   p.g.num_groups = num_groups;
   p.keep = static_cast<uint16_t*>(gate_up);
   p.f = (int32_t)f;
-  return status(run(kFwd, &p, m_rows, f, num_groups, workspace, stream));
+  return status(run(kFwd, c, &p, m_rows, f, num_groups, workspace, stream));
 }
 
 MDG_API mdg_status grouped_gated_gemm_dgrad(const void* dy, const void* w_down, const void* gate_up,
@@ -213,7 +214,8 @@ MDG_API mdg_status grouped_gated_gemm_dgrad(const void* dy, const void* w_down, 
   if (!w_down || !offs || (m_rows > 0 && (!dy || !gate_up || !dgate_up))) return status(MDG_EINVAL);
   if (!aligned16(dy) || !aligned16(w_down) || !aligned16(gate_up) || !aligned4(offs) || !aligned16(dgate_up))
     return status(MDG_EINVAL);
-  const size_t need = workspace_of(kDgrad, m_rows, n, f, num_groups);
+  const Call c = call_of(kDgrad, m_rows, n, f, num_groups);
+  const size_t need = c.workspace;
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MDG_OK) return status(st);
   const Range in[4] = {range_of(dy, m_rows * n * 2), range_of(w_down, (int64_t)num_groups * n * f * 2),
                        range_of(gate_up, m_rows * f * 4), range_of(offs, (int64_t)num_groups * 4)};
@@ -232,7 +234,7 @@ MDG_API mdg_status grouped_gated_gemm_dgrad(const void* dy, const void* w_down, 
   p.g.num_groups = num_groups;
   p.gate_up = static_cast<const uint16_t*>(gate_up);
   p.f = (int32_t)f;
-  return status(run(kDgrad, &p, m_rows, f, num_groups, workspace, stream));
+  return status(run(kDgrad, c, &p, m_rows, f, num_groups, workspace, stream));
 }
 
 }  // extern "C"
