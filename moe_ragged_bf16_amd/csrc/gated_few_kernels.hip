@@ -192,14 +192,19 @@ __global__ __launch_bounds__(256, 3) void gated_small_kernel(GatedParams gp) {
 // Tiles of 128 rows x 128 columns (fwd: 64 hidden columns, gate and up in turns of 16;
 // dgrad: 128 hidden columns), four waves of 64 x 64, stages of 64 reductions (16 KiB an
 // operand), two buffers, two workgroups to a CU, one of which computes while the other
-// waits; and 64 x 64 (32 x 32 a wave) where those leave CUs idle (mid_tile of capi_gated.cpp): a
-// workgroup reads, waits and multiplies in turn, so a smaller tile's stages are shorter (one
-// group of 100 rows of 2 x 2048 x 2048 12.6 us, 20 in tiles of 128, also with four buffers in place of two).
-// With tiles enough, what a CU takes in bounds it, 34 to 45 GB/s with all of them at it: 64 groups of
-// 128 rows on average of 2 x 1536 x 2048 take 200 us, 12 TB/s into LDS; rows that do not
-// start on cache lines (k no multiple of 64) ask for two lines where one would do, 16
-// groups of 188 rows on average of 2 x 1000 x 2000 62 us, of 2 x 1024 x 2048 47.  With few rows
-// the weights' bytes do: 488 rows over 64 groups of 2 x 1536 x 2048 139 us, 5.7 TB/s.
+// waits (with 256 tiles, as dgrad has for 3001 rows over 16 groups of 2000 x 1000, a CU has
+// one, and nothing runs beside its loads: 47 to 60 % of its wave cycles are waits for them and
+// for barriers); and 64 x 64 (32 x 32 a wave) where those leave CUs idle (mid_tile of
+// capi_gated.cpp): a workgroup reads, waits and multiplies in turn, so a smaller tile's
+// stages are shorter (one group of 100 rows of 2 x 2048 x 2048 12.6 us, 20 in tiles of 128,
+// also with four buffers in place of two).
+// With tiles enough, what a CU takes in bounds it, 34 to 45 GB/s with all of them at it: 64
+// groups of 128 rows on average of 2 x 1536 x 2048 take 200 us, 12 TB/s into LDS; rows that
+// do not start on cache lines (k no multiple of 64) ask for two lines where one would do, and
+// loads issue no faster than the L1 works those off (1.69 times the lines from L2; 57 % of the
+// wave cycles wait to issue an instruction, 47 % on cache lines): 16 groups of 188 rows on
+// average of 2 x 1000 x 2000 62 us, of 2 x 1024 x 2048 47.  With few rows the weights' bytes
+// do: 488 rows over 64 groups of 2 x 1536 x 2048 139 us, 5.7 TB/s.
 // (Tried and not kept: weights straight to registers and four buffers of rows, 192 KiB on
 // their way to a CU, 0 to 12 % longer; 256 rows and eight waves, a quarter fewer bytes but
 // one workgroup to a CU, 20 to 40 % longer; two stages' loads and fragments at a time, so that
