@@ -1,5 +1,6 @@
 """What the differentiable gated feed-forward computes and keeps for its gradient: what
 the wanted gradients read, whichever they are."""
+import gc
 import itertools
 
 import pytest
@@ -76,6 +77,7 @@ def test_only_what_they_read_is_kept(wanted):
     read = set().union(*(READ[k] for k, on in zip(NAMES, wanted) if on))
     run(leaves(wanted)[0])
     v, dy = leaves(wanted)
+    gc.collect()
     before = torch.cuda.memory_allocated()
     y = run(v)
     held = torch.cuda.memory_allocated() - before - y.numel() * 2
