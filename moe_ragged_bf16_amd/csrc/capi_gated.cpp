@@ -69,10 +69,11 @@ Kernel kernel_of(Op op, int64_t m_rows, int64_t n, int64_t f, int64_t active, in
     // 8192 x 4096 41 / 35; 80 over 4 of 2 x 1024 x 4096 25 / 30; 200 over 8 of 2 x 512 x 1024 12.3 / 8.7;
     // 15 over 8 of 2 x 416 x 2176 10 / 13; 200 over 8 of 2 x 2048 x 2048 47 / 36; 2 over 8 of 2 x 14336
     // x 4096 84 / 92, 16 310 / 303; 512 over 64 of 2 x 1536 x 2048 152 / 140.  Around the second half's
-    // bound of 8 units to a CU, each row in a group of its own: 16 of 2 x 4096 x 4096, 8 rows (2048
-    // units) 101 / 107, 9 112 / 130, 12 (3072) 146 / 139, 16 189 / 175; 64 of 2 x 1536 x 2048, 21 rows
-    // (2016) 61 / 61, 24 69 / 73, 32 (3072) 88 / 79; 32 of 2 x 2048 x 2048, 16 rows (2048) 66 / 63,
-    // 24 (3072) 92 / 87; 8 of 2 x 14336 x 4096, 3 rows (2688) 128 / 130, 5 200 / 222, 8 (7168) 308 / 310.
+    // bound of 8 units to a CU, each row in a group of its own (units to a CU in brackets): 16 of 2 x
+    // 4096 x 4096, 8 rows [8] 101 / 107, 9 [9] 112 / 130, 12 [12] 146 / 139, 16 [16] 189 / 175; 64 of
+    // 2 x 1536 x 2048, 21 rows [7.9] 61 / 61, 24 [9] 69 / 73, 32 [12] 88 / 79; 32 of 2 x 2048 x 2048, 16
+    // rows [8] 66 / 63, 24 [12] 92 / 87; 8 of 2 x 14336 x 4096, 3 rows [10.5] 128 / 130, 5 [17.5] 200 /
+    // 222, 8 [28] 308 / 310.
     const int64_t units = (active + m_rows / kGatedSmallRows) * up(f, kGatedSmallCols);
     if ((m_rows <= 32 * active && units * 4 <= 5 * cus) || (m_rows <= 16 * active && units <= 8 * cus)) return kSmall;
     // The tile kernel where groups fill a 256-row tile on average and its tiles 5/8 of the CUs, 9/8
