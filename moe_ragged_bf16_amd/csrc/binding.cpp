@@ -6,7 +6,7 @@
 // product 13.5 and 7.1 to 8.5).  One token's route, whose five outputs are allocated
 // one by one, takes 7.4 to 8.1 (1.6 less when they shared a storage, which their
 // owner could then not save or free one by one).  A call of the gated product takes 5 to 7,
-// a block norm 5.3, clipping of 4 tensors 8.2 and of 300 19; the gated feed-forward's forward and
+// a block norm 5.3, clipping of 4 tensors 8.5 and of 300 16; the gated feed-forward's forward and
 // backward pass, eight entries, 117 (238 with a Python call for each).
 //
 // The C entries are those of the library that the package has loaded; setup()
